@@ -12,6 +12,9 @@ Entry points (same names as the C ABI):
   outcome_predict(...)   sd_outcome_predict
   compact(...)           sd_compact
   uniforms(...)          sd_uniforms
+and, from ``logits.py`` (C ABI in ``include/sd_logits.h``), the logit operators
+around the verify step: token_counts, token_counts_add, process_logits,
+top_logits, distill_loss, distill_grad.
 """
 from __future__ import annotations
 
@@ -120,6 +123,7 @@ def lib():
             L.sd_version.restype = ctypes.c_char_p
             L.sd_status_string.argtypes = [ctypes.c_int]
             L.sd_status_string.restype = ctypes.c_char_p
+            logits._bind(L)
             _lib = L
     return _lib
 
@@ -627,3 +631,9 @@ def verify_vsharded_dist(target_s, draft_s, tokens, temperature, seed, *, V, v0,
 
 def version() -> str:
     return lib().sd_version().decode()
+
+
+from . import logits  # noqa: E402  (uses the names above)
+from .logits import (SD_MAX_BIAS, SD_MAX_TOP, SD_STATUS_BAD_PENALTY, TopLogits,  # noqa: E402,F401
+                     distill_grad, distill_loss, process_logits, token_counts, token_counts_add,
+                     top_logits)

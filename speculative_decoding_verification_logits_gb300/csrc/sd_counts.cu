@@ -1,0 +1,151 @@
+// Token counts of each sequence, the state that penalties on logits read:
+// 16 bits per vocabulary entry, the low 15 the number of times the output
+// text holds the token (saturating), the top one set where the prompt does.
+//
+// Integer work.  sd_token_counts gives each CTA one slice of one sequence's
+// vocabulary: a histogram in shared memory, two 16-bit bins per word, fed by
+// the whole history (read from L2 by the slices after the first) and written
+// out once.  Counts cannot carry into the neighbouring bin: at most 32768
+// tokens are added to bins of at most 32767 before every bin is cut back.
+// sd_token_counts_add is one thread per emitted token.
+
+#include "sd_device.cuh"
+#include "sd_logits.h"
+
+namespace sdv {
+
+constexpr int kCntNT = 512;
+constexpr int kCntSlice = 32768;      // bins of one CTA: 64 KB, three CTAs per SM
+constexpr int kCntChunk = 32768;      // tokens added between two cuts
+
+__global__ void __launch_bounds__(kCntNT) sd_token_counts_kernel(
+    int L, int V, int nslice, int slice, const int32_t *history, const int32_t *lengths,
+    const int32_t *prompt_lengths, uint16_t *counts, int32_t *status) {
+  // a programmatic dependent of the stream's previous kernel: nothing is read
+  // before it has finished; the next launch may be scheduled at once
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  extern __shared__ uint32_t bins[];   // bin i of the slice: half i & 1 of word i >> 1
+  const int b = blockIdx.x / nslice, s0 = (blockIdx.x % nslice) * slice;
+  const int n = min(slice, V - s0), nw = (n + 1) >> 1, tid = threadIdx.x;
+  const int32_t *h = history + (int64_t)b * L;
+  const int len = min(max(__ldg(lengths + b), 0), L);
+  const int pl = prompt_lengths ? min(max(__ldg(prompt_lengths + b), 0), len) : 0;
+  for (int i = tid; i < nw; i += kCntNT) bins[i] = 0u;
+  __syncthreads();
+  bool bad = false;
+  for (int c0 = pl; c0 < len; c0 += min(kCntChunk, len - c0)) {
+    const int c1 = c0 + min(kCntChunk, len - c0);
+    for (int i = c0 + tid; i < c1; i += kCntNT) {
+      const int t = __ldg(h + i);
+      bad |= t < 0 || t >= V;
+      const unsigned e = (unsigned)t - (unsigned)s0;
+      if (e < (unsigned)n) atomicAdd(&bins[e >> 1], 1u << (16 * (e & 1u)));
+    }
+    __syncthreads();
+    if (len - pl > 32767) {
+      for (int i = tid; i < nw; i += kCntNT) {
+        const uint32_t w = bins[i];
+        bins[i] = min(w & 0xffffu, 32767u) | (min(w >> 16, 32767u) << 16);
+      }
+      __syncthreads();
+    }
+  }
+  for (int i = tid; i < pl; i += kCntNT) {
+    const int t = __ldg(h + i);
+    bad |= t < 0 || t >= V;
+    const unsigned e = (unsigned)t - (unsigned)s0;
+    if (e < (unsigned)n) atomicOr(&bins[e >> 1], 0x8000u << (16 * (e & 1u)));
+  }
+  __syncthreads();
+  uint16_t *out = counts + (int64_t)b * V + s0;
+  if (((uintptr_t)out & 15) == 0) {
+    for (int i = tid; i < n / 8; i += kCntNT)
+      reinterpret_cast<uint4 *>(out)[i] = reinterpret_cast<const uint4 *>(bins)[i];
+    for (int i = (n & ~7) + tid; i < n; i += kCntNT)
+      out[i] = reinterpret_cast<const uint16_t *>(bins)[i];
+  } else {
+    for (int i = tid; i < n; i += kCntNT) out[i] = reinterpret_cast<const uint16_t *>(bins)[i];
+  }
+  if (bad && s0 == 0 && status) atomicOr(status, (int)SD_STATUS_BAD_TOKEN);
+}
+
+__global__ void __launch_bounds__(256) sd_token_counts_add_kernel(
+    int M, int V, const int32_t *tokens, const int32_t *n, uint16_t *counts, int32_t *status,
+    int64_t total) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int64_t x = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+  if (x >= total) return;
+  const int b = (int)(x / M), i = (int)(x % M);
+  if (i >= __ldg(n + b)) return;
+  const int t = __ldg(tokens + x);
+  if (t < 0 || t >= V) {
+    if (status) atomicOr(status, (int)SD_STATUS_BAD_TOKEN);
+    return;
+  }
+  // a 16-bit exchange: a row of an odd vocabulary shares words with its neighbours
+  unsigned short *p = reinterpret_cast<unsigned short *>(counts + (int64_t)b * V + t);
+  unsigned short old = *p, seen;
+  do {
+    if ((old & 0x7fffu) == 0x7fffu) break;
+    seen = old;
+    old = atomicCAS(p, seen, (unsigned short)(seen + 1));
+  } while (old != seen);
+}
+
+}  // namespace sdv
+
+using namespace sdv;
+
+extern "C" sd_status_t sd_token_counts(int32_t B, int32_t L, int32_t V, const int32_t *history,
+                                       const int32_t *lengths, const int32_t *prompt_lengths,
+                                       uint16_t *counts, int32_t *status, void *stream) {
+  sdv::NvtxRange nvtx_range("sd_token_counts");
+  if (B < 0 || L < 0 || V < 1 || V > SD_MAX_V) return SD_ERR_INVALID_ARG;
+  if (B == 0) return SD_OK;
+  if ((L > 0 && !history) || !lengths || !counts || ((uintptr_t)counts & 1))
+    return SD_ERR_INVALID_ARG;
+  const int nslice = (V + kCntSlice - 1) / kCntSlice;
+  const int slice = ((V + nslice - 1) / nslice + 7) & ~7;
+  if ((int64_t)B * nslice > INT32_MAX) return SD_ERR_INVALID_ARG;
+  static FuncAttrs attrs;
+  attrs.apply((const void *)sd_token_counts_kernel, 2 * kCntSlice, false, "the count kernel");
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(B * nslice), 1, 1);
+  cfg.blockDim = dim3(kCntNT, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)2 * slice;
+  cfg.stream = (cudaStream_t)stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, sd_token_counts_kernel, (int)L, (int)V, nslice,
+                                           slice, history, lengths, prompt_lengths, counts,
+                                           status);
+  return e == cudaSuccess ? SD_OK : SD_ERR_CUDA;
+}
+
+extern "C" sd_status_t sd_token_counts_add(int32_t B, int32_t M, int32_t V, const int32_t *tokens,
+                                           const int32_t *n, uint16_t *counts, int32_t *status,
+                                           void *stream) {
+  sdv::NvtxRange nvtx_range("sd_token_counts_add");
+  if (B < 0 || M < 0 || V < 1 || V > SD_MAX_V) return SD_ERR_INVALID_ARG;
+  if (B == 0 || M == 0) return SD_OK;
+  if (!tokens || !n || !counts || ((uintptr_t)counts & 1)) return SD_ERR_INVALID_ARG;
+  const int64_t total = (int64_t)B * M;
+  if ((total + 255) / 256 > INT32_MAX) return SD_ERR_INVALID_ARG;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((total + 255) / 256), 1, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = (cudaStream_t)stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, sd_token_counts_add_kernel, (int)M, (int)V,
+                                           tokens, n, counts, status, total);
+  return e == cudaSuccess ? SD_OK : SD_ERR_CUDA;
+}

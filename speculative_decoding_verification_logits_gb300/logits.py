@@ -1,0 +1,309 @@
+"""Binding of the logit operators around the verify step (C ABI in
+``include/sd_logits.h``): token counts, penalties with biases and grammar
+masks, a teacher's top logits, and the distillation loss with its gradient.
+
+Like the rest of the package this module only checks and marshals arguments.
+
+  token_counts(...), token_counts_add(...)   sd_token_counts, sd_token_counts_add
+  process_logits(...)                        sd_process_logits
+  top_logits(...)                            sd_top_logits
+  distill_loss(...), distill_grad(...)       sd_distill
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple
+
+import torch
+
+from . import _P, SD_BF16, SD_F32, _check, _need, _on_stream, lib
+
+SD_STATUS_BAD_PENALTY = 0x8
+SD_MAX_TOP, SD_MAX_BIAS = 128, 1024
+
+_DTYPES = {torch.float32: SD_F32, torch.bfloat16: SD_BF16}
+
+
+class ProcessArgs(ctypes.Structure):
+    """Mirror of ``sd_process_args`` in include/sd_logits.h."""
+    _fields_ = [
+        ("B", ctypes.c_int32), ("R", ctypes.c_int32), ("V", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("logits", _P), ("logits_sb", ctypes.c_int64),
+        ("logits_sr", ctypes.c_int64), ("out", _P), ("out_sb", ctypes.c_int64),
+        ("out_sr", ctypes.c_int64), ("counts", _P), ("prev", _P), ("P", ctypes.c_int32),
+        ("base", ctypes.c_int32), ("repetition", _P), ("presence", _P), ("frequency", _P),
+        ("bias_ids", _P), ("bias_vals", _P), ("n_bias", ctypes.c_int32), ("mask", _P),
+        ("mask_sb", ctypes.c_int64), ("mask_sr", ctypes.c_int64), ("status", _P),
+    ]
+
+
+class DistillArgs(ctypes.Structure):
+    """Mirror of ``sd_distill_args`` in include/sd_logits.h."""
+    _fields_ = [
+        ("N", ctypes.c_int32), ("V", ctypes.c_int32), ("k", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("student", _P), ("student_s", ctypes.c_int64), ("ids", _P),
+        ("vals", _P), ("rest", _P), ("weight", _P), ("T", ctypes.c_float), ("loss", _P),
+        ("grad", _P), ("grad_s", ctypes.c_int64), ("status", _P),
+    ]
+
+
+class TopLogits(NamedTuple):
+    vals: torch.Tensor   # [...][k] float32, larger first
+    ids: torch.Tensor    # [...][k] int32, -1 where nothing is left
+    rest: torch.Tensor   # [...] float32: log sum exp(x / T) of the others
+
+
+def _bind(L):
+    """Argument types of the entry points, and the structs' layouts."""
+    i32, i64, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+    L.sd_token_counts.argtypes = [i32, i32, i32, _P, _P, _P, _P, _P, _P]
+    L.sd_token_counts_add.argtypes = [i32, i32, i32, _P, _P, _P, _P, _P]
+    L.sd_process_logits.argtypes = [ctypes.POINTER(ProcessArgs), _P]
+    L.sd_top_logits.argtypes = [i32, i32, i32, _P, i64, i32, f32, _P, _P, _P, _P]
+    L.sd_distill.argtypes = [ctypes.POINTER(DistillArgs), _P]
+    for fn in (L.sd_token_counts, L.sd_token_counts_add, L.sd_process_logits, L.sd_top_logits,
+               L.sd_distill):
+        fn.restype = ctypes.c_int
+    for fn, mirror in ((L.sd_process_args_size, ProcessArgs),
+                       (L.sd_distill_args_size, DistillArgs)):
+        fn.argtypes, fn.restype = [], ctypes.c_size_t
+        if fn() != ctypes.sizeof(mirror):
+            raise RuntimeError(f"{mirror.__name__} layout differs between library and binding")
+
+
+def _stream_of(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _rows(t, name, dims):
+    """Checks a tensor of logit rows: CUDA, float32 or bfloat16, each row contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    if t.dim() not in dims:
+        raise ValueError(f"{name} has {t.dim()} dimensions, expected {' or '.join(map(str, dims))}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return dt
+
+
+def _out_like(x, out, name):
+    """Checks an output given by the caller: shape and type of x, rows contiguous,
+    either x itself or memory of its own."""
+    _rows(out, name, (x.dim(),))
+    if out.dtype != x.dtype or out.shape != x.shape or out.device != x.device:
+        raise ValueError(f"{name} must have the shape, type and device of the input")
+    if out.data_ptr() == x.data_ptr() and out.stride() == x.stride():
+        return
+    ends = lambda t: t.data_ptr() + t.element_size() * (
+        1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))
+    if x.numel() and out.data_ptr() < ends(x) and x.data_ptr() < ends(out):
+        raise ValueError(f"{name} overlaps the input without being the same tensor")
+
+
+def _opt(t, name, dtype, shape, device):
+    return None if t is None else _need(t, name, dtype, shape, device).data_ptr()
+
+
+@_on_stream
+def token_counts(history, lengths, V: int, *, prompt_lengths=None, out=None, status=None,
+                 stream=None) -> torch.Tensor:
+    """counts [B][V] int16 of history [B][L] (int32), lengths [B] and
+    prompt_lengths [B] (int32, none: no prompt): the low 15 bits are how often
+    the output text holds the token (at most 32767), the sign bit is set where
+    the prompt holds it."""
+    _need(history, "history", torch.int32)
+    if history.dim() != 2:
+        raise ValueError("history must be [B][L]")
+    B, L = history.shape
+    dev = history.device
+    _need(lengths, "lengths", torch.int32, (B,), dev)
+    if out is None:
+        out = torch.empty((B, V), dtype=torch.int16, device=dev)
+    else:
+        _need(out, "out", torch.int16, (B, V), dev)
+    _check(lib().sd_token_counts(B, L, V, history.data_ptr(), lengths.data_ptr(),
+                                 _opt(prompt_lengths, "prompt_lengths", torch.int32, (B,), dev),
+                                 out.data_ptr(),
+                                 _opt(status, "status", torch.int32, (1,), dev),
+                                 _stream_of(dev)), "sd_token_counts")
+    return out
+
+
+@_on_stream
+def token_counts_add(counts, tokens, n, *, status=None, stream=None) -> torch.Tensor:
+    """Adds tokens[b][:n[b]] of tokens [B][M] to counts [B][V] in place: after a
+    round, out_tokens and tau of its VerifyResult."""
+    _need(counts, "counts", torch.int16)
+    if counts.dim() != 2:
+        raise ValueError("counts must be [B][V]")
+    B, V = counts.shape
+    dev = counts.device
+    _need(tokens, "tokens", torch.int32, None, dev)
+    if tokens.dim() != 2 or tokens.shape[0] != B:
+        raise ValueError("tokens must be [B][M]")
+    _need(n, "n", torch.int32, (B,), dev)
+    _check(lib().sd_token_counts_add(B, tokens.shape[1], V, tokens.data_ptr(), n.data_ptr(),
+                                     counts.data_ptr(),
+                                     _opt(status, "status", torch.int32, (1,), dev),
+                                     _stream_of(dev)), "sd_token_counts_add")
+    return counts
+
+
+@_on_stream
+def process_logits(logits, *, counts=None, prev=None, base: int = 0, repetition=None,
+                   presence=None, frequency=None, bias_ids=None, bias_vals=None, mask=None,
+                   out=None, status=None, stream=None) -> torch.Tensor:
+    """Logits [B][R][V] (or [B][V]: one row each) under penalties, biases and a
+    grammar's mask, as the verify step should see them.
+
+    counts [B][V] int16 (token_counts); prev [B][P] int32: this round's drafts,
+    of which row r counts prev[b][:base + r] (target rows of a round: the
+    drafted tokens and base 0); repetition, presence, frequency [B] float32;
+    bias_ids [B][n] int32 (-1: empty) with bias_vals [B][n] float32; mask
+    [B][R][ceil(V / 32)] or [B][ceil(V / 32)] int32, a set bit allows the
+    token.  All are optional.  out may be the logits tensor itself."""
+    dt = _rows(logits, "logits", (2, 3))
+    dev = logits.device
+    three = logits.dim() == 3
+    B, V = logits.shape[0], logits.shape[-1]
+    R = logits.shape[1] if three else 1
+    if out is None:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+    else:
+        _out_like(logits, out, "out")
+    P = 0
+    if prev is not None:
+        _need(prev, "prev", torch.int32, None, dev)
+        if prev.dim() != 2 or prev.shape[0] != B:
+            raise ValueError("prev must be [B][P]")
+        P = prev.shape[1]
+    if (bias_ids is None) != (bias_vals is None):
+        raise ValueError("bias_ids and bias_vals go together")
+    n_bias = 0
+    if bias_ids is not None:
+        _need(bias_ids, "bias_ids", torch.int32, None, dev)
+        if bias_ids.dim() != 2 or bias_ids.shape[0] != B:
+            raise ValueError("bias_ids must be [B][n]")
+        n_bias = bias_ids.shape[1]
+        _need(bias_vals, "bias_vals", torch.float32, (B, n_bias), dev)
+    mb = mr = 0
+    if mask is not None:
+        if not mask.is_cuda or mask.device != dev or mask.dtype != torch.int32:
+            raise ValueError(f"mask must be an int32 tensor on {dev}")
+        W = (V + 31) // 32
+        shape = tuple(mask.shape)
+        if shape == (B, R, W):
+            mb, mr = mask.stride(0), mask.stride(1)
+        elif shape == (B, W):
+            mb = mask.stride(0)
+        else:
+            raise ValueError(f"mask has shape {shape}, expected {(B, R, W)} or {(B, W)}")
+        if W > 1 and mask.stride(-1) != 1:
+            raise ValueError("mask must have contiguous rows")
+    a = ProcessArgs(B, R, V, dt, logits.data_ptr(), logits.stride(0),
+                    logits.stride(1) if three else 0, out.data_ptr(), out.stride(0),
+                    out.stride(1) if three else 0,
+                    _opt(counts, "counts", torch.int16, (B, V), dev),
+                    None if prev is None else prev.data_ptr(), P, int(base),
+                    _opt(repetition, "repetition", torch.float32, (B,), dev),
+                    _opt(presence, "presence", torch.float32, (B,), dev),
+                    _opt(frequency, "frequency", torch.float32, (B,), dev),
+                    bias_ids.data_ptr() if n_bias else None,
+                    bias_vals.data_ptr() if n_bias else None, n_bias,
+                    None if mask is None else mask.data_ptr(), mb, mr,
+                    _opt(status, "status", torch.int32, (1,), dev))
+    _check(lib().sd_process_logits(a, _stream_of(dev)), "sd_process_logits")
+    return out
+
+
+def _row_stride(t, name):
+    """Rows of a [N][V] or [A][B][V] tensor at one stride: (N, stride)."""
+    if t.dim() == 2:
+        return t.shape[0], t.stride(0)
+    A, B, _ = t.shape
+    if A > 1 and B > 1 and t.stride(0) != B * t.stride(1):
+        raise ValueError(f"{name} must have its rows at one stride")
+    return A * B, t.stride(1) if B > 1 else t.stride(0)
+
+
+@_on_stream
+def top_logits(logits, k: int, *, temperature: float = 1.0, out: TopLogits | None = None,
+               stream=None) -> TopLogits:
+    """The k largest logits of each row of [N][V] or [A][B][V] (ties to the
+    lowest index, -inf never chosen) and the log-sum-exp at `temperature` of
+    the others: what distill_loss and distill_grad take of a teacher."""
+    dt = _rows(logits, "logits", (2, 3))
+    dev = logits.device
+    N, stride = _row_stride(logits, "logits")
+    lead = tuple(logits.shape[:-1])
+    if out is None:
+        out = TopLogits(torch.empty((*lead, k), dtype=torch.float32, device=dev),
+                        torch.empty((*lead, k), dtype=torch.int32, device=dev),
+                        torch.empty(lead, dtype=torch.float32, device=dev))
+    else:
+        _need(out.vals, "out.vals", torch.float32, (*lead, k), dev)
+        _need(out.ids, "out.ids", torch.int32, (*lead, k), dev)
+        _need(out.rest, "out.rest", torch.float32, lead, dev)
+    _check(lib().sd_top_logits(N, logits.shape[-1], dt, logits.data_ptr(), stride, int(k),
+                               float(temperature), out.vals.data_ptr(), out.ids.data_ptr(),
+                               out.rest.data_ptr(), _stream_of(dev)), "sd_top_logits")
+    return out
+
+
+def _distill(student, ids, vals, rest, temperature, weight, loss, grad, status):
+    dt = _rows(student, "student", (2, 3))
+    dev = student.device
+    N, stride = _row_stride(student, "student")
+    lead = tuple(student.shape[:-1])
+    if ids.dim() != len(lead) + 1:
+        raise ValueError("ids must have the student's leading dimensions and k")
+    k = ids.shape[-1]
+    _need(ids, "ids", torch.int32, (*lead, k), dev)
+    _need(vals, "vals", torch.float32, (*lead, k), dev)
+    gs = 0
+    if grad is not None:
+        if grad is not student:
+            _out_like(student, grad, "grad")
+        gs = _row_stride(grad, "grad")[1]
+    a = DistillArgs(N, student.shape[-1], k, dt, student.data_ptr(), stride, ids.data_ptr(),
+                    vals.data_ptr(), _opt(rest, "rest", torch.float32, lead, dev),
+                    _opt(weight, "weight", torch.float32, lead, dev), float(temperature),
+                    None if loss is None else loss.data_ptr(),
+                    None if grad is None else grad.data_ptr(), gs,
+                    _opt(status, "status", torch.int32, (1,), dev))
+    _check(lib().sd_distill(a, _stream_of(dev)), "sd_distill")
+
+
+@_on_stream
+def distill_loss(student, ids, vals, rest=None, *, temperature: float = 1.0, weight=None,
+                 out=None, status=None, stream=None) -> torch.Tensor:
+    """Distillation loss of each row of the student's logits ([N][V] or
+    [A][B][V]) against a teacher's top logits (ids, vals, rest of top_logits at
+    the same temperature; without rest the named tokens hold all of the
+    teacher's mass): weight times the divergence of the k named tokens and one
+    bucket of all others.  Evaluation: reads the logits once."""
+    lead = tuple(student.shape[:-1])
+    if out is None:
+        out = torch.empty(lead, dtype=torch.float32, device=student.device)
+    else:
+        _need(out, "out", torch.float32, lead, student.device)
+    _distill(student, ids, vals, rest, temperature, weight, out, None, status)
+    return out
+
+
+@_on_stream
+def distill_grad(student, ids, vals, rest=None, *, temperature: float = 1.0, weight=None,
+                 grad=None, status=None, stream=None):
+    """(loss, grad): the loss of distill_loss and, in the same call, its gradient
+    with respect to the student's logits, times `weight` (what reaches each
+    row's loss from above: 1 / N for a mean).  grad may be the student tensor
+    itself.  To train: student.backward(grad)."""
+    student = student.detach()
+    loss = torch.empty(student.shape[:-1], dtype=torch.float32, device=student.device)
+    if grad is None:
+        grad = torch.empty(student.shape, dtype=student.dtype, device=student.device)
+    _distill(student, ids, vals, rest, temperature, weight, loss, grad, status)
+    return loss, grad
