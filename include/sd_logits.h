@@ -63,7 +63,7 @@ sd_status_t sd_token_counts_add(int32_t B, int32_t M, int32_t V, const int32_t *
  *   seen = c > 0 or v's prompt bit is set
  *   x1   = seen ? (x > 0 ? x / repetition[b] : x * repetition[b]) : x
  *   x2   = x1 - frequency[b] c - presence[b] [c > 0]
- *   x3   = x2 + the bias_vals[b][i] with bias_ids[b][i] = v, in list order
+ *   x3   = x2 + the sum of the bias_vals[b][i] with bias_ids[b][i] = v (in list order)
  *   y    = v allowed by the mask ? x3 : -inf
  * A logit of -inf stays -inf.  All in fp32, rounded once to the logits' type.
  * prev are the tokens drafted in this round: row r of the target's rows

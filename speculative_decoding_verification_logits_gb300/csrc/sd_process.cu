@@ -8,11 +8,16 @@
 // or -inf where the mask forbids the token.  fp32, rounded once.
 //
 // The work is moving memory: a logit is read, written and in most places left
-// as it was.  A CTA takes the same NT vectors' worth of vocabulary through
-// all R rows of one sequence, so that the counts are read once for all of
-// them.  It first makes a bit per token of its window that a count, a draft
-// or a bias touches; a vector without a bit is passed on as raw words.
-// Logits that the mask forbids are not read.
+// as it was.  A CTA takes NT vectors' worth of vocabulary (a window) through
+// all R rows of one sequence, in two parts:
+//  A. rows are copied as raw words with -inf put where the mask forbids the
+//     token; logits that are forbidden all through a vector are not read;
+//  B. the window's touched tokens (a count, a draft or a bias) are listed
+//     once, from a bit per token, and each (row, listed token) is one thread's
+//     work: read the logit again (from L2), compute, write over it.
+// Computing touched logits where A meets them is what this replaces: nearly
+// every warp then holds a touched one and runs the whole computation for a
+// lane or two (64 x 9 x 151936 bf16, masked: 471 us; large batch 495 us).
 
 #include "sd_rows.cuh"
 
@@ -38,24 +43,44 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t *w, int e0, int W) 
   return r & ((1u << VE) - 1u);
 }
 
+// The words of vector v with -inf where its bit in `ok` is clear.
+template <typename E>
+__device__ __forceinline__ uint4 mask_vec(uint4 v, uint32_t ok) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t keep;
+    if (Elt<E>::kPerVec == 8)
+      keep = ((ok >> (2 * i)) & 1u) * 0x0000ffffu + ((ok >> (2 * i + 1)) & 1u) * 0xffff0000u;
+    else
+      keep = 0u - ((ok >> i) & 1u);
+    w[i] = (w[i] & keep) | (Elt<E>::kNegInfWord & ~keep);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // VEC: rows move as 16-byte vectors (the output's rows lie on the same place
 // of the 16-byte grid as the input's); otherwise element by element.
 template <typename E, bool VEC>
 __global__ void __launch_bounds__(kProcNT) sd_process_kernel(const ProcParams P) {
   constexpr int VE = VEC ? Elt<E>::kPerVec : 1, NT = kProcNT, NW = NT / 32;
   constexpr int SZ = Elt<E>::kSize;
+  constexpr uint32_t kAll = (1u << VE) - 1u;
   constexpr int kWin = NT * VE + VE;              // tokens of the window
+  constexpr int kWords = (kWin + 31) / 32;
   constexpr int kBiasPer = SD_MAX_BIAS / NT;      // list entries per thread
   const sd_process_args &a = P.a;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ uint16_t cnt[kWin];
-  __shared__ uint32_t touch[(kWin + 31) / 32 + 1];
+  __shared__ uint16_t hot[kWin];                       // touched tokens of the window
+  __shared__ float bias[kWin];                         // sum of each token's biases
+  __shared__ uint32_t touch[kWords];
   __shared__ int prev_i[SD_MAX_K], prev_v[SD_MAX_K];   // drafts inside the window, in order
   __shared__ int bias_v[SD_MAX_BIAS];                  // biases inside the window, in order
   __shared__ float bias_x[SD_MAX_BIAS];
   __shared__ int bias_n[kBiasPer][NW];
-  __shared__ int n_prev;
+  __shared__ int n_prev, n_hot;
   const int b = blockIdx.x / P.nslice, q0 = (blockIdx.x % P.nslice) * NT;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int V = a.V, R = a.R, w0 = q0 * VE - VE;   // first token of the window
@@ -64,42 +89,134 @@ __global__ void __launch_bounds__(kProcNT) sd_process_kernel(const ProcParams P)
   const float freq = a.frequency ? __ldg(a.frequency + b) : 0.f;
   const bool bad = !(rep > 0.f && rep < INFINITY) || !(fabsf(pres) < INFINITY) ||
                    !(fabsf(freq) < INFINITY);
-  // counts of the window, and the tokens they touch
-  if (tid == 0) touch[(kWin + 31) / 32] = 0u;
+  const int n_draft = a.prev ? a.base + R - 1 : 0;
+  const bool touches = a.counts || n_draft > 0 || a.n_bias > 0;   // part B has work at all
+
+  // the window's counts, this round's drafts and the biases are asked for
+  // first and arrive during part A
+  uint32_t c[VE + 1];
+  if (a.counts) {
 #pragma unroll
-  for (int j = tid; j < (kWin + 31) / 32 * 32; j += NT) {
-    const int v = w0 + j;
-    uint32_t c = 0u;
-    if (a.counts && j < kWin && v >= 0 && v < V) c = __ldg(a.counts + (int64_t)b * V + v);
-    if (j < kWin) cnt[j] = (uint16_t)c;
-    const unsigned m = __ballot_sync(0xffffffffu, c != 0u);
-    if (lane == 0) touch[j >> 5] = m;
-  }
-  // this round's drafts and the biases that fall into the window, in list order
-  bool bad_id = false;
-  if (warp == 0) {
-    int v = -1;
-    if (a.prev && lane < a.base + R - 1) {
-      v = __ldg(a.prev + (int64_t)b * a.P + lane);
-      bad_id = v < 0 || v >= V;
+    for (int i = 0; i <= VE; ++i) {
+      const int j = i * NT + tid, v = w0 + j;
+      c[i] = j < kWin && v >= 0 && v < V ? __ldg(a.counts + (int64_t)b * V + v) : 0u;
     }
-    const bool in = !bad_id && v >= 0 && v >= w0 && v < w0 + kWin;
-    const unsigned m = ballot(in);
-    if (in) {
-      const int at = __popc(m & ((1u << lane) - 1u));
-      prev_i[at] = lane;
-      prev_v[at] = v;
-    }
-    if (lane == 0) n_prev = __popc(m);
   }
+  int draft = -1;
+  if (warp == 0 && lane < n_draft) draft = __ldg(a.prev + (int64_t)b * a.P + lane);
   int bid[kBiasPer];
-  unsigned bhit[kBiasPer];
   if (a.n_bias > 0) {
 #pragma unroll
     for (int j = 0; j < kBiasPer; ++j) {
       const int i = j * NT + tid;
       bid[j] = i < a.n_bias ? __ldg(a.bias_ids + (int64_t)b * a.n_bias + i) : -1;
     }
+  }
+
+  // A. copy and mask
+  const int W = (V + 31) >> 5, q = q0 + tid;
+  const uint8_t *xb = (const uint8_t *)a.logits + b * a.logits_sb * SZ;
+  uint8_t *yb = (uint8_t *)a.out + b * a.out_sb * SZ;
+  const uint32_t *mb = (const uint32_t *)a.mask + b * a.mask_sb;
+  // row r's place: its first element in this thread's vector and which of
+  // them lie in the row
+  auto place = [&](int r, int &e0, uint32_t &valid) {
+    e0 = q * VE - (VEC ? (int)((uintptr_t)(xb + r * a.logits_sr * SZ) & 15) / SZ : 0);
+    valid = kAll;
+    if (e0 < 0) valid = (kAll << -e0) & kAll;
+    if (e0 >= V) valid = 0u;
+    else if (e0 + VE > V) valid &= (1u << (V - e0)) - 1u;
+  };
+  auto allowed = [&](int r) {
+    int e0;
+    uint32_t valid;
+    if (r >= R) return 0u;
+    place(r, e0, valid);
+    if (valid == 0u || !a.mask) return valid;
+    return valid & mask_bits<VE>(mb + r * a.mask_sr, e0, W);
+  };
+  uint32_t next[kProcU];
+#pragma unroll
+  for (int u = 0; u < kProcU; ++u) next[u] = allowed(u);
+  for (int r0 = 0; r0 < R; r0 += kProcU) {
+    uint4 xv[kProcU];
+    uint32_t ok[kProcU];
+#pragma unroll
+    for (int u = 0; u < kProcU; ++u) {
+      ok[u] = next[u];
+      int e0;
+      uint32_t valid;
+      place(r0 + u, e0, valid);
+      if (!ok[u] || bad || (P.inplace && ok[u] == valid)) continue;
+      const uint8_t *x = xb + (r0 + u) * a.logits_sr * SZ;
+      if (VEC && valid == kAll) {
+        xv[u] = __ldcg(reinterpret_cast<const uint4 *>(x + (int64_t)e0 * SZ));
+      } else {
+        float f[Elt<E>::kPerVec] = {};
+#pragma unroll
+        for (int i = 0; i < VE; ++i)
+          if ((ok[u] >> i) & 1u) f[i] = Row<E>::load(x, e0 + i);
+        Row<E>::pack(f, xv[u]);
+      }
+    }
+    // the mask of the next rows, so that their loads need not wait for it
+#pragma unroll
+    for (int u = 0; u < kProcU; ++u) next[u] = allowed(r0 + kProcU + u);
+#pragma unroll
+    for (int u = 0; u < kProcU; ++u) {
+      int e0;
+      uint32_t valid;
+      place(r0 + u, e0, valid);
+      if (r0 + u >= R || valid == 0u || (P.inplace && ok[u] == valid && !bad)) continue;
+      uint4 v = make_uint4(Elt<E>::kNegInfWord, Elt<E>::kNegInfWord, Elt<E>::kNegInfWord,
+                           Elt<E>::kNegInfWord);
+      if (ok[u]) v = ok[u] == kAll ? xv[u] : mask_vec<E>(xv[u], ok[u]);
+      if (bad) {
+        const uint32_t nan = SZ == 2 ? 0x7fc07fc0u : 0x7fc00000u;
+        v = make_uint4(nan, nan, nan, nan);
+      }
+      uint8_t *y = yb + (r0 + u) * a.out_sr * SZ;
+      if (VEC && valid == kAll) {
+        *reinterpret_cast<uint4 *>(y + (int64_t)e0 * SZ) = v;
+      } else {
+        float f[Elt<E>::kPerVec];
+        Elt<E>::unpack(v, f);
+#pragma unroll
+        for (int i = 0; i < VE; ++i)
+          if ((valid >> i) & 1u) Row<E>::store(y, e0 + i, f[i]);
+      }
+    }
+  }
+  if (bad && tid == 0 && q0 == 0 && a.status) atomicOr(a.status, (int)SD_STATUS_BAD_PENALTY);
+  if (!touches) return;
+
+  // B. which tokens of the window are touched
+  bool bad_id = false;
+#pragma unroll
+  for (int i = 0; i <= VE; ++i) {
+    const int j = i * NT + tid;
+    const uint32_t n = a.counts ? c[i] : 0u;
+    if (j < kWin) cnt[j] = (uint16_t)n;
+    const unsigned m = ballot(n != 0u);
+    if (lane == 0 && j < kWin) touch[j >> 5] = m;
+  }
+  if (warp == 0) {
+    bad_id = lane < n_draft && (draft < 0 || draft >= V);
+    const bool in = lane < n_draft && !bad_id && draft >= w0 && draft < w0 + kWin;
+    const unsigned m = ballot(in);
+    if (in) {
+      const int at = __popc(m & ((1u << lane) - 1u));
+      prev_i[at] = lane;
+      prev_v[at] = draft;
+    }
+    if (lane == 0) {
+      n_prev = __popc(m);
+      n_hot = 0;
+    }
+  }
+  unsigned bhit[kBiasPer];
+  if (a.n_bias > 0) {
+    for (int j = tid; j < kWin; j += NT) bias[j] = 0.f;
 #pragma unroll
     for (int j = 0; j < kBiasPer; ++j) {
       bad_id |= bid[j] < -1 || bid[j] >= V;
@@ -109,117 +226,79 @@ __global__ void __launch_bounds__(kProcNT) sd_process_kernel(const ProcParams P)
       if (lane == 0) bias_n[j][warp] = __popc(bhit[j]);
     }
   }
-  __syncthreads();
-  int n_bias = 0;
+  if (bad_id && q0 == 0 && a.status) atomicOr(a.status, (int)SD_STATUS_BAD_TOKEN);
+  if (bad) return;   // the same for every CTA of the sequence: its rows are NaN
+  __syncthreads();   // also: part A's stores come before part B's to the same places
+  if (tid < n_prev) atomicOr(&touch[(prev_v[tid] - w0) >> 5], 1u << ((prev_v[tid] - w0) & 31));
   if (a.n_bias > 0) {
-    int at[kBiasPer];
+    int n = 0, at[kBiasPer];
 #pragma unroll
     for (int j = 0; j < kBiasPer; ++j)
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
-        if (w == warp) at[j] = n_bias;
-        n_bias += bias_n[j][w];
+        if (w == warp) at[j] = n;
+        n += bias_n[j][w];
       }
 #pragma unroll
     for (int j = 0; j < kBiasPer; ++j)
       if (bid[j] >= 0) {
         const int k = at[j] + __popc(bhit[j] & ((1u << lane) - 1u));
-        bias_v[k] = bid[j];
+        bias_v[k] = bid[j] - w0;
         bias_x[k] = __ldg(a.bias_vals + (int64_t)b * a.n_bias + j * NT + tid);
         atomicOr(&touch[(bid[j] - w0) >> 5], 1u << ((bid[j] - w0) & 31));
       }
+    __syncthreads();
+    // a token's biases are summed in list order by the thread of its first one
+    for (int k = tid; k < n; k += NT) {
+      const int v = bias_v[k];
+      int first = k;
+      for (int o = 0; o < k && first == k; ++o)
+        if (bias_v[o] == v) first = o;
+      if (first != k) continue;
+      float s = bias_x[k];
+      for (int o = k + 1; o < n; ++o)
+        if (bias_v[o] == v) s += bias_x[o];
+      bias[v] = s;
+    }
   }
-  if (tid < n_prev) atomicOr(&touch[(prev_v[tid] - w0) >> 5], 1u << ((prev_v[tid] - w0) & 31));
   __syncthreads();
-  if (a.status && q0 == 0) {
-    if (bad && tid == 0) atomicOr(a.status, (int)SD_STATUS_BAD_PENALTY);
-    if (bad_id) atomicOr(a.status, (int)SD_STATUS_BAD_TOKEN);
+  for (int w = tid; w < (kWords + 31) / 32 * 32; w += NT) {
+    const uint32_t m = w < kWords ? touch[w] : 0u;
+    const int n = __popc(m);
+    int scan = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, scan, o);
+      scan += lane >= o ? y : 0;
+    }
+    int at = 0;
+    if (lane == 31) at = atomicAdd(&n_hot, scan);
+    at = __shfl_sync(0xffffffffu, at, 31) + scan - n;
+    for (uint32_t left = m; left; left &= left - 1u) hot[at++] = (uint16_t)(w * 32 + __ffs(left) - 1);
   }
-
-  const int W = (V + 31) >> 5, q = q0 + tid;
-  const uint8_t *xb = (const uint8_t *)a.logits + b * a.logits_sb * SZ;
-  uint8_t *yb = (uint8_t *)a.out + b * a.out_sb * SZ;
-  for (int r0 = 0; r0 < R; r0 += kProcU) {
-    uint4 xv[kProcU];
-    int e0[kProcU];
-    uint32_t ok[kProcU], valid[kProcU];
-#pragma unroll
-    for (int u = 0; u < kProcU; ++u) {
-      const int r = r0 + u;
-      valid[u] = 0u;
-      if (r >= R) continue;
-      const uint8_t *x = xb + r * a.logits_sr * SZ;
-      e0[u] = q * VE - (VEC ? (int)((uintptr_t)x & 15) / SZ : 0);
-      uint32_t in = (1u << VE) - 1u;
-      if (e0[u] < 0) in &= in << -e0[u];
-      if (e0[u] >= V) in = 0u;
-      else if (e0[u] + VE > V) in &= (1u << (V - e0[u])) - 1u;
-      valid[u] = in;
-      ok[u] = in;
-      if (a.mask && in)
-        ok[u] &= mask_bits<VE>((const uint32_t *)a.mask + b * a.mask_sb + r * a.mask_sr, e0[u], W);
-    }
-#pragma unroll
-    for (int u = 0; u < kProcU; ++u) {
-      if (!valid[u] || !ok[u]) continue;
-      const uint8_t *x = xb + (r0 + u) * a.logits_sr * SZ;
-      if (VEC && valid[u] == (1u << VE) - 1u) {
-        xv[u] = __ldcg(reinterpret_cast<const uint4 *>(x + (int64_t)e0[u] * SZ));
-      } else {
-        float f[Elt<E>::kPerVec] = {};
-#pragma unroll
-        for (int i = 0; i < VE; ++i)
-          if ((valid[u] >> i) & 1u) f[i] = Row<E>::load(x, e0[u] + i);
-        Row<E>::pack(f, xv[u]);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kProcU; ++u) {
-      if (!valid[u]) continue;
-      const int r = r0 + u;
-      const int j0 = e0[u] - w0;
-      uint32_t hot = touch[j0 >> 5] >> (j0 & 31);
-      if ((j0 & 31) + VE > 32) hot |= touch[(j0 >> 5) + 1] << (32 - (j0 & 31));
-      hot &= ok[u];
-      if (P.inplace && ok[u] == valid[u] && !hot && !bad) continue;
-      float f[Elt<E>::kPerVec];
-      if (ok[u]) {
-        Elt<E>::unpack(xv[u], f);
-      } else {
-#pragma unroll
-        for (int i = 0; i < Elt<E>::kPerVec; ++i) f[i] = neg_inf();
-      }
-      if (hot) {
-#pragma unroll
-        for (int i = 0; i < VE; ++i) {
-          if (!((hot >> i) & 1u) || f[i] == neg_inf()) continue;
-          const int v = e0[u] + i;
-          const uint32_t word = cnt[j0 + i];
-          int c = (int)(word & 0x7fffu);
-          for (int k = 0; k < n_prev; ++k) c += prev_v[k] == v && prev_i[k] < a.base + r;
-          float x = f[i];
-          if (c > 0 || (word & 0x8000u)) x = x > 0.f ? x / rep : x * rep;
-          if (c > 0) x = x - freq * (float)c - pres;
-          for (int k = 0; k < n_bias; ++k)
-            if (bias_v[k] == v) x += bias_x[k];
-          f[i] = x;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        if (!((ok[u] >> i) & 1u)) f[i] = neg_inf();
-        if (bad) f[i] = __int_as_float(0x7fc00000);
-      }
-      uint8_t *y = yb + r * a.out_sr * SZ;
-      if (VEC && valid[u] == (1u << VE) - 1u) {
-        uint4 v;
-        Row<E>::pack(f, v);
-        *reinterpret_cast<uint4 *>(y + (int64_t)e0[u] * SZ) = v;
-      } else {
-#pragma unroll
-        for (int i = 0; i < VE; ++i)
-          if ((valid[u] >> i) & 1u) Row<E>::store(y, e0[u] + i, f[i]);
-      }
+  __syncthreads();
+  // tpr threads side by side take a row's listed tokens
+  int tpr = 1;
+  while (tpr < NT && tpr < n_hot) tpr *= 2;
+  for (int r = tid / tpr; r < R; r += NT / tpr) {
+    const uint8_t *x = xb + r * a.logits_sr * SZ;
+    uint8_t *y = yb + r * a.out_sr * SZ;
+    const uint32_t *m = mb + r * a.mask_sr;
+    // a vector slice of a row off the grid covers VE tokens of its neighbour's window
+    const int lo = q0 * VE - (VEC ? (int)((uintptr_t)x & 15) / SZ : 0);
+    for (int h = tid & (tpr - 1); h < n_hot; h += tpr) {
+      const int j = hot[h], v = w0 + j;
+      if (v < lo || v >= lo + NT * VE) continue;
+      if (a.mask && !((__ldg(m + (v >> 5)) >> (v & 31)) & 1u)) continue;
+      float f = Row<E>::load(x, v);
+      if (f == neg_inf()) continue;
+      const uint32_t word = cnt[j];
+      int n = (int)(word & 0x7fffu);
+      for (int k = 0; k < n_prev; ++k) n += prev_v[k] == v && prev_i[k] < a.base + r;
+      if (n > 0 || (word & 0x8000u)) f = f > 0.f ? f / rep : f * rep;
+      if (n > 0) f = f - freq * (float)n - pres;
+      if (a.n_bias > 0) f += bias[j];
+      Row<E>::store(y, v, f);
     }
   }
 }
