@@ -9,8 +9,7 @@
 // tokens are added to bins of at most 32767 before every bin is cut back.
 // sd_token_counts_add is one thread per emitted token.
 
-#include "sd_device.cuh"
-#include "sd_logits.h"
+#include "sd_rows.cuh"
 
 namespace sdv {
 
@@ -29,15 +28,15 @@ __global__ void __launch_bounds__(kCntNT) sd_token_counts_kernel(
   const int b = blockIdx.x / nslice, s0 = (blockIdx.x % nslice) * slice;
   const int n = min(slice, V - s0), nw = (n + 1) >> 1, tid = threadIdx.x;
   const int32_t *h = history + (int64_t)b * L;
-  const int len = min(max(__ldg(lengths + b), 0), L);
-  const int pl = prompt_lengths ? min(max(__ldg(prompt_lengths + b), 0), len) : 0;
+  const int len = min(max(ld_int(lengths + b), 0), L);
+  const int pl = prompt_lengths ? min(max(ld_int(prompt_lengths + b), 0), len) : 0;
   for (int i = tid; i < nw; i += kCntNT) bins[i] = 0u;
   __syncthreads();
   bool bad = false;
   for (int c0 = pl; c0 < len; c0 += min(kCntChunk, len - c0)) {
     const int c1 = c0 + min(kCntChunk, len - c0);
     for (int i = c0 + tid; i < c1; i += kCntNT) {
-      const int t = __ldg(h + i);
+      const int t = ld_int(h + i);
       bad |= t < 0 || t >= V;
       const unsigned e = (unsigned)t - (unsigned)s0;
       if (e < (unsigned)n) atomicAdd(&bins[e >> 1], 1u << (16 * (e & 1u)));
@@ -52,7 +51,7 @@ __global__ void __launch_bounds__(kCntNT) sd_token_counts_kernel(
     }
   }
   for (int i = tid; i < pl; i += kCntNT) {
-    const int t = __ldg(h + i);
+    const int t = ld_int(h + i);
     bad |= t < 0 || t >= V;
     const unsigned e = (unsigned)t - (unsigned)s0;
     if (e < (unsigned)n) atomicOr(&bins[e >> 1], 0x8000u << (16 * (e & 1u)));
@@ -78,8 +77,8 @@ __global__ void __launch_bounds__(256) sd_token_counts_add_kernel(
   const int64_t x = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
   if (x >= total) return;
   const int b = (int)(x / M), i = (int)(x % M);
-  if (i >= __ldg(n + b)) return;
-  const int t = __ldg(tokens + x);
+  if (i >= ld_int(n + b)) return;
+  const int t = ld_int(tokens + x);
   if (t < 0 || t >= V) {
     if (status) atomicOr(status, (int)SD_STATUS_BAD_TOKEN);
     return;

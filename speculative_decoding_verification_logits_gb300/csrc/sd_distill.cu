@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kDistNT, 2) sd_distill_kernel(const DistParams
                        a.V);
   const int per = (row.nvec + cs - 1) / cs;
   const int qa = min(rank * per, row.nvec), qb = min(qa + per, row.nvec);
-  const float w = a.weight ? __ldg(a.weight + n) : 1.f;
+  const float w = a.weight ? ld_float(a.weight + n) : 1.f;
   const float zero[VE] = {};
   auto write = [&](int q, const float *f) {
     if (SAME) {
@@ -149,10 +149,10 @@ __global__ void __launch_bounds__(kDistNT, 2) sd_distill_kernel(const DistParams
   int id = -1;
   float t = neg_inf(), xs = neg_inf();
   if (tid < a.k) {
-    id = __ldg(a.ids + (int64_t)n * a.k + tid);
-    t = __ldg(a.vals + (int64_t)n * a.k + tid);
+    id = ld_int(a.ids + (int64_t)n * a.k + tid);
+    t = ld_float(a.vals + (int64_t)n * a.k + tid);
   }
-  const float rest = a.rest ? __ldg(a.rest + n) : neg_inf();
+  const float rest = a.rest ? ld_float(a.rest + n) : neg_inf();
   for (int i = tid; i < P.bit_words; i += NT) named[i] = 0u;
   if (tid == 0) bad_id = 0;
   __syncthreads();

@@ -24,7 +24,7 @@
 namespace sdv {
 
 constexpr int kProcNT = 256;
-constexpr int kProcU = 4;   // rows in flight per thread
+constexpr int kProcU = 4;   // vectors in flight per thread
 
 struct ProcParams {
   sd_process_args a;
@@ -36,155 +36,208 @@ struct ProcParams {
 // by less than VE, where the bits come back as zero), at most W words.
 template <int VE>
 __device__ __forceinline__ uint32_t mask_bits(const uint32_t *w, int e0, int W) {
-  if (e0 < 0) return (__ldg(w) << -e0) & ((1u << VE) - 1u);
+  if (e0 < 0) return (ld4(w) << -e0) & ((1u << VE) - 1u);
   const int i = e0 >> 5, s = e0 & 31;
-  uint32_t r = __ldg(w + i) >> s;
-  if (s + VE > 32 && i + 1 < W) r |= __ldg(w + i + 1) << (32 - s);
+  uint32_t r = ld4(w + i) >> s;
+  if (s + VE > 32 && i + 1 < W) r |= ld4(w + i + 1) << (32 - s);
   return r & ((1u << VE) - 1u);
 }
 
-// The words of vector v with -inf where its bit in `ok` is clear.
+// Bytes of x picked by the selector's nibbles; 8 + i gives byte i's sign in
+// every bit.
+__device__ __forceinline__ uint32_t prmt(uint32_t x, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(x), "r"(sel));
+  return r;
+}
+
+// The words of vector v with -inf where its bit in `ok` is clear: four bits
+// are spread to the sign bits of four bytes by one multiply (the partial
+// products do not meet), which byte permutes then copy over a half or a word.
 template <typename E>
 __device__ __forceinline__ uint4 mask_vec(uint4 v, uint32_t ok) {
-  uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t keep;
-    if (Elt<E>::kPerVec == 8)
-      keep = ((ok >> (2 * i)) & 1u) * 0x0000ffffu + ((ok >> (2 * i + 1)) & 1u) * 0xffff0000u;
-    else
-      keep = 0u - ((ok >> i) & 1u);
-    w[i] = (w[i] & keep) | (Elt<E>::kNegInfWord & ~keep);
+  const uint32_t lo = ((ok & 15u) * 0x10204080u) & 0x80808080u;
+  uint32_t k0, k1, k2, k3;
+  if (Elt<E>::kPerVec == 8) {
+    const uint32_t hi = ((ok >> 4) * 0x10204080u) & 0x80808080u;
+    k0 = prmt(lo, 0x9988);
+    k1 = prmt(lo, 0xbbaa);
+    k2 = prmt(hi, 0x9988);
+    k3 = prmt(hi, 0xbbaa);
+  } else {
+    k0 = prmt(lo, 0x8888);
+    k1 = prmt(lo, 0x9999);
+    k2 = prmt(lo, 0xaaaa);
+    k3 = prmt(lo, 0xbbbb);
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  const uint32_t inf = Elt<E>::kNegInfWord;
+  return make_uint4((v.x & k0) | (inf & ~k0), (v.y & k1) | (inf & ~k1), (v.z & k2) | (inf & ~k2),
+                    (v.w & k3) | (inf & ~k3));
 }
 
 // VEC: rows move as 16-byte vectors (the output's rows lie on the same place
-// of the 16-byte grid as the input's); otherwise element by element.
-template <typename E, bool VEC>
+// of the 16-byte grid as the input's); otherwise element by element.  VPT:
+// vectors of a row per thread.
+template <typename E, bool VEC, int VPT>
 __global__ void __launch_bounds__(kProcNT) sd_process_kernel(const ProcParams P) {
   constexpr int VE = VEC ? Elt<E>::kPerVec : 1, NT = kProcNT, NW = NT / 32;
   constexpr int SZ = Elt<E>::kSize;
   constexpr uint32_t kAll = (1u << VE) - 1u;
-  constexpr int kWin = NT * VE + VE;              // tokens of the window
+  constexpr int kOwn = NT * VPT * VE;              // tokens of a row in this CTA
+  // vectors of eight counts that the window (kOwn tokens, VE - 1 more before
+  // them for rows off the grid) can meet, and the tokens they hold
+  constexpr int kCntVec = (kOwn + VE + 7) / 8 + 1, kWin = kCntVec * 8;
+  constexpr int kCntPer = (kCntVec + NT - 1) / NT;
   constexpr int kWords = (kWin + 31) / 32;
-  constexpr int kBiasPer = SD_MAX_BIAS / NT;      // list entries per thread
+  constexpr int kBiasPer = SD_MAX_BIAS / NT;       // list entries per thread
   const sd_process_args &a = P.a;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  __shared__ uint16_t cnt[kWin];
   __shared__ uint16_t hot[kWin];                       // touched tokens of the window
   __shared__ float bias[kWin];                         // sum of each token's biases
-  __shared__ uint32_t touch[kWords];
+  __shared__ uint32_t touch[kWords];                   // a bit per token
   __shared__ int prev_i[SD_MAX_K], prev_v[SD_MAX_K];   // drafts inside the window, in order
   __shared__ int bias_v[SD_MAX_BIAS];                  // biases inside the window, in order
   __shared__ float bias_x[SD_MAX_BIAS];
   __shared__ int bias_n[kBiasPer][NW];
   __shared__ int n_prev, n_hot;
-  const int b = blockIdx.x / P.nslice, q0 = (blockIdx.x % P.nslice) * NT;
+  const int b = blockIdx.x / P.nslice, q0 = (blockIdx.x % P.nslice) * (NT * VPT);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int V = a.V, R = a.R, w0 = q0 * VE - VE;   // first token of the window
-  const float rep = a.repetition ? __ldg(a.repetition + b) : 1.f;
-  const float pres = a.presence ? __ldg(a.presence + b) : 0.f;
-  const float freq = a.frequency ? __ldg(a.frequency + b) : 0.f;
+  const int V = a.V, R = a.R;
+  const float rep = a.repetition ? ld_float(a.repetition + b) : 1.f;
+  const float pres = a.presence ? ld_float(a.presence + b) : 0.f;
+  const float freq = a.frequency ? ld_float(a.frequency + b) : 0.f;
   const bool bad = !(rep > 0.f && rep < INFINITY) || !(fabsf(pres) < INFINITY) ||
                    !(fabsf(freq) < INFINITY);
   const int n_draft = a.prev ? a.base + R - 1 : 0;
   const bool touches = a.counts || n_draft > 0 || a.n_bias > 0;   // part B has work at all
 
   // the window's counts, this round's drafts and the biases are asked for
-  // first and arrive during part A
-  uint32_t c[VE + 1];
+  // first and arrive during part A.  Counts come as vectors of their own
+  // 16-byte grid; the window's token 0 is the first one of count vector k0.
+  const uint16_t *cb = a.counts + (int64_t)b * V;
+  const int hpc = a.counts ? (int)((uintptr_t)cb & 15) / 2 : 0;
+  const int k0 = (max(q0 * VE - (VE - 1), 0) + hpc) / 8;
+  const int w0 = k0 * 8 - hpc;
+  uint4 c[kCntPer];
   if (a.counts) {
 #pragma unroll
-    for (int i = 0; i <= VE; ++i) {
-      const int j = i * NT + tid, v = w0 + j;
-      c[i] = j < kWin && v >= 0 && v < V ? __ldg(a.counts + (int64_t)b * V + v) : 0u;
+    for (int i = 0; i < kCntPer; ++i) {
+      const int k = i * NT + tid, v = w0 + k * 8;
+      c[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (k >= kCntVec) continue;
+      if (v >= 0 && v + 8 <= V) {
+        c[i] = ld16(cb + v);
+      } else {
+        uint32_t h[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[e] = v + e >= 0 && v + e < V ? ld2(cb + v + e) : 0u;
+        c[i] = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16),
+                          h[6] | (h[7] << 16));
+      }
     }
   }
   int draft = -1;
-  if (warp == 0 && lane < n_draft) draft = __ldg(a.prev + (int64_t)b * a.P + lane);
+  if (warp == 0 && lane < n_draft) draft = ld_int(a.prev + (int64_t)b * a.P + lane);
   int bid[kBiasPer];
   if (a.n_bias > 0) {
 #pragma unroll
     for (int j = 0; j < kBiasPer; ++j) {
       const int i = j * NT + tid;
-      bid[j] = i < a.n_bias ? __ldg(a.bias_ids + (int64_t)b * a.n_bias + i) : -1;
+      bid[j] = i < a.n_bias ? ld_int(a.bias_ids + (int64_t)b * a.n_bias + i) : -1;
     }
   }
 
-  // A. copy and mask
-  const int W = (V + 31) >> 5, q = q0 + tid;
+  // A. copy and mask, a vector's worth of columns of all rows after the other
+  const int W = (V + 31) >> 5;
   const uint8_t *xb = (const uint8_t *)a.logits + b * a.logits_sb * SZ;
   uint8_t *yb = (uint8_t *)a.out + b * a.out_sb * SZ;
   const uint32_t *mb = (const uint32_t *)a.mask + b * a.mask_sb;
-  // row r's place: its first element in this thread's vector and which of
-  // them lie in the row
-  auto place = [&](int r, int &e0, uint32_t &valid) {
-    e0 = q * VE - (VEC ? (int)((uintptr_t)(xb + r * a.logits_sr * SZ) & 15) / SZ : 0);
-    valid = kAll;
-    if (e0 < 0) valid = (kAll << -e0) & kAll;
-    if (e0 >= V) valid = 0u;
-    else if (e0 + VE > V) valid &= (1u << (V - e0)) - 1u;
-  };
-  auto allowed = [&](int r) {
-    int e0;
-    uint32_t valid;
-    if (r >= R) return 0u;
-    place(r, e0, valid);
-    if (valid == 0u || !a.mask) return valid;
-    return valid & mask_bits<VE>(mb + r * a.mask_sr, e0, W);
-  };
-  uint32_t next[kProcU];
+  const int64_t xs = a.logits_sr * SZ, ys = a.out_sr * SZ;
+  // this CTA's vectors lie inside the row whatever its place on the grid
+  const bool inner = q0 > 0 && (q0 + NT * VPT) * VE <= V;
+#pragma unroll 1
+  for (int i = 0; i < VPT; ++i) {
+    const int q = q0 + i * NT + tid;
+    // the row at x: its first element in this thread's vector, and which of
+    // the vector's places lie in the row
+    auto first = [&](const uint8_t *x) {
+      return q * VE - (VEC ? (int)((uintptr_t)x & 15) / SZ : 0);
+    };
+    auto inside = [&](int e0) -> uint32_t {
+      uint32_t in = kAll;
+      if (inner) return in;
+      if (e0 >= V) return 0u;
+      if (e0 < 0) in = (kAll << -e0) & kAll;
+      if (e0 + VE > V) in &= (1u << (V - e0)) - 1u;
+      return in;
+    };
+    const uint8_t *x = xb;          // row r0
+    uint8_t *y = yb;
+    const uint32_t *m = mb;         // row r0, then of the rows whose bits are asked for
+    uint32_t next[kProcU];          // allowed places of the next rows
+    auto ask = [&](const uint8_t *row, int n) {   // of the n rows from `row` and m on
 #pragma unroll
-  for (int u = 0; u < kProcU; ++u) next[u] = allowed(u);
-  for (int r0 = 0; r0 < R; r0 += kProcU) {
-    uint4 xv[kProcU];
-    uint32_t ok[kProcU];
-#pragma unroll
-    for (int u = 0; u < kProcU; ++u) {
-      ok[u] = next[u];
-      int e0;
-      uint32_t valid;
-      place(r0 + u, e0, valid);
-      if (!ok[u] || bad || (P.inplace && ok[u] == valid)) continue;
-      const uint8_t *x = xb + (r0 + u) * a.logits_sr * SZ;
-      if (VEC && valid == kAll) {
-        xv[u] = __ldcg(reinterpret_cast<const uint4 *>(x + (int64_t)e0 * SZ));
-      } else {
-        float f[Elt<E>::kPerVec] = {};
-#pragma unroll
-        for (int i = 0; i < VE; ++i)
-          if ((ok[u] >> i) & 1u) f[i] = Row<E>::load(x, e0 + i);
-        Row<E>::pack(f, xv[u]);
+      for (int u = 0; u < kProcU; ++u) {
+        next[u] = 0u;
+        if (u < n) {
+          const int e0 = first(row + u * xs);
+          next[u] = inside(e0);
+          if (a.mask && next[u]) next[u] &= mask_bits<VE>(m + u * a.mask_sr, e0, W);
+        }
       }
-    }
-    // the mask of the next rows, so that their loads need not wait for it
+    };
+    ask(x, R);
+    for (int left = R; left > 0; left -= kProcU) {
+      uint4 xv[kProcU];
+      uint32_t ok[kProcU];
 #pragma unroll
-    for (int u = 0; u < kProcU; ++u) next[u] = allowed(r0 + kProcU + u);
+      for (int u = 0; u < kProcU; ++u) {
+        ok[u] = next[u];
+        xv[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (u < left && ok[u] && !bad) {
+          const uint8_t *row = x + u * xs;
+          const int e0 = first(row);
+          const uint32_t in = inside(e0);
+          if (P.inplace && ok[u] == in) continue;
+          if (VEC && in == kAll) {
+            xv[u] = ld16(row + (int64_t)e0 * SZ);
+          } else {
+            float f[Elt<E>::kPerVec] = {};
 #pragma unroll
-    for (int u = 0; u < kProcU; ++u) {
-      int e0;
-      uint32_t valid;
-      place(r0 + u, e0, valid);
-      if (r0 + u >= R || valid == 0u || (P.inplace && ok[u] == valid && !bad)) continue;
-      uint4 v = make_uint4(Elt<E>::kNegInfWord, Elt<E>::kNegInfWord, Elt<E>::kNegInfWord,
-                           Elt<E>::kNegInfWord);
-      if (ok[u]) v = ok[u] == kAll ? xv[u] : mask_vec<E>(xv[u], ok[u]);
-      if (bad) {
-        const uint32_t nan = SZ == 2 ? 0x7fc07fc0u : 0x7fc00000u;
-        v = make_uint4(nan, nan, nan, nan);
+            for (int e = 0; e < VE; ++e)
+              if ((ok[u] >> e) & 1u) f[e] = Row<E>::load(row, e0 + e);
+            Row<E>::pack(f, xv[u]);
+          }
+        }
       }
-      uint8_t *y = yb + (r0 + u) * a.out_sr * SZ;
-      if (VEC && valid == kAll) {
-        *reinterpret_cast<uint4 *>(y + (int64_t)e0 * SZ) = v;
-      } else {
-        float f[Elt<E>::kPerVec];
-        Elt<E>::unpack(v, f);
+      // the mask of the rows after these, so that their loads need not wait for it
+      m += kProcU * a.mask_sr;
+      ask(x + kProcU * xs, left - kProcU);
 #pragma unroll
-        for (int i = 0; i < VE; ++i)
-          if ((valid >> i) & 1u) Row<E>::store(y, e0 + i, f[i]);
+      for (int u = 0; u < kProcU; ++u) {
+        if (u >= left) continue;
+        const int e0 = first(x + u * xs);
+        const uint32_t in = inside(e0);
+        if (in == 0u || (P.inplace && ok[u] == in && !bad)) continue;
+        uint4 v = ok[u] == kAll ? xv[u] : mask_vec<E>(xv[u], ok[u]);
+        if (bad) {
+          const uint32_t nan = SZ == 2 ? 0x7fc07fc0u : 0x7fc00000u;
+          v = make_uint4(nan, nan, nan, nan);
+        }
+        uint8_t *row = y + u * ys;
+        if (VEC && in == kAll) {
+          *reinterpret_cast<uint4 *>(row + (int64_t)e0 * SZ) = v;
+        } else {
+          float f[Elt<E>::kPerVec];
+          Elt<E>::unpack(v, f);
+#pragma unroll
+          for (int e = 0; e < VE; ++e)
+            if ((in >> e) & 1u) Row<E>::store(row, e0 + e, f[e]);
+        }
       }
+      x += kProcU * xs;
+      y += kProcU * ys;
     }
   }
   if (bad && tid == 0 && q0 == 0 && a.status) atomicOr(a.status, (int)SD_STATUS_BAD_PENALTY);
@@ -193,13 +246,19 @@ __global__ void __launch_bounds__(kProcNT) sd_process_kernel(const ProcParams P)
   // B. which tokens of the window are touched
   bool bad_id = false;
 #pragma unroll
-  for (int i = 0; i <= VE; ++i) {
-    const int j = i * NT + tid;
-    const uint32_t n = a.counts ? c[i] : 0u;
-    if (j < kWin) cnt[j] = (uint16_t)n;
-    const unsigned m = ballot(n != 0u);
-    if (lane == 0 && j < kWin) touch[j >> 5] = m;
+  for (int i = 0; i < kCntPer; ++i) {
+    const int k = i * NT + tid;
+    if (k >= kCntVec) continue;
+    uint32_t m = 0u;
+    if (a.counts) {
+      const uint32_t h[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        m |= ((h[e] & 0xffffu ? 1u : 0u) | (h[e] >> 16 ? 2u : 0u)) << (2 * e);
+    }
+    reinterpret_cast<uint8_t *>(touch)[k] = (uint8_t)m;
   }
+  if (tid < kWords * 4 - kCntVec) reinterpret_cast<uint8_t *>(touch)[kCntVec + tid] = 0u;
   if (warp == 0) {
     bad_id = lane < n_draft && (draft < 0 || draft >= V);
     const bool in = lane < n_draft && !bad_id && draft >= w0 && draft < w0 + kWin;
@@ -244,17 +303,17 @@ __global__ void __launch_bounds__(kProcNT) sd_process_kernel(const ProcParams P)
       if (bid[j] >= 0) {
         const int k = at[j] + __popc(bhit[j] & ((1u << lane) - 1u));
         bias_v[k] = bid[j] - w0;
-        bias_x[k] = __ldg(a.bias_vals + (int64_t)b * a.n_bias + j * NT + tid);
+        bias_x[k] = ld_float(a.bias_vals + (int64_t)b * a.n_bias + j * NT + tid);
         atomicOr(&touch[(bid[j] - w0) >> 5], 1u << ((bid[j] - w0) & 31));
       }
     __syncthreads();
     // a token's biases are summed in list order by the thread of its first one
     for (int k = tid; k < n; k += NT) {
       const int v = bias_v[k];
-      int first = k;
-      for (int o = 0; o < k && first == k; ++o)
-        if (bias_v[o] == v) first = o;
-      if (first != k) continue;
+      int one = k;
+      for (int o = 0; o < k && one == k; ++o)
+        if (bias_v[o] == v) one = o;
+      if (one != k) continue;
       float s = bias_x[k];
       for (int o = k + 1; o < n; ++o)
         if (bias_v[o] == v) s += bias_x[o];
@@ -281,18 +340,18 @@ __global__ void __launch_bounds__(kProcNT) sd_process_kernel(const ProcParams P)
   int tpr = 1;
   while (tpr < NT && tpr < n_hot) tpr *= 2;
   for (int r = tid / tpr; r < R; r += NT / tpr) {
-    const uint8_t *x = xb + r * a.logits_sr * SZ;
-    uint8_t *y = yb + r * a.out_sr * SZ;
+    const uint8_t *x = xb + r * xs;
+    uint8_t *y = yb + r * ys;
     const uint32_t *m = mb + r * a.mask_sr;
-    // a vector slice of a row off the grid covers VE tokens of its neighbour's window
+    // the tokens of this row that are this CTA's
     const int lo = q0 * VE - (VEC ? (int)((uintptr_t)x & 15) / SZ : 0);
     for (int h = tid & (tpr - 1); h < n_hot; h += tpr) {
       const int j = hot[h], v = w0 + j;
-      if (v < lo || v >= lo + NT * VE) continue;
-      if (a.mask && !((__ldg(m + (v >> 5)) >> (v & 31)) & 1u)) continue;
+      if (v < lo || v >= lo + kOwn) continue;
+      if (a.mask && !((ld4(m + (v >> 5)) >> (v & 31)) & 1u)) continue;
       float f = Row<E>::load(x, v);
+      const uint32_t word = a.counts ? ld2(cb + v) : 0u;
       if (f == neg_inf()) continue;
-      const uint32_t word = cnt[j];
       int n = (int)(word & 0x7fffu);
       for (int k = 0; k < n_prev; ++k) n += prev_v[k] == v && prev_i[k] < a.base + r;
       if (n > 0 || (word & 0x8000u)) f = f > 0.f ? f / rep : f * rep;
@@ -303,12 +362,12 @@ __global__ void __launch_bounds__(kProcNT) sd_process_kernel(const ProcParams P)
   }
 }
 
-template <typename E, bool VEC>
+template <typename E, bool VEC, int VPT>
 static cudaError_t launch_process(ProcParams &P, cudaStream_t s) {
   constexpr int VE = VEC ? Elt<E>::kPerVec : 1;
   // vectors of a row that starts anywhere on the 16-byte grid
   const int64_t nvec = ((int64_t)P.a.V + 2 * VE - 2) / VE;
-  P.nslice = (int)((nvec + kProcNT - 1) / kProcNT);
+  P.nslice = (int)((nvec + kProcNT * VPT - 1) / (kProcNT * VPT));
   if ((int64_t)P.a.B * P.nslice > INT32_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(P.a.B * P.nslice), 1, 1);
@@ -319,7 +378,17 @@ static cudaError_t launch_process(ProcParams &P, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sd_process_kernel<E, VEC>, (const ProcParams)P);
+  return cudaLaunchKernelEx(&cfg, sd_process_kernel<E, VEC, VPT>, (const ProcParams)P);
+}
+
+// Two vectors per thread where that still gives every SM several CTAs (the
+// window's list is then made half as often), else one.
+template <typename E>
+static cudaError_t launch_process_any(ProcParams &P, bool vec, cudaStream_t s) {
+  if (!vec) return launch_process<E, false, 1>(P, s);
+  const int64_t two = (int64_t)P.a.B * P.a.V / (2 * kProcNT * Elt<E>::kPerVec);
+  return two >= 8 * sm_count() ? launch_process<E, true, 2>(P, s)
+                               : launch_process<E, true, 1>(P, s);
 }
 
 }  // namespace sdv
@@ -360,10 +429,7 @@ extern "C" sd_status_t sd_process_logits(const sd_process_args *args, void *stre
                    ((uint64_t)(a.logits_sb - a.out_sb) * es % 16 == 0 || a.B <= 1) &&
                    ((uint64_t)(a.logits_sr - a.out_sr) * es % 16 == 0 || a.R <= 1);
   cudaStream_t s = (cudaStream_t)stream;
-  cudaError_t e;
-  if (a.dtype == SD_BF16)
-    e = vec ? launch_process<__nv_bfloat16, true>(P, s) : launch_process<__nv_bfloat16, false>(P, s);
-  else
-    e = vec ? launch_process<float, true>(P, s) : launch_process<float, false>(P, s);
+  const cudaError_t e = a.dtype == SD_BF16 ? launch_process_any<__nv_bfloat16>(P, vec, s)
+                                           : launch_process_any<float>(P, vec, s);
   return e == cudaSuccess ? SD_OK : e == cudaErrorInvalidValue ? SD_ERR_INVALID_ARG : SD_ERR_CUDA;
 }

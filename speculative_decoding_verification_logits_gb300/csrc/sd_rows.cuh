@@ -24,6 +24,31 @@ __device__ __forceinline__ void row_cluster_wait() {
   asm volatile("barrier.cluster.wait;" ::: "memory");
 }
 
+// Global loads that stay where they are written: volatile, so that none is
+// moved above the wait for the stream's previous kernel, across a barrier
+// after which memory holds something else (outputs in place of inputs), or
+// out of the condition that says whether its address is one at all (optional
+// arrays, places outside a row).  Through L2 only.
+__device__ __forceinline__ uint4 ld16(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld4(const void *p) {
+  uint32_t v;
+  asm volatile("ld.global.cg.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld2(const void *p) {
+  unsigned short v;
+  asm volatile("ld.global.cg.u16 %0, [%1];" : "=h"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ int ld_int(const int32_t *p) { return (int)ld4(p); }
+__device__ __forceinline__ float ld_float(const float *p) { return __uint_as_float(ld4(p)); }
+
 // Two floats rounded to nearest-even bf16, the first in the low half.
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
@@ -40,7 +65,7 @@ struct Row<float> {
                    __float_as_uint(f[3]));
   }
   static __device__ __forceinline__ float load(const uint8_t *row, int64_t e) {
-    return __ldcg(reinterpret_cast<const float *>(row) + e);
+    return __uint_as_float(ld4(reinterpret_cast<const float *>(row) + e));
   }
   static __device__ __forceinline__ void store(uint8_t *row, int64_t e, float f) {
     reinterpret_cast<float *>(row)[e] = f;
@@ -53,8 +78,7 @@ struct Row<__nv_bfloat16> {
                    pack_bf16(f[6], f[7]));
   }
   static __device__ __forceinline__ float load(const uint8_t *row, int64_t e) {
-    const unsigned short h = __ldcg(reinterpret_cast<const unsigned short *>(row) + e);
-    return __uint_as_float((uint32_t)h << 16);
+    return __uint_as_float(ld2(reinterpret_cast<const unsigned short *>(row) + e) << 16);
   }
   static __device__ __forceinline__ void store(uint8_t *row, int64_t e, float f) {
     reinterpret_cast<unsigned short *>(row)[e] = (unsigned short)pack_bf16(f, 0.f);
@@ -80,7 +104,7 @@ struct RowView {
   // vector q (q < nvec), -inf in the places outside the row
   __device__ __forceinline__ uint4 load(int q) const {
     const int e0 = first(q);
-    if (whole(q)) return __ldcg(reinterpret_cast<const uint4 *>(row + (int64_t)e0 * Elt<E>::kSize));
+    if (whole(q)) return ld16(row + (int64_t)e0 * Elt<E>::kSize);
     return load_edge(e0);
   }
   __device__ __noinline__ uint4 load_edge(int e0) const {

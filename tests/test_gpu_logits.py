@@ -153,6 +153,17 @@ def test_process_logits(dev, B, R, V, dtype):
     assert int(st) == 0
 
 
+@pytest.mark.parametrize("parts", [("counts", "prev", "base", "frequency"), ("mask",),
+                                   ("bias_ids", "bias_vals", "counts", "repetition")])
+@pytest.mark.parametrize("B,R,V,dtype", [(40, 2, 128256, BF), (80, 1, 32000, F32),
+                                         (101, 3, 50021, BF)])
+def test_process_logits_many_sequences(dev, B, R, V, dtype, parts):
+    # enough work for two vectors per thread
+    x, k = _process_case(B, R, V, dtype, 6)
+    k = {n: k[n] for n in parts}
+    _check_process(sd.process_logits(x.to(dev), **_to(k, dev)), x, k)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("parts", [(), ("counts",), ("counts", "repetition"), ("prev", "base"),
                                    ("prev", "base", "frequency", "presence"), ("mask",),
