@@ -21,6 +21,8 @@
 
 #include "sd_rows.cuh"
 
+#include <type_traits>
+
 namespace sdv {
 
 constexpr int kProcNT = 256;
@@ -79,7 +81,7 @@ __device__ __forceinline__ uint4 mask_vec(uint4 v, uint32_t ok) {
 // of the 16-byte grid as the input's); otherwise element by element.  VPT:
 // vectors of a row per thread.
 template <typename E, bool VEC, int VPT>
-__global__ void __launch_bounds__(kProcNT) sd_process_kernel(const ProcParams P) {
+__global__ void __launch_bounds__(kProcNT, 4) sd_process_kernel(const ProcParams P) {
   constexpr int VE = VEC ? Elt<E>::kPerVec : 1, NT = kProcNT, NW = NT / 32;
   constexpr int SZ = Elt<E>::kSize;
   constexpr uint32_t kAll = (1u << VE) - 1u;
@@ -154,11 +156,10 @@ __global__ void __launch_bounds__(kProcNT) sd_process_kernel(const ProcParams P)
   uint8_t *yb = (uint8_t *)a.out + b * a.out_sb * SZ;
   const uint32_t *mb = (const uint32_t *)a.mask + b * a.mask_sb;
   const int64_t xs = a.logits_sr * SZ, ys = a.out_sr * SZ;
-  // this CTA's vectors lie inside the row whatever its place on the grid
-  const bool inner = q0 > 0 && (q0 + NT * VPT) * VE <= V;
-#pragma unroll 1
-  for (int i = 0; i < VPT; ++i) {
-    const int q = q0 + i * NT + tid;
+  // INNER: this CTA's vectors lie inside the row whatever its place on the
+  // grid; its loop is kept apart from the one with the rows' ends
+  auto column = [&](auto INNER, int q) {
+    constexpr bool inner = decltype(INNER)::value;
     // the row at x: its first element in this thread's vector, and which of
     // the vector's places lie in the row
     auto first = [&](const uint8_t *x) {
@@ -239,6 +240,13 @@ __global__ void __launch_bounds__(kProcNT) sd_process_kernel(const ProcParams P)
       x += kProcU * xs;
       y += kProcU * ys;
     }
+  };
+  if (q0 > 0 && (q0 + NT * VPT) * VE <= V) {
+#pragma unroll 1
+    for (int i = 0; i < VPT; ++i) column(std::true_type(), q0 + i * NT + tid);
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < VPT; ++i) column(std::false_type(), q0 + i * NT + tid);
   }
   if (bad && tid == 0 && q0 == 0 && a.status) atomicOr(a.status, (int)SD_STATUS_BAD_PENALTY);
   if (!touches) return;
@@ -336,28 +344,44 @@ __global__ void __launch_bounds__(kProcNT) sd_process_kernel(const ProcParams P)
     for (uint32_t left = m; left; left &= left - 1u) hot[at++] = (uint16_t)(w * 32 + __ffs(left) - 1);
   }
   __syncthreads();
-  // tpr threads side by side take a row's listed tokens
-  int tpr = 1;
-  while (tpr < NT && tpr < n_hot) tpr *= 2;
-  for (int r = tid / tpr; r < R; r += NT / tpr) {
-    const uint8_t *x = xb + r * xs;
-    uint8_t *y = yb + r * ys;
-    const uint32_t *m = mb + r * a.mask_sr;
-    // the tokens of this row that are this CTA's
-    const int lo = q0 * VE - (VEC ? (int)((uintptr_t)x & 15) / SZ : 0);
-    for (int h = tid & (tpr - 1); h < n_hot; h += tpr) {
-      const int j = hot[h], v = w0 + j;
-      if (v < lo || v >= lo + kOwn) continue;
-      if (a.mask && !((ld4(m + (v >> 5)) >> (v & 31)) & 1u)) continue;
-      float f = Row<E>::load(x, v);
-      const uint32_t word = a.counts ? ld2(cb + v) : 0u;
-      if (f == neg_inf()) continue;
-      int n = (int)(word & 0x7fffu);
-      for (int k = 0; k < n_prev; ++k) n += prev_v[k] == v && prev_i[k] < a.base + r;
-      if (n > 0 || (word & 0x8000u)) f = f > 0.f ? f / rep : f * rep;
-      if (n > 0) f = f - freq * (float)n - pres;
-      if (a.n_bias > 0) f += bias[j];
-      Row<E>::store(y, v, f);
+  // tpt threads side by side take the listed tokens, NT / tpt such groups the
+  // rows; a thread has kProcU rows of its token in flight
+  int tpt = 1;
+  while (tpt < NT && tpt < n_hot) tpt *= 2;
+  const int groups = NT / tpt, r0 = tid / tpt;
+  for (int h = tid & (tpt - 1); h < n_hot; h += tpt) {
+    const int j = hot[h], v = w0 + j;
+    const uint32_t word = a.counts ? ld2(cb + v) : 0u;
+    const int n0 = (int)(word & 0x7fffu);
+    const float add = a.n_bias > 0 ? bias[j] : 0.f;
+    uint32_t drafts = 0u;   // the drafts that equal the token
+    for (int k = 0; k < n_prev; ++k) drafts |= prev_v[k] == v ? 1u << prev_i[k] : 0u;
+    for (int r = r0; r < R; r += groups * kProcU) {
+      float f[kProcU];
+#pragma unroll
+      for (int u = 0; u < kProcU; ++u) {
+        const int row = r + u * groups;
+        f[u] = neg_inf();
+        if (row >= R) continue;
+        const uint8_t *x = xb + row * xs;
+        // a row off the grid leaves up to VE - 1 of the window to a neighbour
+        const int lo = q0 * VE - (VEC ? (int)((uintptr_t)x & 15) / SZ : 0);
+        if (v < lo || v >= lo + kOwn) continue;
+        f[u] = Row<E>::load(x, v);
+        if (a.mask && !((ld4(mb + row * a.mask_sr + (v >> 5)) >> (v & 31)) & 1u)) f[u] = neg_inf();
+      }
+#pragma unroll
+      for (int u = 0; u < kProcU; ++u) {
+        const int row = r + u * groups;
+        float x = f[u];
+        if (x == neg_inf()) continue;   // not this CTA's, forbidden, or as it was
+        const int before = a.base + row;
+        const int n = n0 + __popc(before >= 32 ? drafts : drafts & ((1u << before) - 1u));
+        if (n > 0 || (word & 0x8000u)) x = x > 0.f ? x / rep : x * rep;
+        if (n > 0) x = x - freq * (float)n - pres;
+        if (a.n_bias > 0) x += add;
+        Row<E>::store(yb + row * ys, v, x);
+      }
     }
   }
 }
