@@ -26,11 +26,10 @@
 namespace sdv {
 
 constexpr int kProcNT = 256;
-constexpr int kProcU = 4;   // vectors in flight per thread
+constexpr int kProcU = 3;   // rows in flight per thread
 
 struct ProcParams {
   sd_process_args a;
-  int nslice;
   int inplace;
 };
 
@@ -78,14 +77,13 @@ __device__ __forceinline__ uint4 mask_vec(uint4 v, uint32_t ok) {
 }
 
 // VEC: rows move as 16-byte vectors (the output's rows lie on the same place
-// of the 16-byte grid as the input's); otherwise element by element.  VPT:
-// vectors of a row per thread.
-template <typename E, bool VEC, int VPT>
-__global__ void __launch_bounds__(kProcNT, 4) sd_process_kernel(const ProcParams P) {
+// of the 16-byte grid as the input's); otherwise element by element.
+template <typename E, bool VEC>
+__global__ void __launch_bounds__(kProcNT, 6) sd_process_kernel(const ProcParams P) {
   constexpr int VE = VEC ? Elt<E>::kPerVec : 1, NT = kProcNT, NW = NT / 32;
   constexpr int SZ = Elt<E>::kSize;
   constexpr uint32_t kAll = (1u << VE) - 1u;
-  constexpr int kOwn = NT * VPT * VE;              // tokens of a row in this CTA
+  constexpr int kOwn = NT * VE;                    // tokens of a row in this CTA
   // vectors of eight counts that the window (kOwn tokens, VE - 1 more before
   // them for rows off the grid) can meet, and the tokens they hold
   constexpr int kCntVec = (kOwn + VE + 7) / 8 + 1, kWin = kCntVec * 8;
@@ -103,7 +101,9 @@ __global__ void __launch_bounds__(kProcNT, 4) sd_process_kernel(const ProcParams
   __shared__ float bias_x[SD_MAX_BIAS];
   __shared__ int bias_n[kBiasPer][NW];
   __shared__ int n_prev, n_hot;
-  const int b = blockIdx.x / P.nslice, q0 = (blockIdx.x % P.nslice) * (NT * VPT);
+  // windows of low ids first: texts have most of their tokens there, so these
+  // CTAs' part B is the longest
+  const int b = blockIdx.x % a.B, q0 = (blockIdx.x / a.B) * NT;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int V = a.V, R = a.R;
   const float rep = a.repetition ? ld_float(a.repetition + b) : 1.f;
@@ -150,15 +150,15 @@ __global__ void __launch_bounds__(kProcNT, 4) sd_process_kernel(const ProcParams
     }
   }
 
-  // A. copy and mask, a vector's worth of columns of all rows after the other
-  const int W = (V + 31) >> 5;
+  // A. copy and mask this thread's vector of every row
+  const int W = (V + 31) >> 5, q = q0 + tid;
   const uint8_t *xb = (const uint8_t *)a.logits + b * a.logits_sb * SZ;
   uint8_t *yb = (uint8_t *)a.out + b * a.out_sb * SZ;
   const uint32_t *mb = (const uint32_t *)a.mask + b * a.mask_sb;
   const int64_t xs = a.logits_sr * SZ, ys = a.out_sr * SZ;
   // INNER: this CTA's vectors lie inside the row whatever its place on the
   // grid; its loop is kept apart from the one with the rows' ends
-  auto column = [&](auto INNER, int q) {
+  auto copy = [&](auto INNER) {
     constexpr bool inner = decltype(INNER)::value;
     // the row at x: its first element in this thread's vector, and which of
     // the vector's places lie in the row
@@ -241,13 +241,10 @@ __global__ void __launch_bounds__(kProcNT, 4) sd_process_kernel(const ProcParams
       y += kProcU * ys;
     }
   };
-  if (q0 > 0 && (q0 + NT * VPT) * VE <= V) {
-#pragma unroll 1
-    for (int i = 0; i < VPT; ++i) column(std::true_type(), q0 + i * NT + tid);
-  } else {
-#pragma unroll 1
-    for (int i = 0; i < VPT; ++i) column(std::false_type(), q0 + i * NT + tid);
-  }
+  if (q0 > 0 && (q0 + NT) * VE <= V)
+    copy(std::true_type());
+  else
+    copy(std::false_type());
   if (bad && tid == 0 && q0 == 0 && a.status) atomicOr(a.status, (int)SD_STATUS_BAD_PENALTY);
   if (!touches) return;
 
@@ -386,15 +383,15 @@ __global__ void __launch_bounds__(kProcNT, 4) sd_process_kernel(const ProcParams
   }
 }
 
-template <typename E, bool VEC, int VPT>
-static cudaError_t launch_process(ProcParams &P, cudaStream_t s) {
+template <typename E, bool VEC>
+static cudaError_t launch_process(const ProcParams &P, cudaStream_t s) {
   constexpr int VE = VEC ? Elt<E>::kPerVec : 1;
   // vectors of a row that starts anywhere on the 16-byte grid
   const int64_t nvec = ((int64_t)P.a.V + 2 * VE - 2) / VE;
-  P.nslice = (int)((nvec + kProcNT * VPT - 1) / (kProcNT * VPT));
-  if ((int64_t)P.a.B * P.nslice > INT32_MAX) return cudaErrorInvalidValue;
+  const int64_t grid = (nvec + kProcNT - 1) / kProcNT * P.a.B;
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(P.a.B * P.nslice), 1, 1);
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
   cfg.blockDim = dim3(kProcNT, 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -402,17 +399,7 @@ static cudaError_t launch_process(ProcParams &P, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sd_process_kernel<E, VEC, VPT>, (const ProcParams)P);
-}
-
-// Two vectors per thread where that still gives every SM several CTAs (the
-// window's list is then made half as often), else one.
-template <typename E>
-static cudaError_t launch_process_any(ProcParams &P, bool vec, cudaStream_t s) {
-  if (!vec) return launch_process<E, false, 1>(P, s);
-  const int64_t two = (int64_t)P.a.B * P.a.V / (2 * kProcNT * Elt<E>::kPerVec);
-  return two >= 8 * sm_count() ? launch_process<E, true, 2>(P, s)
-                               : launch_process<E, true, 1>(P, s);
+  return cudaLaunchKernelEx(&cfg, sd_process_kernel<E, VEC>, P);
 }
 
 }  // namespace sdv
@@ -453,7 +440,10 @@ extern "C" sd_status_t sd_process_logits(const sd_process_args *args, void *stre
                    ((uint64_t)(a.logits_sb - a.out_sb) * es % 16 == 0 || a.B <= 1) &&
                    ((uint64_t)(a.logits_sr - a.out_sr) * es % 16 == 0 || a.R <= 1);
   cudaStream_t s = (cudaStream_t)stream;
-  const cudaError_t e = a.dtype == SD_BF16 ? launch_process_any<__nv_bfloat16>(P, vec, s)
-                                           : launch_process_any<float>(P, vec, s);
+  cudaError_t e;
+  if (a.dtype == SD_BF16)
+    e = vec ? launch_process<__nv_bfloat16, true>(P, s) : launch_process<__nv_bfloat16, false>(P, s);
+  else
+    e = vec ? launch_process<float, true>(P, s) : launch_process<float, false>(P, s);
   return e == cudaSuccess ? SD_OK : e == cudaErrorInvalidValue ? SD_ERR_INVALID_ARG : SD_ERR_CUDA;
 }
