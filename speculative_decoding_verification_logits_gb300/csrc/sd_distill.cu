@@ -14,41 +14,30 @@
 // Gradient: named w/T (q - p) = w/T q (1 - e^d); others w/T (q_r - p_r) e_j / Z_r
 // with e_j / Z_r the softmax among the others.
 //
-// One cluster of cs CTAs per row, each CTA a contiguous share of the row's
-// vectors.  Pass 1: running maximum and sum of the others in one read (the
-// named tokens' places are bits in shared memory).  The cluster exchanges
-// (offset, sum) and every CTA works out the k + 1 buckets.  Pass 2 reads the
-// share again (from L2) and writes the gradient; the named places are
-// written over last.  HBM-bound: 2 or 4 bytes per logit for the loss, twice
-// that with the gradient.
+// One cluster of cs CTAs per row, which holds it in shared memory.  The named
+// places are set to -inf there, so that both passes meet only the others.
+// Pass 1: running maximum and sum.  The cluster exchanges (offset, sum) and
+// every CTA works out the k + 1 buckets.  Pass 2 writes the gradient of its
+// share, then the named places over it.  HBM-bound: 2 or 4 bytes per logit
+// for the loss, twice that with the gradient.
 
 #include "sd_rows.cuh"
 
 namespace sdv {
 
-constexpr int kDistNT = 512;
+constexpr int kDistNT = 256;
 constexpr int kDistNW = kDistNT / 32;
-constexpr int kDistU = 4;         // vectors in flight per thread
-constexpr int kDistMaxCS = 8;
+constexpr int kDistU = 4;         // vectors at a time per thread
 
 struct DistParams {
   sd_distill_args a;
   int cs;
-  int bit_words;   // shared-memory words of the named bits
 };
 
-// The sum of 2^(x c2 - o) over a share of the others; o = max x c2.
+// A share of the others: its largest logit, the sum of 2^((x - m) c2).
 struct DistStat {
-  float o, z;
-  int bad;
+  float m, z;
 };
-
-__device__ __forceinline__ void dist_merge(float &o, float &z, float o2, float z2) {
-  const float m = fmaxf(o, o2);
-  const float s = m == neg_inf() ? 0.f : m;   // an empty share leaves its zero sum as it is
-  z = z * ex2(o - s) + z2 * ex2(o2 - s);
-  o = m;
-}
 
 // d - 1 + exp(-d), without cancellation for small d
 __device__ __forceinline__ float dist_h(float d) {
@@ -89,62 +78,45 @@ __device__ __forceinline__ float block_max(float x, float *red) {
   return s;
 }
 
-template <typename E>
-__device__ __forceinline__ void store_vec(const RowView<E> &row, int q, const float *f) {
-  constexpr int VE = Elt<E>::kPerVec;
-  const int e0 = row.first(q);
-  uint8_t *y = const_cast<uint8_t *>(row.row);
-  if (row.whole(q)) {
-    uint4 v;
-    Row<E>::pack(f, v);
-    *reinterpret_cast<uint4 *>(y + (int64_t)e0 * Elt<E>::kSize) = v;
-  } else {
-#pragma unroll
-    for (int i = 0; i < VE; ++i)
-      if (e0 + i >= 0 && e0 + i < row.n) Row<E>::store(y, e0 + i, f[i]);
-  }
-}
-
 // GRAD: write the gradient; SAME: its rows lie on the 16-byte grid as the
 // student's do (whole vectors), otherwise they are written element by element.
 template <typename E, bool GRAD, bool SAME>
-__global__ void __launch_bounds__(kDistNT, 2) sd_distill_kernel(const DistParams P) {
-  constexpr int VE = Elt<E>::kPerVec, NT = kDistNT, NW = kDistNW;
+__global__ void __launch_bounds__(kDistNT, kHeldCtas) sd_distill_kernel(const DistParams P) {
+  constexpr int VE = Elt<E>::kPerVec, NT = kDistNT, NW = kDistNW, U = kDistU;
   const sd_distill_args &a = P.a;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  extern __shared__ uint32_t named[];   // bit per place of this CTA's vectors
+  extern __shared__ uint4 held[];
   cg::cluster_group cluster = cg::this_cluster();
   const int cs = P.cs, rank = (int)cluster.block_rank(), n = blockIdx.x / cs;
   const int tid = threadIdx.x;
-  __shared__ DistStat stat[kDistMaxCS];
-  __shared__ float red[NW];
-  __shared__ int bad_id;
-  const RowView<E> row(a.student, (int64_t)n * a.student_s, a.V);
-  const RowView<E> out(GRAD ? a.grad : a.student, (int64_t)n * (GRAD ? a.grad_s : a.student_s),
-                       a.V);
-  const int per = (row.nvec + cs - 1) / cs;
-  const int qa = min(rank * per, row.nvec), qb = min(qa + per, row.nvec);
+  __shared__ DistStat stat[kHeldMaxCS];
+  __shared__ float red[NW], wm[NW], wz[NW];
+  __shared__ __align__(16) int ids[SD_MAX_TOP];
+  Held<E> H(a.student, (int64_t)n * a.student_s, a.V, rank, cs, held);
   const float w = a.weight ? ld_float(a.weight + n) : 1.f;
-  const float zero[VE] = {};
-  auto write = [&](int q, const float *f) {
-    if (SAME) {
-      store_vec<E>(out, q, f);
+  uint8_t *out = GRAD ? (uint8_t *)a.grad + (int64_t)n * a.grad_s * Elt<E>::kSize : nullptr;
+  auto write = [&](int i, const uint4 &v) {   // vector i of the share
+    const int e0 = H.row.first(H.qa + i);
+    if (SAME && H.row.whole(H.qa + i)) {
+      *reinterpret_cast<uint4 *>(out + (int64_t)e0 * Elt<E>::kSize) = v;
     } else {
-      const int e0 = row.first(q);
-      uint8_t *y = const_cast<uint8_t *>(out.row);
+      float f[VE];
+      Elt<E>::unpack(v, f);
 #pragma unroll
-      for (int i = 0; i < VE; ++i)
-        if (e0 + i >= 0 && e0 + i < row.n) Row<E>::store(y, e0 + i, f[i]);
+      for (int e = 0; e < VE; ++e)
+        if (e0 + e >= 0 && e0 + e < a.V) Row<E>::store(out, e0 + e, f[e]);
     }
   };
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   if (w == 0.f) {   // the same for every CTA of the row
     if (GRAD)
-      for (int q = qa + tid; q < qb; q += NT) write(q, zero);
+      for (int i = tid; i < H.n; i += NT) write(i, zero);
     if (a.loss && rank == 0 && tid == 0) a.loss[n] = 0.f;
     return;
   }
   row_cluster_arrive();
+  H.template fetch<NT>();
   // the named tokens: one per thread
   int id = -1;
   float t = neg_inf(), xs = neg_inf();
@@ -153,92 +125,47 @@ __global__ void __launch_bounds__(kDistNT, 2) sd_distill_kernel(const DistParams
     t = ld_float(a.vals + (int64_t)n * a.k + tid);
   }
   const float rest = a.rest ? ld_float(a.rest + n) : neg_inf();
-  for (int i = tid; i < P.bit_words; i += NT) named[i] = 0u;
-  if (tid == 0) bad_id = 0;
-  __syncthreads();
-  bool mine = false;   // this CTA's share holds the token
-  if (id < -1 || id >= a.V) {
-    bad_id = 1;
-  } else if (id >= 0) {
-    xs = Row<E>::load(row.row, id);
-    const int at = id + row.hp - qa * VE;
-    mine = at >= 0 && at < (qb - qa) * VE;
-    if (mine && ((atomicOr(&named[at >> 5], 1u << (at & 31)) >> (at & 31)) & 1u)) bad_id = 1;
+  if (tid < SD_MAX_TOP) ids[tid] = id;
+  bool bad = id < -1 || id >= a.V;
+  const bool is = id >= 0 && !bad;
+  if (is) xs = Row<E>::load(H.row.row, id);
+  else t = neg_inf();
+  cp_wait<0>();
+  __syncthreads();   // the share and the ids are there
+  const int at = is ? H.place(id) : -1;
+  if (at >= 0) {
+    if (VE == 8) reinterpret_cast<uint16_t *>(held)[at] = 0xff80u;
+    else reinterpret_cast<uint32_t *>(held)[at] = 0xff800000u;
   }
-  if (id < 0) t = neg_inf();
-  __syncthreads();
-
-  // pass 1: the others' offset and sum
-  const float c2 = log2e_over(a.T);
-  float o = neg_inf(), z = 0.f;
-  for (int q = qa + tid; q < qb; q += NT * kDistU) {
-    uint4 v[kDistU];
-#pragma unroll
-    for (int u = 0; u < kDistU; ++u)
-      if (q + u * NT < qb) v[u] = row.load(q + u * NT);
-#pragma unroll
-    for (int u = 0; u < kDistU; ++u) {
-      const int p = q + u * NT;
-      if (p >= qb) continue;
-      float f[VE];
-      Elt<E>::unpack(v[u], f);
-      float m = Elt<E>::vmax(v[u]);
-      const int at = (p - qa) * VE;
-      const uint32_t bits = (named[at >> 5] >> (at & 31)) & ((1u << VE) - 1u);
-      if (bits) {
-        m = neg_inf();
-#pragma unroll
-        for (int i = 0; i < VE; ++i) {
-          if ((bits >> i) & 1u) f[i] = neg_inf();
-          m = fmaxf(m, f[i]);
-        }
-      }
-      if (m * c2 > o) {
-        z *= ex2(o - m * c2);
-        o = m * c2;
-      }
-      const float s = o == neg_inf() ? 0.f : o;
-#pragma unroll
-      for (int i = 0; i < VE; ++i) z += ex2(fmaf(f[i], c2, -s));
+  if (is)   // named before?
+    for (int i = 0; i < tid; i += 4) {
+      const int4 o = *reinterpret_cast<const int4 *>(ids + i);
+      bad |= o.x == id || (o.y == id && i + 1 < tid) || (o.z == id && i + 2 < tid) ||
+             (o.w == id && i + 3 < tid);
     }
-  }
-#pragma unroll
-  for (int i = 16; i > 0; i >>= 1) {
-    const float o2 = __shfl_xor_sync(0xffffffffu, o, i), z2 = __shfl_xor_sync(0xffffffffu, z, i);
-    dist_merge(o, z, o2, z2);
-  }
-  __shared__ float wo[NW], wz[NW];
-  if ((tid & 31) == 0) {
-    wo[tid >> 5] = o;
-    wz[tid >> 5] = z;
-  }
-  __syncthreads();
-  o = wo[0];
-  z = wz[0];
-#pragma unroll
-  for (int i = 1; i < NW; ++i) dist_merge(o, z, wo[i], wz[i]);
+  bad = __syncthreads_or(bad) != 0;
+
+  // pass 1: the others' largest logit and sum
+  const float c2 = log2e_over(a.T);
+  ExpSum<E> sum;
+  sum.template add_share<NT, U>(held, H.n, c2);
+  sum.template block<NW>(c2, wm, wz);
   row_cluster_wait();
   if (tid < cs) {
     DistStat *s = cluster.map_shared_rank(&stat[rank], tid);
-    s->o = o;
-    s->z = z;
-    s->bad = bad_id;
+    s->m = sum.m;
+    s->z = sum.z;
   }
   cluster.sync();
-  o = neg_inf();
-  z = 0.f;
-  bool bad = false;
-  for (int r = 0; r < cs; ++r) {
-    dist_merge(o, z, stat[r].o, stat[r].z);
-    bad |= stat[r].bad != 0;
-  }
+  float m = neg_inf(), z = 0.f;
+  for (int r = 0; r < cs; ++r) exp_merge(m, z, stat[r].m, stat[r].z, c2);
   // the teacher's shares, relative to its largest logit (in units of logits:
   // rest T is exact in the fused products)
-  const bool taught = __syncthreads_or((id >= 0 && t != neg_inf()) || rest != neg_inf());
+  const bool taught = __syncthreads_or((is && t != neg_inf()) || rest != neg_inf()) != 0;
   const float tm = block_max<NW>(fmaxf(t, tid == 0 ? rest * a.T : neg_inf()), red);
   if (bad || !taught) {   // the same for every CTA of the row
     if (GRAD)
-      for (int q = qa + tid; q < qb; q += NT) write(q, zero);
+      for (int i = tid; i < H.n; i += NT) write(i, zero);
     if (rank == 0 && tid == 0) {
       if (a.loss) a.loss[n] = 0.f;
       if (bad && a.status) atomicOr(a.status, (int)SD_STATUS_BAD_TOKEN);
@@ -251,18 +178,18 @@ __global__ void __launch_bounds__(kDistNT, 2) sd_distill_kernel(const DistParams
   const float zt = block_sum<NW>(te, red) + re;
   const float p = te / zt, pr = re / zt;
   // the student's, relative to its largest logit
-  const float so = fmaxf(block_max<NW>(xs * c2, red), o);
-  const float s0 = so == neg_inf() ? 0.f : so;
-  const float sl = fmaf(xs, c2, -s0), se = id >= 0 ? ex2(sl) : 0.f;
-  const float ol = o == neg_inf() ? neg_inf() : o - s0 + log2f(z);   // the others' log2 sum
-  const float zr = z * ex2(o - s0);
+  const float sm = fmaxf(block_max<NW>(xs, red), m);
+  const float s0 = sm == neg_inf() ? 0.f : sm;
+  const float sl = (xs - s0) * c2, se = is ? ex2(sl) : 0.f;
+  const float ol = m == neg_inf() ? neg_inf() : (m - s0) * c2 + log2f(z);   // the others' log2 sum
+  const float zr = z * ex2((m - s0) * c2);
   const float zs = block_sum<NW>(se, red) + zr;
   const float q = se / zs, qr = zr / zs;
   const float ln2 = 0.693147180559945309f;
   const float norm = log2f(zt) - log2f(zs);
   const float d = ((tl - sl) - norm) * ln2, dr = ((rl - ol) - norm) * ln2;
   if (a.loss && rank == 0) {
-    float term = id >= 0 ? dist_term(p, q, d) : 0.f;
+    float term = is ? dist_term(p, q, d) : 0.f;
     if (tid == 0) term += dist_term(pr, qr, dr);
     const float kl = block_sum<NW>(term, red);
     if (tid == 0) a.loss[n] = w * kl;
@@ -277,55 +204,25 @@ __global__ void __launch_bounds__(kDistNT, 2) sd_distill_kernel(const DistParams
   }
   const float wt = w / a.T;
   const float coef = z > 0.f || z != z ? wt * diff / z : 0.f;
-  const float o0 = o == neg_inf() ? 0.f : o;
-  for (int v0 = qa + tid; v0 < qb; v0 += NT * kDistU) {
-    uint4 v[kDistU];
-#pragma unroll
-    for (int u = 0; u < kDistU; ++u)
-      if (v0 + u * NT < qb) v[u] = row.load(v0 + u * NT);
-#pragma unroll
-    for (int u = 0; u < kDistU; ++u) {
-      if (v0 + u * NT >= qb) continue;
-      float f[VE];
-      Elt<E>::unpack(v[u], f);
-#pragma unroll
-      for (int i = 0; i < VE; ++i) f[i] = coef * ex2(fmaf(f[i], c2, -o0));
-      write(v0 + u * NT, f);
-    }
-  }
+  const float m0 = m == neg_inf() ? 0.f : m;
+  const uint64_t cc = pk2(c2, c2), oo = pk2(-m0, -m0), ss = pk2(coef, coef);
+#pragma unroll 4
+  for (int i = tid; i < H.n; i += NT) write(i, VecExp<E>::scaled(held[i], cc, oo, ss));
   __syncthreads();  // the named places are written over the pass above
-  if (mine) {
+  if (at >= 0) {
     const float g = fabsf(d) < 0.5f ? -q * expm1f(d) : q - p;
-    Row<E>::store(const_cast<uint8_t *>(out.row), id, wt * g);
+    Row<E>::store(out, id, wt * g);
   }
 }
 
 template <typename E, bool GRAD, bool SAME>
 static cudaError_t launch_distill(DistParams &P, cudaStream_t s) {
-  constexpr int VE = Elt<E>::kPerVec;
-  const int64_t nvec = ((int64_t)P.a.V + 2 * VE - 2) / VE;
-  const int64_t slots = 2LL * sm_count();
-  int cs = 1;
-  while (cs < kDistMaxCS && (int64_t)P.a.N * cs * 2 <= slots && nvec / (2 * cs) >= kDistNT)
-    cs *= 2;
-  P.cs = cs;
-  if ((int64_t)P.a.N * cs > INT32_MAX) return cudaErrorInvalidValue;
-  P.bit_words = (int)(((nvec + cs - 1) / cs * VE + 31) / 32);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(P.a.N * cs), 1, 1);
-  cfg.blockDim = dim3(kDistNT, 1, 1);
-  cfg.dynamicSmemBytes = (size_t)4 * P.bit_words;   // at most 32 KB
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cs;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, sd_distill_kernel<E, GRAD, SAME>, (const DistParams)P);
+  int smem = 0;
+  P.cs = held_cluster<E>(P.a.N, P.a.V, kDistNT, &smem);
+  static FuncAttrs attrs;
+  attrs.apply((const void *)sd_distill_kernel<E, GRAD, SAME>, kHeldBytes + 16, true,
+              "the distillation kernel");
+  return launch_held(sd_distill_kernel<E, GRAD, SAME>, P, P.a.N, P.cs, kDistNT, smem, s);
 }
 
 template <typename E>

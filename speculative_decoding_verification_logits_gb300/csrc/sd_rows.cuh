@@ -118,4 +118,219 @@ struct RowView {
   }
 };
 
+// -------------------------------------------------- rows held on chip --
+// A cluster of cs CTAs holds a row in shared memory, each CTA a contiguous
+// share of its vectors, so that the row is read from memory once however
+// often it is used.  (Read again through L2, a row's second pass came from
+// DRAM: the rows in flight and what is written for them exceed L2.)  Three
+// CTAs per SM: while one computes or writes, the others' copies are under way.
+constexpr int kHeldCtas = 3;
+constexpr int kHeldBytes = 66000;   // largest share: three of them and static arrays per SM
+constexpr int kHeldMaxCS = 16;
+
+template <typename E>
+struct Held {
+  RowView<E> row;
+  int qa, n;       // first vector and vectors of this CTA's share
+  uint4 *v;        // the share in shared memory, -inf outside the row
+  __device__ __forceinline__ Held(const void *base, int64_t offset, int V, int rank, int cs,
+                                  uint4 *smem)
+      : row(base, offset, V), v(smem) {
+    const int per = (row.nvec + cs - 1) / cs;
+    qa = min(rank * per, row.nvec);
+    n = min(per, row.nvec - qa);
+  }
+  // asks for every vector of the share; each thread copies its own ones
+  template <int NT>
+  __device__ __forceinline__ void fetch() {
+    for (int i = threadIdx.x; i < n; i += NT) {
+      const int q = qa + i;
+      if (row.whole(q))
+        cp_async16(smem_u32(v + i), row.row + (int64_t)row.first(q) * Elt<E>::kSize);
+      else
+        v[i] = row.load(q);
+    }
+    cp_commit();
+  }
+  // the place of element e in the share, or -1
+  __device__ __forceinline__ int place(int e) const {
+    const int at = e + row.hp - qa * RowView<E>::VE;
+    return at >= 0 && at < n * RowView<E>::VE ? at : -1;
+  }
+};
+
+// The cluster size for N rows of V elements: the fewest CTAs that hold a row,
+// more where N rows would leave SMs without their CTAs (down to two vectors
+// per thread).  0: a row does not fit.
+template <typename E>
+static int held_cluster(int64_t N, int V, int NT, int *share_bytes) {
+  constexpr int VE = Elt<E>::kPerVec;
+  const int64_t nvec = ((int64_t)V + 2 * VE - 2) / VE;
+  int64_t cs = (nvec * 16 + kHeldBytes - 1) / kHeldBytes;
+  if (cs > kHeldMaxCS) return 0;
+  const int64_t slots = (int64_t)kHeldCtas * sm_count();
+  while (cs < 8 && N * (cs + 1) <= slots && nvec / (cs + 1) >= 2 * NT) ++cs;
+  *share_bytes = (int)((nvec + cs - 1) / cs * 16);
+  return (int)cs;
+}
+
+// Launches fn(P) with one cluster of cs CTAs per row, as a programmatic
+// dependent of the stream's previous kernel.
+template <typename P>
+static cudaError_t launch_held(void (*fn)(const P), const P &params, int64_t N, int cs, int NT,
+                               int smem, cudaStream_t s) {
+  if (N * cs > INT32_MAX) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(N * cs), 1, 1);
+  cfg.blockDim = dim3(NT, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, fn, params);
+}
+
+// ------------------------------------------------- exponentials of vectors --
+// Per vector, with the offset and the scale as packed pairs: the sum of
+// 2^((x + o) c), and s 2^((x + o) c).  The offset is a logit and is taken off
+// before the scale goes on, so that rows of the type's lowest value (a mask's
+// stand-in for -inf) stay finite.
+template <typename E>
+struct VecExp;
+template <>
+struct VecExp<__nv_bfloat16> {
+  static __device__ __forceinline__ uint64_t pair(uint32_t w) {
+    return pk2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  }
+  static __device__ __forceinline__ void ex2_pair(uint32_t w, uint64_t c, uint64_t o, float &a,
+                                                  float &b) {
+    upk2(mul2(add2(pair(w), o), c), a, b);
+    a = ex2(a);
+    b = ex2(b);
+  }
+  static __device__ __forceinline__ uint64_t sum(const uint4 &v, uint64_t c, uint64_t o,
+                                                 uint64_t acc) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float a, b;
+      ex2_pair(w[i], c, o, a, b);
+      acc = add2(acc, pk2(a, b));
+    }
+    return acc;
+  }
+  static __device__ __forceinline__ uint4 scaled(const uint4 &v, uint64_t c, uint64_t o,
+                                                 uint64_t s) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float a, b;
+      ex2_pair(w[i], c, o, a, b);
+      upk2(mul2(pk2(a, b), s), a, b);
+      r[i] = pack_bf16(a, b);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+  }
+};
+template <>
+struct VecExp<float> {
+  static __device__ __forceinline__ void ex2_pair(uint32_t x, uint32_t y, uint64_t c, uint64_t o,
+                                                  float &a, float &b) {
+    upk2(mul2(add2(pk2(__uint_as_float(x), __uint_as_float(y)), o), c), a, b);
+    a = ex2(a);
+    b = ex2(b);
+  }
+  static __device__ __forceinline__ uint64_t sum(const uint4 &v, uint64_t c, uint64_t o,
+                                                 uint64_t acc) {
+    float a, b;
+    ex2_pair(v.x, v.y, c, o, a, b);
+    acc = add2(acc, pk2(a, b));
+    ex2_pair(v.z, v.w, c, o, a, b);
+    return add2(acc, pk2(a, b));
+  }
+  static __device__ __forceinline__ uint4 scaled(const uint4 &v, uint64_t c, uint64_t o,
+                                                 uint64_t s) {
+    float f[4];
+    ex2_pair(v.x, v.y, c, o, f[0], f[1]);
+    ex2_pair(v.z, v.w, c, o, f[2], f[3]);
+    upk2(mul2(pk2(f[0], f[1]), s), f[0], f[1]);
+    upk2(mul2(pk2(f[2], f[3]), s), f[2], f[3]);
+    uint4 r;
+    Row<float>::pack(f, r);
+    return r;
+  }
+};
+
+// Running (largest m, sum z of 2^((x - m) c)) over vectors.
+__device__ __forceinline__ void exp_merge(float &m, float &z, float m2, float z2, float c) {
+  const float b = fmaxf(m, m2), s = b == neg_inf() ? 0.f : b;   // an empty sum stays zero
+  z = z * ex2((m - s) * c) + z2 * ex2((m2 - s) * c);
+  m = b;
+}
+template <typename E>
+struct ExpSum {
+  float m, z;
+  __device__ __forceinline__ ExpSum() : m(neg_inf()), z(0.f) {}
+  // U vectors at once: one maximum, one rescaling
+  template <int U>
+  __device__ __forceinline__ void add(const uint4 *v, float c) {
+    float b = Elt<E>::vmax(v[0]);
+#pragma unroll
+    for (int u = 1; u < U; ++u) b = fmaxf(b, Elt<E>::vmax(v[u]));
+    if (b > m) {
+      z *= ex2((m - b) * c);
+      m = b;
+    }
+    const float s = m == neg_inf() ? 0.f : -m;
+    const uint64_t c2 = pk2(c, c), s2 = pk2(s, s);
+    uint64_t acc = 0ull;
+#pragma unroll
+    for (int u = 0; u < U; ++u) acc = VecExp<E>::sum(v[u], c2, s2, acc);
+    float x, y;
+    upk2(acc, x, y);
+    z += x + y;
+  }
+  // this thread's vectors of a share: NT apart, U at a time
+  template <int NT, int U>
+  __device__ __forceinline__ void add_share(const uint4 *held, int n, float c) {
+    int i = threadIdx.x;
+    for (; i + (U - 1) * NT < n; i += U * NT) {
+      uint4 v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = held[i + u * NT];
+      add<U>(v, c);
+    }
+    for (; i < n; i += NT) {
+      const uint4 v = held[i];
+      add<1>(&v, c);
+    }
+  }
+  // the block's, in every thread; wm and wz hold a float per warp
+  template <int NW>
+  __device__ __forceinline__ void block(float c, float *wm, float *wz) {
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, m, i), z2 = __shfl_xor_sync(0xffffffffu, z, i);
+      exp_merge(m, z, m2, z2, c);
+    }
+    if ((threadIdx.x & 31) == 0) {
+      wm[threadIdx.x >> 5] = m;
+      wz[threadIdx.x >> 5] = z;
+    }
+    __syncthreads();
+    m = wm[0];
+    z = wz[0];
+#pragma unroll
+    for (int i = 1; i < NW; ++i) exp_merge(m, z, wm[i], wz[i], c);
+  }
+};
+
 }  // namespace sdv
