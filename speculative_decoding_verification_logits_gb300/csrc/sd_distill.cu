@@ -29,9 +29,15 @@ constexpr int kDistNT = 256;
 constexpr int kDistNW = kDistNT / 32;
 constexpr int kDistU = 4;         // vectors at a time per thread
 
+constexpr int kStreamNT = 384;    // streamed rows: threads, two CTAs per SM
+constexpr int kStreamU = 4;       // vectors of a step per thread
+constexpr int kStreamD = 3;       // steps of the copy ring
+
 struct DistParams {
   sd_distill_args a;
-  int cs;
+  int cs;          // held rows: cluster size
+  int vec_words;   // streamed rows: words with a bit per vector, and
+  int bit_words;   // per place, of the named tokens
 };
 
 // A share of the others: its largest logit, the sum of 2^((x - m) c2).
@@ -55,27 +61,111 @@ __device__ __forceinline__ float dist_term(float p, float q, float d) {
   return fabsf(d) < 0.5f ? p * dist_h(d) : fmaf(p, d, q - p);
 }
 
-template <int NW>
-__device__ __forceinline__ float block_sum(float x, float *red) {
-  x = warp_sum(x);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-  __syncthreads();
-  float s = 0.f;
+// The named tokens of a row in shared memory: id (-1: empty slot), the
+// teacher's and the student's logit, and the gradient that comes out.
+struct Named {
+  int id[SD_MAX_TOP];
+  float t[SD_MAX_TOP], x[SD_MAX_TOP], g[SD_MAX_TOP];
+};
+// What a row's second pass needs: the others' gradient is
+// coef 2^((x - m) c2); not `live`: the row's loss and gradient are zero.
+struct Buckets {
+  float coef, m;
+  int live;
+};
+
+// The k + 1 buckets, by one warp: loss, the named tokens' gradients and the
+// others' factor from the others' (largest m, sum z of 2^((x - m) c2)).
+__device__ __forceinline__ void dist_buckets(Named &N, Buckets &B, int k, float rest, float T,
+                                             float c2, float w, float m, float z, bool bad,
+                                             float *loss) {
+  constexpr int J = SD_MAX_TOP / 32;
+  const int lane = threadIdx.x & 31;
+  float t[J], x[J];
+  bool is[J];
+  float tm = rest * T, sm = m;   // largest logits (rest T is exact in the fused product below)
+  bool taught = rest != neg_inf();
 #pragma unroll
-  for (int w = 0; w < NW; ++w) s += red[w];
-  __syncthreads();
-  return s;
+  for (int j = 0; j < J; ++j) {
+    const int i = j * 32 + lane;
+    is[j] = i < k && N.id[i] >= 0;
+    t[j] = is[j] ? N.t[i] : neg_inf();
+    x[j] = is[j] ? N.x[i] : neg_inf();
+    tm = fmaxf(tm, t[j]);
+    sm = fmaxf(sm, x[j]);
+    taught |= t[j] != neg_inf();
+  }
+  taught = ballot(taught) != 0u;
+  if (bad || !taught) {
+    if (lane == 0) {
+      B.live = 0;
+      if (loss) *loss = 0.f;
+    }
+    return;
+  }
+  tm = warp_max(tm);
+  sm = warp_max(sm);
+  const float s0 = sm == neg_inf() ? 0.f : sm;
+  float te[J], se[J], tsum = 0.f, ssum = 0.f;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    t[j] = (t[j] - tm) * c2;
+    x[j] = (x[j] - s0) * c2;
+    te[j] = ex2(t[j]);
+    se[j] = is[j] ? ex2(x[j]) : 0.f;
+    tsum += te[j];
+    ssum += se[j];
+  }
+  const float rl = rest == neg_inf() ? neg_inf() : fmaf(rest, T, -tm) * c2, re = ex2(rl);
+  const float ol = m == neg_inf() ? neg_inf() : (m - s0) * c2 + log2f(z);   // the others' log2 sum
+  const float zr = z * ex2((m - s0) * c2);
+  const float zt = warp_sum(tsum) + re, zs = warp_sum(ssum) + zr;
+  const float pr = re / zt, qr = zr / zs;
+  const float ln2 = 0.693147180559945309f;
+  const float norm = log2f(zt) - log2f(zs);
+  const float dr = ((rl - ol) - norm) * ln2;
+  const float wt = w / T;
+  float kl = lane == 0 ? dist_term(pr, qr, dr) : 0.f, named = 0.f;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    if (j * 32 >= k) continue;   // the same for the warp
+    const float p = te[j] / zt, q = se[j] / zs, d = ((t[j] - x[j]) - norm) * ln2;
+    if (is[j]) {
+      kl += dist_term(p, q, d);
+      N.g[j * 32 + lane] = wt * (fabsf(d) < 0.5f ? -q * expm1f(d) : q - p);
+      named += p - q;
+    }
+  }
+  kl = warp_sum(kl);
+  named = warp_sum(named);
+  if (lane == 0) {
+    if (loss) *loss = w * kl;
+    // q_r - p_r without cancellation: by expm1 where the others have little of
+    // the mass, from the named tokens' sums where they have most of it
+    float diff = qr;
+    if (pr > 0.f) diff = qr > 0.5f ? named : fabsf(dr) < 0.5f ? -qr * expm1f(dr) : qr - pr;
+    B.live = 1;
+    B.coef = z > 0.f || z != z ? wt * diff / z : 0.f;
+    B.m = m == neg_inf() ? 0.f : m;
+  }
 }
-template <int NW>
-__device__ __forceinline__ float block_max(float x, float *red) {
-  x = warp_max(x);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-  __syncthreads();
-  float s = neg_inf();
+
+// A vector of the gradient: q of a row of n elements at `row` in memory, SAME
+// grid or element by element from element e0 on.
+template <typename E, bool SAME>
+__device__ __forceinline__ void write_grad(uint8_t *out, const RowView<E> &row, int q,
+                                           const uint4 &v) {
+  constexpr int VE = Elt<E>::kPerVec;
+  const int e0 = row.first(q);
+  if (SAME && row.whole(q)) {
+    *reinterpret_cast<uint4 *>(out + (int64_t)e0 * Elt<E>::kSize) = v;
+  } else {
+    float f[VE];
+    Elt<E>::unpack(v, f);
 #pragma unroll
-  for (int w = 0; w < NW; ++w) s = fmaxf(s, red[w]);
-  __syncthreads();
-  return s;
+    for (int e = 0; e < VE; ++e)
+      if (e0 + e >= 0 && e0 + e < row.n) Row<E>::store(out, e0 + e, f[e]);
+  }
 }
 
 // GRAD: write the gradient; SAME: its rows lie on the 16-byte grid as the
@@ -91,27 +181,16 @@ __global__ void __launch_bounds__(kDistNT, kHeldCtas) sd_distill_kernel(const Di
   const int cs = P.cs, rank = (int)cluster.block_rank(), n = blockIdx.x / cs;
   const int tid = threadIdx.x;
   __shared__ DistStat stat[kHeldMaxCS];
-  __shared__ float red[NW], wm[NW], wz[NW];
-  __shared__ __align__(16) int ids[SD_MAX_TOP];
+  __shared__ float wm[NW], wz[NW];
+  __shared__ __align__(16) Named named;
+  __shared__ Buckets buckets;
   Held<E> H(a.student, (int64_t)n * a.student_s, a.V, rank, cs, held);
   const float w = a.weight ? ld_float(a.weight + n) : 1.f;
   uint8_t *out = GRAD ? (uint8_t *)a.grad + (int64_t)n * a.grad_s * Elt<E>::kSize : nullptr;
-  auto write = [&](int i, const uint4 &v) {   // vector i of the share
-    const int e0 = H.row.first(H.qa + i);
-    if (SAME && H.row.whole(H.qa + i)) {
-      *reinterpret_cast<uint4 *>(out + (int64_t)e0 * Elt<E>::kSize) = v;
-    } else {
-      float f[VE];
-      Elt<E>::unpack(v, f);
-#pragma unroll
-      for (int e = 0; e < VE; ++e)
-        if (e0 + e >= 0 && e0 + e < a.V) Row<E>::store(out, e0 + e, f[e]);
-    }
-  };
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   if (w == 0.f) {   // the same for every CTA of the row
     if (GRAD)
-      for (int i = tid; i < H.n; i += NT) write(i, zero);
+      for (int i = tid; i < H.n; i += NT) write_grad<E, SAME>(out, H.row, H.qa + i, zero);
     if (a.loss && rank == 0 && tid == 0) a.loss[n] = 0.f;
     return;
   }
@@ -125,13 +204,16 @@ __global__ void __launch_bounds__(kDistNT, kHeldCtas) sd_distill_kernel(const Di
     t = ld_float(a.vals + (int64_t)n * a.k + tid);
   }
   const float rest = a.rest ? ld_float(a.rest + n) : neg_inf();
-  if (tid < SD_MAX_TOP) ids[tid] = id;
   bool bad = id < -1 || id >= a.V;
   const bool is = id >= 0 && !bad;
   if (is) xs = Row<E>::load(H.row.row, id);
-  else t = neg_inf();
+  if (tid < SD_MAX_TOP) {
+    named.id[tid] = is ? id : -1;
+    named.t[tid] = t;
+    named.x[tid] = xs;
+  }
   cp_wait<0>();
-  __syncthreads();   // the share and the ids are there
+  __syncthreads();   // the share and the named tokens are there
   const int at = is ? H.place(id) : -1;
   if (at >= 0) {
     if (VE == 8) reinterpret_cast<uint16_t *>(held)[at] = 0xff80u;
@@ -139,7 +221,7 @@ __global__ void __launch_bounds__(kDistNT, kHeldCtas) sd_distill_kernel(const Di
   }
   if (is)   // named before?
     for (int i = 0; i < tid; i += 4) {
-      const int4 o = *reinterpret_cast<const int4 *>(ids + i);
+      const int4 o = *reinterpret_cast<const int4 *>(named.id + i);
       bad |= o.x == id || (o.y == id && i + 1 < tid) || (o.z == id && i + 2 < tid) ||
              (o.w == id && i + 3 < tid);
     }
@@ -157,66 +239,202 @@ __global__ void __launch_bounds__(kDistNT, kHeldCtas) sd_distill_kernel(const Di
     s->z = sum.z;
   }
   cluster.sync();
-  float m = neg_inf(), z = 0.f;
-  for (int r = 0; r < cs; ++r) exp_merge(m, z, stat[r].m, stat[r].z, c2);
-  // the teacher's shares, relative to its largest logit (in units of logits:
-  // rest T is exact in the fused products)
-  const bool taught = __syncthreads_or((is && t != neg_inf()) || rest != neg_inf()) != 0;
-  const float tm = block_max<NW>(fmaxf(t, tid == 0 ? rest * a.T : neg_inf()), red);
-  if (bad || !taught) {   // the same for every CTA of the row
-    if (GRAD)
-      for (int i = tid; i < H.n; i += NT) write(i, zero);
-    if (rank == 0 && tid == 0) {
-      if (a.loss) a.loss[n] = 0.f;
-      if (bad && a.status) atomicOr(a.status, (int)SD_STATUS_BAD_TOKEN);
-    }
-    return;
-  }
-  const float tl = (t - tm) * c2;
-  const float rl = rest == neg_inf() ? neg_inf() : fmaf(rest, a.T, -tm) * c2;
-  const float te = ex2(tl), re = ex2(rl);
-  const float zt = block_sum<NW>(te, red) + re;
-  const float p = te / zt, pr = re / zt;
-  // the student's, relative to its largest logit
-  const float sm = fmaxf(block_max<NW>(xs, red), m);
-  const float s0 = sm == neg_inf() ? 0.f : sm;
-  const float sl = (xs - s0) * c2, se = is ? ex2(sl) : 0.f;
-  const float ol = m == neg_inf() ? neg_inf() : (m - s0) * c2 + log2f(z);   // the others' log2 sum
-  const float zr = z * ex2((m - s0) * c2);
-  const float zs = block_sum<NW>(se, red) + zr;
-  const float q = se / zs, qr = zr / zs;
-  const float ln2 = 0.693147180559945309f;
-  const float norm = log2f(zt) - log2f(zs);
-  const float d = ((tl - sl) - norm) * ln2, dr = ((rl - ol) - norm) * ln2;
-  if (a.loss && rank == 0) {
-    float term = is ? dist_term(p, q, d) : 0.f;
-    if (tid == 0) term += dist_term(pr, qr, dr);
-    const float kl = block_sum<NW>(term, red);
-    if (tid == 0) a.loss[n] = w * kl;
+  if (tid < 32) {
+    float m = neg_inf(), z = 0.f;
+    for (int r = 0; r < cs; ++r) exp_merge(m, z, stat[r].m, stat[r].z, c2);
+    dist_buckets(named, buckets, a.k, rest, a.T, c2, w, m, z, bad,
+                 a.loss && rank == 0 ? a.loss + n : nullptr);
+    if (bad && rank == 0 && tid == 0 && a.status) atomicOr(a.status, (int)SD_STATUS_BAD_TOKEN);
   }
   if (!GRAD) return;
-  // q_r - p_r without cancellation: by expm1 where the others have little of
-  // the mass, from the named tokens' sums where they have most of it
-  float diff = qr;
-  if (pr > 0.f) {
-    const float named_diff = block_sum<NW>(p - q, red);
-    diff = qr > 0.5f ? named_diff : fabsf(dr) < 0.5f ? -qr * expm1f(dr) : qr - pr;
+  __syncthreads();
+  if (!buckets.live) {
+    for (int i = tid; i < H.n; i += NT) write_grad<E, SAME>(out, H.row, H.qa + i, zero);
+    return;
   }
-  const float wt = w / a.T;
-  const float coef = z > 0.f || z != z ? wt * diff / z : 0.f;
-  const float m0 = m == neg_inf() ? 0.f : m;
-  const uint64_t cc = pk2(c2, c2), oo = pk2(-m0, -m0), ss = pk2(coef, coef);
+  const uint64_t cc = pk2(c2, c2), mm = pk2(-buckets.m, -buckets.m),
+                 ss = pk2(buckets.coef, buckets.coef);
 #pragma unroll 4
-  for (int i = tid; i < H.n; i += NT) write(i, VecExp<E>::scaled(held[i], cc, oo, ss));
+  for (int i = tid; i < H.n; i += NT)
+    write_grad<E, SAME>(out, H.row, H.qa + i, VecExp<E>::scaled(held[i], cc, mm, ss));
   __syncthreads();  // the named places are written over the pass above
-  if (at >= 0) {
-    const float g = fabsf(d) < 0.5f ? -q * expm1f(d) : q - p;
-    Row<E>::store(out, id, wt * g);
+  if (at >= 0) Row<E>::store(out, id, named.g[tid]);
+}
+
+// Many rows: one CTA per row, streamed once for the sum and, for the gradient,
+// once more from L2.  The named tokens are marked in shared memory, a bit per
+// vector (looked at for every vector) and a bit per place.  Nothing but the
+// CTA's own barriers lies between the passes.
+template <typename E, bool GRAD, bool SAME>
+__global__ void __launch_bounds__(kStreamNT, 2) sd_distill_stream_kernel(const DistParams P) {
+  constexpr int VE = Elt<E>::kPerVec, NT = kStreamNT, NW = NT / 32, U = kStreamU;
+  static_assert(U == 4, "a warp's four words of vector bits are one load");
+  const sd_distill_args &a = P.a;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  using Stream = RowStream<E, NT, U, kStreamD>;
+  extern __shared__ uint4 ring[];
+  uint32_t *vecs = reinterpret_cast<uint32_t *>(ring + Stream::kBytes / 16);
+  uint32_t *bits = vecs + P.vec_words;
+  __shared__ float wm[NW], wz[NW];
+  __shared__ Named named;
+  __shared__ Buckets buckets;
+  __shared__ int dup;
+  const int tid = threadIdx.x;
+  for (int i = tid; i < P.vec_words + P.bit_words; i += NT) vecs[i] = 0u;
+  if (tid == 0) dup = 0;
+  Stream S(ring, a.student, a.student_s, a.N, a.V, GRAD ? 2 : 1, a.weight);
+  const float c2 = log2e_over(a.T);
+  // this row's teacher, asked for a row ahead
+  int id_next = -1;
+  float t_next = neg_inf(), w_next = 1.f, rest_next = neg_inf();
+  auto ahead = [&](int n) {
+    if (n >= a.N) return;
+    if (tid < a.k) {
+      id_next = ld_int(a.ids + (int64_t)n * a.k + tid);
+      t_next = ld_float(a.vals + (int64_t)n * a.k + tid);
+    }
+    if (a.weight) w_next = ld_float(a.weight + n);
+    if (a.rest) rest_next = ld_float(a.rest + n);
+  };
+  ahead(blockIdx.x);
+  int late = -1;            // a named place of the row before, still to be written
+  uint8_t *late_out = nullptr;
+  __syncthreads();
+  for (int n = blockIdx.x; n < a.N; n += gridDim.x) {
+    const int id = id_next;
+    const float t = t_next, w = w_next, rest = rest_next;
+    ahead(n + gridDim.x);
+    const RowView<E> row(a.student, (int64_t)n * a.student_s, a.V);
+    uint8_t *out = GRAD ? (uint8_t *)a.grad + (int64_t)n * a.grad_s * Elt<E>::kSize : nullptr;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    if (w == 0.f) {
+      if (GRAD)
+        for (int q = tid; q < row.nvec; q += NT) write_grad<E, SAME>(out, row, q, zero);
+      if (a.loss && tid == 0) a.loss[n] = 0.f;
+      continue;
+    }
+    bool bad = id < -1 || id >= a.V;
+    const bool is = id >= 0 && !bad;
+    const int at = id + row.hp;
+    float xs = neg_inf();
+    if (is) {
+      xs = Row<E>::load(row.row, id);
+      if ((atomicOr(&bits[at >> 5], 1u << (at & 31)) >> (at & 31)) & 1u) dup = 1;
+      atomicOr(&vecs[at / VE >> 5], 1u << (at / VE & 31));
+    }
+    if (bad) dup = 1;
+    __syncthreads();   // the bits are set; the row before is all written
+    if (late >= 0) Row<E>::store(late_out, late, named.g[tid]);
+    // pass 1
+    ExpSum<E> sum;
+    for (int q = 0; q < row.nvec; q += Stream::kStep) {
+      uint4 v[U];
+      S.next(v);
+      const int first = q + Stream::at();
+      if (q + Stream::kStep > row.nvec) {
+        const uint32_t inf = Elt<E>::kNegInfWord;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (first + u * 32 >= row.nvec) v[u] = make_uint4(inf, inf, inf, inf);
+      }
+      const uint4 mark = *reinterpret_cast<const uint4 *>(vecs + (q >> 5) + (tid >> 5) * U);
+      if (mark.x | mark.y | mark.z | mark.w) {
+        const uint32_t w[U] = {mark.x, mark.y, mark.z, mark.w};
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (!((w[u] >> (tid & 31)) & 1u)) continue;
+          const int at = (first + u * 32) * VE;
+          const uint32_t hit = bits[at >> 5] >> (at & 31);
+          float f[VE];
+          Elt<E>::unpack(v[u], f);
+#pragma unroll
+          for (int e = 0; e < VE; ++e)
+            if ((hit >> e) & 1u) f[e] = neg_inf();
+          Row<E>::pack(f, v[u]);
+        }
+      }
+      sum.template add<U>(v, c2);
+    }
+    if (tid < SD_MAX_TOP) {
+      named.id[tid] = is ? id : -1;
+      named.t[tid] = t;
+      named.x[tid] = xs;
+    }
+    sum.template block<NW>(c2, wm, wz);   // its barrier: the named tokens are there too
+    if (is) bits[at >> 5] = vecs[at / VE >> 5] = 0u;
+    if (tid < 32) {
+      const bool any = dup != 0;
+      dist_buckets(named, buckets, a.k, rest, a.T, c2, w, sum.m, sum.z, any,
+                   a.loss ? a.loss + n : nullptr);
+      if (tid == 0) {
+        dup = 0;
+        if (any && a.status) atomicOr(a.status, (int)SD_STATUS_BAD_TOKEN);
+      }
+    }
+    __syncthreads();
+    late = -1;
+    if (!GRAD) continue;
+    // pass 2
+    const bool live = buckets.live != 0;
+    const float coef = live ? buckets.coef : 0.f;
+    const uint64_t cc = pk2(c2, c2), mm = pk2(-buckets.m, -buckets.m), ss = pk2(coef, coef);
+    uint8_t *to = out + ((int64_t)Stream::at() * VE - row.hp) * Elt<E>::kSize;
+    for (int q = 0; q < row.nvec; q += Stream::kStep, to += Stream::kStep * 16) {
+      uint4 v[U];
+      S.next(v);
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = live ? VecExp<E>::scaled(v[u], cc, mm, ss) : zero;
+      if (SAME && q > 0 && q + Stream::kStep < row.nvec) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) *reinterpret_cast<uint4 *>(to + u * 512) = v[u];
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = q + Stream::at() + u * 32;
+          if (i < row.nvec) write_grad<E, SAME>(out, row, i, v[u]);
+        }
+      }
+    }
+    if (is && live) {   // written over the pass above, after the next barrier
+      late = id;
+      late_out = out;
+    }
+  }
+  if (GRAD) {
+    __syncthreads();
+    if (late >= 0) Row<E>::store(late_out, late, named.g[tid]);
   }
 }
 
 template <typename E, bool GRAD, bool SAME>
+static cudaError_t launch_distill_stream(DistParams &P, cudaStream_t s) {
+  constexpr int VE = Elt<E>::kPerVec;
+  using Stream = RowStream<E, kStreamNT, kStreamU, kStreamD>;
+  const int64_t nvec = ((int64_t)P.a.V + 2 * VE - 2) / VE;
+  P.vec_words = (int)((nvec + Stream::kStep - 1) / Stream::kStep * (Stream::kStep / 32));
+  P.bit_words = (int)((nvec * VE + 31) / 32);
+  static FuncAttrs attrs;
+  attrs.apply((const void *)sd_distill_stream_kernel<E, GRAD, SAME>, 220 * 1024, false,
+              "the distillation kernel");
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min(P.a.N, 2 * sm_count()), 1, 1);
+  cfg.blockDim = dim3(kStreamNT, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)Stream::kBytes + 4 * (size_t)(P.vec_words + P.bit_words);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sd_distill_stream_kernel<E, GRAD, SAME>, (const DistParams)P);
+}
+
+template <typename E, bool GRAD, bool SAME>
 static cudaError_t launch_distill(DistParams &P, cudaStream_t s) {
+  const int mode = env_int("SDL_STREAM", -1);
+  if (mode != 0 && (mode > 0 || P.a.N >= 2 * sm_count()))
+    return launch_distill_stream<E, GRAD, SAME>(P, s);
   int smem = 0;
   P.cs = held_cluster<E>(P.a.N, P.a.V, kDistNT, &smem);
   static FuncAttrs attrs;

@@ -197,6 +197,95 @@ static cudaError_t launch_held(void (*fn)(const P), const P &params, int64_t N, 
   return cudaLaunchKernelEx(&cfg, fn, params);
 }
 
+// ------------------------------------------------------ rows streamed --
+// One CTA takes rows first, first + grid, ... from end to end (each `passes`
+// times in a row).  Every thread copies its own vectors, U a step, into its
+// own places of a ring of D steps; the copies run on across the ends of
+// passes and rows, so that what happens there costs no bandwidth.  Rows of
+// weight 0 are left out.  In a step a warp has 32 U vectors side by side:
+// its vector u of the step that begins at q is q + at() + 32 u.
+template <typename E, int NT, int U, int D>
+struct RowStream {
+  static constexpr int kStep = NT * U;                  // vectors of a step
+  static constexpr int kBytes = D * kStep * 16;
+  uint4 *ring;
+  const void *base;
+  const float *weight;
+  int64_t stride;
+  int N, V, passes;
+  // the next step to ask for
+  RowView<E> view;
+  const uint8_t *src;   // this thread's first vector of it, where it is inside the row
+  int row, pass, q, put, take;
+  static __device__ __forceinline__ int at() {
+    return (threadIdx.x >> 5) * 32 * U + (threadIdx.x & 31);
+  }
+  __device__ __forceinline__ RowStream(uint4 *ring_, const void *base_, int64_t stride_, int N_,
+                                       int V_, int passes_, const float *weight_)
+      : ring(ring_ + threadIdx.x), base(base_), weight(weight_), stride(stride_), N(N_), V(V_),
+        passes(passes_), view(base_, 0, V_), row(blockIdx.x), put(0), take(0) {
+    open();
+#pragma unroll 1
+    for (int d = 0; d < D - 1; ++d) ask();
+  }
+  // at `row` or the next one that counts
+  __device__ __forceinline__ void open() {
+    if (weight)
+      while (row < N && ld_float(weight + row) == 0.f) row += gridDim.x;
+    if (row < N) view = RowView<E>(base, (int64_t)row * stride, V);
+    pass = 0;
+    rewind();
+  }
+  __device__ __forceinline__ void rewind() {
+    q = 0;
+    src = view.row + ((int64_t)at() * RowView<E>::VE - view.hp) * Elt<E>::kSize;
+  }
+  __device__ __forceinline__ void ask() {
+    uint4 *to = ring + put * kStep;
+    if (row < N) {
+      if (q > 0 && q + kStep < view.nvec) {   // no end of the row in the step
+#pragma unroll
+        for (int u = 0; u < U; ++u) cp_async16(smem_u32(to + u * NT), src + u * 512);
+      } else {
+#pragma unroll 1
+        for (int u = 0; u < U; ++u) {
+          const int i = q + at() + u * 32;
+          if (i >= view.nvec) break;
+          if (view.whole(i)) cp_async16(smem_u32(to + u * NT), src + u * 512);
+          else to[u * NT] = view.load(i);
+        }
+      }
+      q += kStep;
+      src += kStep * 16;
+      if (q >= view.nvec) {
+        if (++pass < passes) {
+          rewind();
+        } else {
+          row += gridDim.x;
+          open();
+        }
+      }
+    }
+    cp_commit();
+    put = put + 1 == D ? 0 : put + 1;
+  }
+  // the oldest step's vectors; asks for another one
+  __device__ __forceinline__ void next(uint4 *v) {
+    cp_wait<D - 2>();
+    const uint4 *from = ring + take * kStep;
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = from[u * NT];
+    take = take + 1 == D ? 0 : take + 1;
+    ask();
+  }
+  // vector u of the step `ahead` (< D - 1) steps after the oldest, once it is there
+  __device__ __forceinline__ uint4 peek(int ahead, int u) const {
+    int slot = take + ahead;
+    slot = slot >= D ? slot - D : slot;
+    return ring[slot * kStep + u * NT];
+  }
+};
+
 // ------------------------------------------------- exponentials of vectors --
 // Per vector, with the offset and the scale as packed pairs: the sum of
 // 2^((x + o) c), and s 2^((x + o) c).  The offset is a logit and is taken off
@@ -206,6 +295,17 @@ template <typename E>
 struct VecExp;
 template <>
 struct VecExp<__nv_bfloat16> {
+  // the largest element of U vectors (packed maxima, exact)
+  template <int U>
+  static __device__ __forceinline__ float largest(const uint4 *v) {
+    const auto h = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); };
+    __nv_bfloat162 m = __hmax2(__hmax2(h(v[0].x), h(v[0].y)), __hmax2(h(v[0].z), h(v[0].w)));
+#pragma unroll
+    for (int u = 1; u < U; ++u)
+      m = __hmax2(m, __hmax2(__hmax2(h(v[u].x), h(v[u].y)), __hmax2(h(v[u].z), h(v[u].w))));
+    const uint32_t w = *reinterpret_cast<const uint32_t *>(&m);
+    return fmaxf(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  }
   static __device__ __forceinline__ uint64_t pair(uint32_t w) {
     return pk2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   }
@@ -242,6 +342,13 @@ struct VecExp<__nv_bfloat16> {
 };
 template <>
 struct VecExp<float> {
+  template <int U>
+  static __device__ __forceinline__ float largest(const uint4 *v) {
+    float m = Elt<float>::vmax(v[0]);
+#pragma unroll
+    for (int u = 1; u < U; ++u) m = fmaxf(m, Elt<float>::vmax(v[u]));
+    return m;
+  }
   static __device__ __forceinline__ void ex2_pair(uint32_t x, uint32_t y, uint64_t c, uint64_t o,
                                                   float &a, float &b) {
     upk2(mul2(add2(pk2(__uint_as_float(x), __uint_as_float(y)), o), c), a, b);
@@ -282,9 +389,7 @@ struct ExpSum {
   // U vectors at once: one maximum, one rescaling
   template <int U>
   __device__ __forceinline__ void add(const uint4 *v, float c) {
-    float b = Elt<E>::vmax(v[0]);
-#pragma unroll
-    for (int u = 1; u < U; ++u) b = fmaxf(b, Elt<E>::vmax(v[u]));
+    const float b = VecExp<E>::template largest<U>(v);
     if (b > m) {
       z *= ex2((m - b) * c);
       m = b;
