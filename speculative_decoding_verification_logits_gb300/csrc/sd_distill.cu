@@ -30,8 +30,8 @@ constexpr int kDistNW = kDistNT / 32;
 constexpr int kDistU = 4;         // vectors at a time per thread
 
 constexpr int kStreamNT = 384;    // streamed rows: threads, two CTAs per SM
-constexpr int kStreamU = 4;       // vectors of a step per thread
-constexpr int kStreamD = 3;       // steps of the copy ring
+constexpr int kStreamU = 3;       // vectors of a step per thread
+constexpr int kStreamD = 4;       // steps of the copy ring
 
 struct DistParams {
   sd_distill_args a;
@@ -170,95 +170,131 @@ __device__ __forceinline__ void write_grad(uint8_t *out, const RowView<E> &row, 
 
 // GRAD: write the gradient; SAME: its rows lie on the 16-byte grid as the
 // student's do (whole vectors), otherwise they are written element by element.
+// Rows held on chip: cluster c takes rows c, c + clusters, ...; while it writes
+// one row's gradient, each vector's place is given to the next row at once.
 template <typename E, bool GRAD, bool SAME>
 __global__ void __launch_bounds__(kDistNT, kHeldCtas) sd_distill_kernel(const DistParams P) {
-  constexpr int VE = Elt<E>::kPerVec, NT = kDistNT, NW = kDistNW, U = kDistU;
+  constexpr int NT = kDistNT, NW = kDistNW, U = kDistU;
   const sd_distill_args &a = P.a;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  row_cluster_arrive();
   extern __shared__ uint4 held[];
   cg::cluster_group cluster = cg::this_cluster();
-  const int cs = P.cs, rank = (int)cluster.block_rank(), n = blockIdx.x / cs;
-  const int tid = threadIdx.x;
-  __shared__ DistStat stat[kHeldMaxCS];
+  const int cs = P.cs, rank = (int)cluster.block_rank();
+  const int tid = threadIdx.x, step = gridDim.x / cs;
+  __shared__ DistStat stat[2][kHeldMaxCS];
   __shared__ float wm[NW], wz[NW];
   __shared__ __align__(16) Named named;
   __shared__ Buckets buckets;
-  Held<E> H(a.student, (int64_t)n * a.student_s, a.V, rank, cs, held);
-  const float w = a.weight ? ld_float(a.weight + n) : 1.f;
-  uint8_t *out = GRAD ? (uint8_t *)a.grad + (int64_t)n * a.grad_s * Elt<E>::kSize : nullptr;
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  if (w == 0.f) {   // the same for every CTA of the row
-    if (GRAD)
-      for (int i = tid; i < H.n; i += NT) write_grad<E, SAME>(out, H.row, H.qa + i, zero);
-    if (a.loss && rank == 0 && tid == 0) a.loss[n] = 0.f;
-    return;
-  }
-  row_cluster_arrive();
-  H.template fetch<NT>();
-  // the named tokens: one per thread
-  int id = -1;
-  float t = neg_inf(), xs = neg_inf();
-  if (tid < a.k) {
-    id = ld_int(a.ids + (int64_t)n * a.k + tid);
-    t = ld_float(a.vals + (int64_t)n * a.k + tid);
-  }
-  const float rest = a.rest ? ld_float(a.rest + n) : neg_inf();
-  bool bad = id < -1 || id >= a.V;
-  const bool is = id >= 0 && !bad;
-  if (is) xs = Row<E>::load(H.row.row, id);
-  if (tid < SD_MAX_TOP) {
-    named.id[tid] = is ? id : -1;
-    named.t[tid] = t;
-    named.x[tid] = xs;
-  }
-  cp_wait<0>();
-  __syncthreads();   // the share and the named tokens are there
-  const int at = is ? H.place(id) : -1;
-  if (at >= 0) {
-    if (VE == 8) reinterpret_cast<uint16_t *>(held)[at] = 0xff80u;
-    else reinterpret_cast<uint32_t *>(held)[at] = 0xff800000u;
-  }
-  if (is)   // named before?
-    for (int i = 0; i < tid; i += 4) {
-      const int4 o = *reinterpret_cast<const int4 *>(named.id + i);
-      bad |= o.x == id || (o.y == id && i + 1 < tid) || (o.z == id && i + 2 < tid) ||
-             (o.w == id && i + 3 < tid);
-    }
-  bad = __syncthreads_or(bad) != 0;
-
-  // pass 1: the others' largest logit and sum
   const float c2 = log2e_over(a.T);
-  ExpSum<E> sum;
-  sum.template add_share<NT, U>(held, H.n, c2);
-  sum.template block<NW>(c2, wm, wz);
-  row_cluster_wait();
-  if (tid < cs) {
-    DistStat *s = cluster.map_shared_rank(&stat[rank], tid);
-    s->m = sum.m;
-    s->z = sum.z;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  auto share = [&](int n) {
+    return Held<E>(a.student, (int64_t)n * a.student_s, a.V, rank, cs, smem_u32(held));
+  };
+  auto grad_row = [&](int n) { return (uint8_t *)a.grad + (int64_t)n * a.grad_s * Elt<E>::kSize; };
+  // the first row from n on whose weight is not zero; the others are done with
+  float w_next = 1.f;
+  auto counting = [&](int n) {
+    for (; n < a.N; n += step) {
+      w_next = a.weight ? ld_float(a.weight + n) : 1.f;
+      if (w_next != 0.f) break;
+      if (GRAD) {
+        const Held<E> H = share(n);
+        for (int i = tid; i < H.n; i += NT) write_grad<E, SAME>(grad_row(n), H.row, H.qa + i, zero);
+      }
+      if (a.loss && rank == 0 && tid == 0) a.loss[n] = 0.f;
+    }
+    return n;
+  };
+  int id_next = -1;
+  float t_next = neg_inf(), rest_next = neg_inf();
+  auto ahead = [&](int n) {
+    if (n >= a.N) return;
+    if (tid < a.k) {
+      id_next = ld_int(a.ids + (int64_t)n * a.k + tid);
+      t_next = ld_float(a.vals + (int64_t)n * a.k + tid);
+    }
+    if (a.rest) rest_next = ld_float(a.rest + n);
+  };
+  int n = counting(blockIdx.x / cs);
+  if (n < a.N) share(n).template fetch<NT>();
+  ahead(n);
+  row_cluster_wait();   // every CTA of the cluster has started
+  for (int turn = 0; n < a.N; turn ^= 1) {
+    const Held<E> H = share(n);
+    const int id = id_next;
+    const float t = t_next, w = w_next, rest = rest_next;
+    bool bad = id < -1 || id >= a.V;
+    const bool is = id >= 0 && !bad;
+    const float xs = is ? Row<E>::load(H.row.row, id) : neg_inf();
+    const int n_next = counting(n + step);
+    ahead(n_next);
+    if (tid < SD_MAX_TOP) {
+      named.id[tid] = is ? id : -1;
+      named.t[tid] = t;
+      named.x[tid] = xs;
+    }
+    cp_wait<0>();
+    __syncthreads();   // the share and the named tokens are there
+    const int at = is ? H.place(id) : -1;
+    if (at >= 0) H.clear(at);
+    if (is)   // named before?
+      for (int i = 0; i < tid; i += 4) {
+        const int4 o = *reinterpret_cast<const int4 *>(named.id + i);
+        bad |= o.x == id || (o.y == id && i + 1 < tid) || (o.z == id && i + 2 < tid) ||
+               (o.w == id && i + 3 < tid);
+      }
+    bad = __syncthreads_or(bad) != 0;
+
+    // pass 1: the others' largest logit and sum
+    ExpSum<E> sum;
+    sum.template add_share<NT, U>(H, c2);
+    sum.template block<NW>(c2, wm, wz);
+    if (tid < cs) {
+      DistStat *s = cluster.map_shared_rank(&stat[turn][rank], tid);
+      s->m = sum.m;
+      s->z = sum.z;
+    }
+    __syncwarp();
+    cluster_sync_aligned();
+    if (tid < 32) {
+      float m = neg_inf(), z = 0.f;
+      for (int r = 0; r < cs; ++r) exp_merge(m, z, stat[turn][r].m, stat[turn][r].z, c2);
+      dist_buckets(named, buckets, a.k, rest, a.T, c2, w, m, z, bad,
+                   a.loss && rank == 0 ? a.loss + n : nullptr);
+      if (bad && rank == 0 && tid == 0 && a.status) atomicOr(a.status, (int)SD_STATUS_BAD_TOKEN);
+    }
+    __syncthreads();
+    // pass 2, each place given to the next row as it is done with
+    const Held<E> H_next = share(min(n_next, a.N - 1));
+    const int n_fetch = n_next < a.N ? H_next.n : 0;
+    if (GRAD) {
+      uint8_t *out = grad_row(n);
+      const bool live = buckets.live != 0;
+      const float coef = live ? buckets.coef : 0.f;
+      const ExpBase B(buckets.m, c2);
+      const uint64_t ss = pk2(coef, coef);
+      uint8_t *to = out + (int64_t)H.row.first(H.qa) * Elt<E>::kSize;
+#pragma unroll 2
+      for (int i = tid; i < H.n; i += NT) {
+        uint4 v = H.get(i);
+        v = !live ? zero : !B.far ? VecExp<E>::template scaled<false>(v, B, ss)
+                                  : VecExp<E>::template scaled<true>(v, B, ss);
+        if (SAME && H.inner(i)) *reinterpret_cast<uint4 *>(to + (int64_t)i * 16) = v;
+        else write_grad<E, SAME>(out, H.row, H.qa + i, v);
+        if (i < n_fetch) H_next.fetch(i);
+      }
+      // a share of a row on another place of the grid may be a vector longer
+      for (int i = H.n + (tid - H.n % NT + NT) % NT; i < n_fetch; i += NT) H_next.fetch(i);
+      cp_commit();
+      __syncthreads();  // the named places are written over the pass above
+      if (live && at >= 0) Row<E>::store(out, id, named.g[tid]);
+    } else if (n_fetch > 0) {
+      H_next.template fetch<NT>();
+    }
+    n = n_next;
   }
-  cluster.sync();
-  if (tid < 32) {
-    float m = neg_inf(), z = 0.f;
-    for (int r = 0; r < cs; ++r) exp_merge(m, z, stat[r].m, stat[r].z, c2);
-    dist_buckets(named, buckets, a.k, rest, a.T, c2, w, m, z, bad,
-                 a.loss && rank == 0 ? a.loss + n : nullptr);
-    if (bad && rank == 0 && tid == 0 && a.status) atomicOr(a.status, (int)SD_STATUS_BAD_TOKEN);
-  }
-  if (!GRAD) return;
-  __syncthreads();
-  if (!buckets.live) {
-    for (int i = tid; i < H.n; i += NT) write_grad<E, SAME>(out, H.row, H.qa + i, zero);
-    return;
-  }
-  const uint64_t cc = pk2(c2, c2), mm = pk2(-buckets.m, -buckets.m),
-                 ss = pk2(buckets.coef, buckets.coef);
-#pragma unroll 4
-  for (int i = tid; i < H.n; i += NT)
-    write_grad<E, SAME>(out, H.row, H.qa + i, VecExp<E>::scaled(held[i], cc, mm, ss));
-  __syncthreads();  // the named places are written over the pass above
-  if (at >= 0) Row<E>::store(out, id, named.g[tid]);
 }
 
 // Many rows: one CTA per row, streamed once for the sum and, for the gradient,
@@ -268,7 +304,6 @@ __global__ void __launch_bounds__(kDistNT, kHeldCtas) sd_distill_kernel(const Di
 template <typename E, bool GRAD, bool SAME>
 __global__ void __launch_bounds__(kStreamNT, 2) sd_distill_stream_kernel(const DistParams P) {
   constexpr int VE = Elt<E>::kPerVec, NT = kStreamNT, NW = NT / 32, U = kStreamU;
-  static_assert(U == 4, "a warp's four words of vector bits are one load");
   const sd_distill_args &a = P.a;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -338,20 +373,15 @@ __global__ void __launch_bounds__(kStreamNT, 2) sd_distill_stream_kernel(const D
         for (int u = 0; u < U; ++u)
           if (first + u * 32 >= row.nvec) v[u] = make_uint4(inf, inf, inf, inf);
       }
-      const uint4 mark = *reinterpret_cast<const uint4 *>(vecs + (q >> 5) + (tid >> 5) * U);
-      if (mark.x | mark.y | mark.z | mark.w) {
-        const uint32_t w[U] = {mark.x, mark.y, mark.z, mark.w};
+      uint32_t w[U], any = 0u;
+#pragma unroll
+      for (int u = 0; u < U; ++u) any |= w[u] = vecs[(q >> 5) + (tid >> 5) * U + u];
+      if (any) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           if (!((w[u] >> (tid & 31)) & 1u)) continue;
           const int at = (first + u * 32) * VE;
-          const uint32_t hit = bits[at >> 5] >> (at & 31);
-          float f[VE];
-          Elt<E>::unpack(v[u], f);
-#pragma unroll
-          for (int e = 0; e < VE; ++e)
-            if ((hit >> e) & 1u) f[e] = neg_inf();
-          Row<E>::pack(f, v[u]);
+          v[u] = mask_vec<E>(v[u], ~(bits[at >> 5] >> (at & 31)) & ((1u << VE) - 1u));
         }
       }
       sum.template add<U>(v, c2);
@@ -361,10 +391,18 @@ __global__ void __launch_bounds__(kStreamNT, 2) sd_distill_stream_kernel(const D
       named.t[tid] = t;
       named.x[tid] = xs;
     }
-    sum.template block<NW>(c2, wm, wz);   // its barrier: the named tokens are there too
+    sum.warp(c2);
+    if ((tid & 31) == 0) {
+      wm[tid >> 5] = sum.m;
+      wz[tid >> 5] = sum.z;
+    }
+    __syncthreads();   // the warps' sums and the named tokens are there
     if (is) bits[at >> 5] = vecs[at / VE >> 5] = 0u;
     if (tid < 32) {
       const bool any = dup != 0;
+      sum.m = tid < NW ? wm[tid] : neg_inf();
+      sum.z = tid < NW ? wz[tid] : 0.f;
+      sum.warp(c2);
       dist_buckets(named, buckets, a.k, rest, a.T, c2, w, sum.m, sum.z, any,
                    a.loss ? a.loss + n : nullptr);
       if (tid == 0) {
@@ -378,16 +416,20 @@ __global__ void __launch_bounds__(kStreamNT, 2) sd_distill_stream_kernel(const D
     // pass 2
     const bool live = buckets.live != 0;
     const float coef = live ? buckets.coef : 0.f;
-    const uint64_t cc = pk2(c2, c2), mm = pk2(-buckets.m, -buckets.m), ss = pk2(coef, coef);
-    uint8_t *to = out + ((int64_t)Stream::at() * VE - row.hp) * Elt<E>::kSize;
-    for (int q = 0; q < row.nvec; q += Stream::kStep, to += Stream::kStep * 16) {
+    const ExpBase B(buckets.m, c2);
+    const uint64_t ss = pk2(coef, coef);
+    const int last = (row.nvec - 1) / Stream::kStep * Stream::kStep;
+    uint8_t *to = out + ((int64_t)(last + Stream::at()) * VE - row.hp) * Elt<E>::kSize;
+    for (int q = last; q >= 0; q -= Stream::kStep, to -= Stream::kStep * 16) {
       uint4 v[U];
       S.next(v);
 #pragma unroll
-      for (int u = 0; u < U; ++u) v[u] = live ? VecExp<E>::scaled(v[u], cc, mm, ss) : zero;
+      for (int u = 0; u < U; ++u)
+        v[u] = !live ? zero : !B.far ? VecExp<E>::template scaled<false>(v[u], B, ss)
+                                     : VecExp<E>::template scaled<true>(v[u], B, ss);
       if (SAME && q > 0 && q + Stream::kStep < row.nvec) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) *reinterpret_cast<uint4 *>(to + u * 512) = v[u];
+        for (int u = 0; u < U; ++u) __stcs(reinterpret_cast<uint4 *>(to + u * 512), v[u]);
       } else {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -440,7 +482,7 @@ static cudaError_t launch_distill(DistParams &P, cudaStream_t s) {
   static FuncAttrs attrs;
   attrs.apply((const void *)sd_distill_kernel<E, GRAD, SAME>, kHeldBytes + 16, true,
               "the distillation kernel");
-  return launch_held(sd_distill_kernel<E, GRAD, SAME>, P, P.a.N, P.cs, kDistNT, smem, s);
+  return launch_held(sd_distill_kernel<E, GRAD, SAME>, P, P.a.N, true, P.cs, kDistNT, smem, s);
 }
 
 template <typename E>

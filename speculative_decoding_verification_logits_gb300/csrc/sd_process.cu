@@ -44,38 +44,6 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t *w, int e0, int W) 
   return r & ((1u << VE) - 1u);
 }
 
-// Bytes of x picked by the selector's nibbles; 8 + i gives byte i's sign in
-// every bit.
-__device__ __forceinline__ uint32_t prmt(uint32_t x, uint32_t sel) {
-  uint32_t r;
-  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(x), "r"(sel));
-  return r;
-}
-
-// The words of vector v with -inf where its bit in `ok` is clear: four bits
-// are spread to the sign bits of four bytes by one multiply (the partial
-// products do not meet), which byte permutes then copy over a half or a word.
-template <typename E>
-__device__ __forceinline__ uint4 mask_vec(uint4 v, uint32_t ok) {
-  const uint32_t lo = ((ok & 15u) * 0x10204080u) & 0x80808080u;
-  uint32_t k0, k1, k2, k3;
-  if (Elt<E>::kPerVec == 8) {
-    const uint32_t hi = ((ok >> 4) * 0x10204080u) & 0x80808080u;
-    k0 = prmt(lo, 0x9988);
-    k1 = prmt(lo, 0xbbaa);
-    k2 = prmt(hi, 0x9988);
-    k3 = prmt(hi, 0xbbaa);
-  } else {
-    k0 = prmt(lo, 0x8888);
-    k1 = prmt(lo, 0x9999);
-    k2 = prmt(lo, 0xaaaa);
-    k3 = prmt(lo, 0xbbbb);
-  }
-  const uint32_t inf = Elt<E>::kNegInfWord;
-  return make_uint4((v.x & k0) | (inf & ~k0), (v.y & k1) | (inf & ~k1), (v.z & k2) | (inf & ~k2),
-                    (v.w & k3) | (inf & ~k3));
-}
-
 // VEC: rows move as 16-byte vectors (the output's rows lie on the same place
 // of the 16-byte grid as the input's); otherwise element by element.
 template <typename E, bool VEC>

@@ -85,6 +85,57 @@ struct Row<__nv_bfloat16> {
   }
 };
 
+// Bytes of x picked by the selector's nibbles; 8 + i gives byte i's sign in
+// every bit.
+__device__ __forceinline__ uint32_t prmt(uint32_t x, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(x), "r"(sel));
+  return r;
+}
+
+// The words of vector v with -inf where its bit in `ok` is clear: four bits
+// are spread to the sign bits of four bytes by one multiply (the partial
+// products do not meet), which byte permutes then copy over a half or a word.
+template <typename E>
+__device__ __forceinline__ uint4 mask_vec(uint4 v, uint32_t ok) {
+  const uint32_t lo = ((ok & 15u) * 0x10204080u) & 0x80808080u;
+  uint32_t k0, k1, k2, k3;
+  if (Elt<E>::kPerVec == 8) {
+    const uint32_t hi = ((ok >> 4) * 0x10204080u) & 0x80808080u;
+    k0 = prmt(lo, 0x9988);
+    k1 = prmt(lo, 0xbbaa);
+    k2 = prmt(hi, 0x9988);
+    k3 = prmt(hi, 0xbbaa);
+  } else {
+    k0 = prmt(lo, 0x8888);
+    k1 = prmt(lo, 0x9999);
+    k2 = prmt(lo, 0xaaaa);
+    k3 = prmt(lo, 0xbbbb);
+  }
+  const uint32_t inf = Elt<E>::kNegInfWord;
+  return make_uint4((v.x & k0) | (inf & ~k0), (v.y & k1) | (inf & ~k1), (v.z & k2) | (inf & ~k2),
+                    (v.w & k3) | (inf & ~k3));
+}
+
+// Shared memory by its 32-bit address.  The copy goes through L1 (.ca): past it
+// (.cg) every sector was counted twice between L2 and the SM (576 x 151936
+// bf16 rows read once: 352 MB instead of 177 MB).
+__device__ __forceinline__ void row_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t p) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(p));
+  return v;
+}
+__device__ __forceinline__ void sts16(uint32_t p, const uint4 &v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+
 // A row of n elements at `row`, hp elements into its 16-byte grid.
 template <typename E>
 struct RowView {
@@ -131,31 +182,47 @@ constexpr int kHeldMaxCS = 16;
 template <typename E>
 struct Held {
   RowView<E> row;
-  int qa, n;       // first vector and vectors of this CTA's share
-  uint4 *v;        // the share in shared memory, -inf outside the row
+  int qa, n;           // first vector and vectors of this CTA's share
+  int lo, hi;          // vectors [lo, hi) of the share lie wholly inside the row
+  const uint8_t *src;  // vector 0 of the share in memory (if it lies inside the row)
+  uint32_t at;         // the share in shared memory, -inf outside the row
   __device__ __forceinline__ Held(const void *base, int64_t offset, int V, int rank, int cs,
-                                  uint4 *smem)
-      : row(base, offset, V), v(smem) {
+                                  uint32_t smem)
+      : row(base, offset, V), at(smem) {
     const int per = (row.nvec + cs - 1) / cs;
     qa = min(rank * per, row.nvec);
     n = min(per, row.nvec - qa);
+    lo = n > 0 && !row.whole(qa) ? 1 : 0;
+    hi = n > 0 && !row.whole(qa + n - 1) ? n - 1 : n;
+    src = row.row + (int64_t)row.first(qa) * Elt<E>::kSize;
+  }
+  __device__ __forceinline__ bool inner(int i) const {
+    return (unsigned)(i - lo) < (unsigned)(hi - lo);
+  }
+  __device__ __forceinline__ uint4 get(int i) const { return lds16(at + i * 16); }
+  // asks for vector i < n of the share
+  __device__ __forceinline__ void fetch(int i) const {
+    if (inner(i)) row_async16(at + i * 16, src + (int64_t)i * 16);
+    else sts16(at + i * 16, row.load(qa + i));
   }
   // asks for every vector of the share; each thread copies its own ones
   template <int NT>
-  __device__ __forceinline__ void fetch() {
-    for (int i = threadIdx.x; i < n; i += NT) {
-      const int q = qa + i;
-      if (row.whole(q))
-        cp_async16(smem_u32(v + i), row.row + (int64_t)row.first(q) * Elt<E>::kSize);
-      else
-        v[i] = row.load(q);
-    }
+  __device__ __forceinline__ void fetch() const {
+    for (int i = threadIdx.x; i < n; i += NT) fetch(i);
     cp_commit();
   }
   // the place of element e in the share, or -1
   __device__ __forceinline__ int place(int e) const {
-    const int at = e + row.hp - qa * RowView<E>::VE;
-    return at >= 0 && at < n * RowView<E>::VE ? at : -1;
+    const int p = e + row.hp - qa * RowView<E>::VE;
+    return p >= 0 && p < n * RowView<E>::VE ? p : -1;
+  }
+  // -inf at place p
+  __device__ __forceinline__ void clear(int p) const {
+    if (Elt<E>::kSize == 2)
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + p * 2), "h"((unsigned short)0xff80)
+                   : "memory");
+    else
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + p * 4), "r"(0xff800000u) : "memory");
   }
 };
 
@@ -174,14 +241,13 @@ static int held_cluster(int64_t N, int V, int NT, int *share_bytes) {
   return (int)cs;
 }
 
-// Launches fn(P) with one cluster of cs CTAs per row, as a programmatic
-// dependent of the stream's previous kernel.
+// Launches fn(P) with clusters of cs CTAs, as a programmatic dependent of the
+// stream's previous kernel: `clusters` of them or, where `resident`, no more
+// than the device holds at once (asked once per kernel, size and device).
 template <typename P>
-static cudaError_t launch_held(void (*fn)(const P), const P &params, int64_t N, int cs, int NT,
-                               int smem, cudaStream_t s) {
-  if (N * cs > INT32_MAX) return cudaErrorInvalidValue;
+static cudaError_t launch_held(void (*fn)(const P), const P &params, int64_t clusters,
+                               bool resident, int cs, int NT, int smem, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(N * cs), 1, 1);
   cfg.blockDim = dim3(NT, 1, 1);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
@@ -193,6 +259,36 @@ static cudaError_t launch_held(void (*fn)(const P), const P &params, int64_t N, 
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
+  if (resident) {
+    struct Entry {
+      const void *fn;
+      int dev, cs, smem, n;
+    };
+    static std::mutex mu;
+    static Entry cache[64];
+    static int used, at;
+    const int dev = current_device();
+    std::lock_guard<std::mutex> g(mu);
+    int n = 0;
+    for (int i = 0; i < used; ++i)
+      if (cache[i].fn == (const void *)fn && cache[i].dev == dev && cache[i].cs == cs &&
+          cache[i].smem == smem)
+        n = cache[i].n;
+    if (n == 0) {
+      cfg.gridDim = dim3((unsigned)cs, 1, 1);
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&n, (const void *)fn, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        n = 1;
+      }
+      cache[at] = Entry{(const void *)fn, dev, cs, smem, n};
+      at = (at + 1) % 64;
+      used = std::min(used + 1, 64);
+    }
+    clusters = std::min<int64_t>(clusters, n);
+  }
+  if (clusters * cs > INT32_MAX) return cudaErrorInvalidValue;
+  cfg.gridDim = dim3((unsigned)(clusters * cs), 1, 1);
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, fn, params);
 }
@@ -201,14 +297,15 @@ static cudaError_t launch_held(void (*fn)(const P), const P &params, int64_t N, 
 // One CTA takes rows first, first + grid, ... from end to end (each `passes`
 // times in a row).  Every thread copies its own vectors, U a step, into its
 // own places of a ring of D steps; the copies run on across the ends of
-// passes and rows, so that what happens there costs no bandwidth.  Rows of
+// passes and rows, so that what happens there costs no bandwidth.  The second
+// pass goes backwards: what L2 still holds of the row is its end.  Rows of
 // weight 0 are left out.  In a step a warp has 32 U vectors side by side:
 // its vector u of the step that begins at q is q + at() + 32 u.
 template <typename E, int NT, int U, int D>
 struct RowStream {
   static constexpr int kStep = NT * U;                  // vectors of a step
   static constexpr int kBytes = D * kStep * 16;
-  uint4 *ring;
+  uint32_t ring;        // this thread's place of the ring
   const void *base;
   const float *weight;
   int64_t stride;
@@ -222,7 +319,7 @@ struct RowStream {
   }
   __device__ __forceinline__ RowStream(uint4 *ring_, const void *base_, int64_t stride_, int N_,
                                        int V_, int passes_, const float *weight_)
-      : ring(ring_ + threadIdx.x), base(base_), weight(weight_), stride(stride_), N(N_), V(V_),
+      : ring(smem_u32(ring_ + threadIdx.x)), base(base_), weight(weight_), stride(stride_), N(N_), V(V_),
         passes(passes_), view(base_, 0, V_), row(blockIdx.x), put(0), take(0) {
     open();
 #pragma unroll 1
@@ -233,33 +330,31 @@ struct RowStream {
     if (weight)
       while (row < N && ld_float(weight + row) == 0.f) row += gridDim.x;
     if (row < N) view = RowView<E>(base, (int64_t)row * stride, V);
-    pass = 0;
-    rewind();
-  }
-  __device__ __forceinline__ void rewind() {
-    q = 0;
+    pass = q = 0;
     src = view.row + ((int64_t)at() * RowView<E>::VE - view.hp) * Elt<E>::kSize;
   }
   __device__ __forceinline__ void ask() {
-    uint4 *to = ring + put * kStep;
+    const uint32_t to = ring + put * (kStep * 16);
     if (row < N) {
       if (q > 0 && q + kStep < view.nvec) {   // no end of the row in the step
 #pragma unroll
-        for (int u = 0; u < U; ++u) cp_async16(smem_u32(to + u * NT), src + u * 512);
+        for (int u = 0; u < U; ++u) row_async16(to + u * (NT * 16), src + u * 512);
       } else {
 #pragma unroll 1
         for (int u = 0; u < U; ++u) {
           const int i = q + at() + u * 32;
           if (i >= view.nvec) break;
-          if (view.whole(i)) cp_async16(smem_u32(to + u * NT), src + u * 512);
-          else to[u * NT] = view.load(i);
+          if (view.whole(i)) row_async16(to + u * (NT * 16), src + u * 512);
+          else sts16(to + u * (NT * 16), view.load(i));
         }
       }
-      q += kStep;
-      src += kStep * 16;
-      if (q >= view.nvec) {
-        if (++pass < passes) {
-          rewind();
+      const int way = pass == 0 ? kStep : -kStep;
+      q += way;
+      src += (int64_t)way * 16;
+      if (q >= view.nvec || q < 0) {
+        if (++pass < passes) {   // back over the row, from the step just asked for
+          q -= kStep;
+          src -= kStep * 16;
         } else {
           row += gridDim.x;
           open();
@@ -272,9 +367,9 @@ struct RowStream {
   // the oldest step's vectors; asks for another one
   __device__ __forceinline__ void next(uint4 *v) {
     cp_wait<D - 2>();
-    const uint4 *from = ring + take * kStep;
+    const uint32_t from = ring + take * (kStep * 16);
 #pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = from[u * NT];
+    for (int u = 0; u < U; ++u) v[u] = lds16(from + u * (NT * 16));
     take = take + 1 == D ? 0 : take + 1;
     ask();
   }
@@ -282,15 +377,34 @@ struct RowStream {
   __device__ __forceinline__ uint4 peek(int ahead, int u) const {
     int slot = take + ahead;
     slot = slot >= D ? slot - D : slot;
-    return ring[slot * kStep + u * NT];
+    return lds16(ring + (slot * kStep + u * NT) * 16);
   }
 };
 
 // ------------------------------------------------- exponentials of vectors --
-// Per vector, with the offset and the scale as packed pairs: the sum of
-// 2^((x + o) c), and s 2^((x + o) c).  The offset is a logit and is taken off
-// before the scale goes on, so that rows of the type's lowest value (a mask's
-// stand-in for -inf) stay finite.
+// 2^((x - m) c) for the elements of vectors, in packed pairs: as 2^(x c - m c),
+// one fused operation, where m c is far from fp32's range, and with the
+// difference first where it is not (FAR: rows of the type's lowest value, a
+// mask's stand-in for -inf, stay finite).  Errors in m c are the same for
+// every term of a row.
+constexpr float kFar = 1e37f;
+struct ExpBase {
+  uint64_t o, c;   // FAR: (-m, c), else (-m c, c)
+  bool far;
+  __device__ __forceinline__ ExpBase(float m, float cc) {
+    const float s = m == neg_inf() ? 0.f : m;
+    far = fabsf(s * cc) > kFar;
+    const float b = far ? -s : -s * cc;
+    o = pk2(b, b);
+    c = pk2(cc, cc);
+  }
+  template <bool FAR>
+  __device__ __forceinline__ void pair(uint64_t x, float &a, float &b) const {
+    upk2(FAR ? mul2(add2(x, o), c) : fma2(x, c, o), a, b);
+    a = ex2(a);
+    b = ex2(b);
+  }
+};
 template <typename E>
 struct VecExp;
 template <>
@@ -306,34 +420,28 @@ struct VecExp<__nv_bfloat16> {
     const uint32_t w = *reinterpret_cast<const uint32_t *>(&m);
     return fmaxf(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   }
-  static __device__ __forceinline__ uint64_t pair(uint32_t w) {
+  static __device__ __forceinline__ uint64_t widen(uint32_t w) {
     return pk2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   }
-  static __device__ __forceinline__ void ex2_pair(uint32_t w, uint64_t c, uint64_t o, float &a,
-                                                  float &b) {
-    upk2(mul2(add2(pair(w), o), c), a, b);
-    a = ex2(a);
-    b = ex2(b);
-  }
-  static __device__ __forceinline__ uint64_t sum(const uint4 &v, uint64_t c, uint64_t o,
-                                                 uint64_t acc) {
+  template <bool FAR>
+  static __device__ __forceinline__ uint64_t sum(const uint4 &v, const ExpBase &B, uint64_t acc) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float a, b;
-      ex2_pair(w[i], c, o, a, b);
+      B.pair<FAR>(widen(w[i]), a, b);
       acc = add2(acc, pk2(a, b));
     }
     return acc;
   }
-  static __device__ __forceinline__ uint4 scaled(const uint4 &v, uint64_t c, uint64_t o,
-                                                 uint64_t s) {
+  template <bool FAR>
+  static __device__ __forceinline__ uint4 scaled(const uint4 &v, const ExpBase &B, uint64_t s) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t r[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float a, b;
-      ex2_pair(w[i], c, o, a, b);
+      B.pair<FAR>(widen(w[i]), a, b);
       upk2(mul2(pk2(a, b), s), a, b);
       r[i] = pack_bf16(a, b);
     }
@@ -349,25 +457,22 @@ struct VecExp<float> {
     for (int u = 1; u < U; ++u) m = fmaxf(m, Elt<float>::vmax(v[u]));
     return m;
   }
-  static __device__ __forceinline__ void ex2_pair(uint32_t x, uint32_t y, uint64_t c, uint64_t o,
-                                                  float &a, float &b) {
-    upk2(mul2(add2(pk2(__uint_as_float(x), __uint_as_float(y)), o), c), a, b);
-    a = ex2(a);
-    b = ex2(b);
+  static __device__ __forceinline__ uint64_t two(uint32_t x, uint32_t y) {
+    return pk2(__uint_as_float(x), __uint_as_float(y));
   }
-  static __device__ __forceinline__ uint64_t sum(const uint4 &v, uint64_t c, uint64_t o,
-                                                 uint64_t acc) {
+  template <bool FAR>
+  static __device__ __forceinline__ uint64_t sum(const uint4 &v, const ExpBase &B, uint64_t acc) {
     float a, b;
-    ex2_pair(v.x, v.y, c, o, a, b);
+    B.pair<FAR>(two(v.x, v.y), a, b);
     acc = add2(acc, pk2(a, b));
-    ex2_pair(v.z, v.w, c, o, a, b);
+    B.pair<FAR>(two(v.z, v.w), a, b);
     return add2(acc, pk2(a, b));
   }
-  static __device__ __forceinline__ uint4 scaled(const uint4 &v, uint64_t c, uint64_t o,
-                                                 uint64_t s) {
+  template <bool FAR>
+  static __device__ __forceinline__ uint4 scaled(const uint4 &v, const ExpBase &B, uint64_t s) {
     float f[4];
-    ex2_pair(v.x, v.y, c, o, f[0], f[1]);
-    ex2_pair(v.z, v.w, c, o, f[2], f[3]);
+    B.pair<FAR>(two(v.x, v.y), f[0], f[1]);
+    B.pair<FAR>(two(v.z, v.w), f[2], f[3]);
     upk2(mul2(pk2(f[0], f[1]), s), f[0], f[1]);
     upk2(mul2(pk2(f[2], f[3]), s), f[2], f[3]);
     uint4 r;
@@ -394,38 +499,45 @@ struct ExpSum {
       z *= ex2((m - b) * c);
       m = b;
     }
-    const float s = m == neg_inf() ? 0.f : -m;
-    const uint64_t c2 = pk2(c, c), s2 = pk2(s, s);
+    const ExpBase B(m, c);
     uint64_t acc = 0ull;
+    if (!B.far) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) acc = VecExp<E>::sum(v[u], c2, s2, acc);
+      for (int u = 0; u < U; ++u) acc = VecExp<E>::template sum<false>(v[u], B, acc);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) acc = VecExp<E>::template sum<true>(v[u], B, acc);
+    }
     float x, y;
     upk2(acc, x, y);
     z += x + y;
   }
   // this thread's vectors of a share: NT apart, U at a time
   template <int NT, int U>
-  __device__ __forceinline__ void add_share(const uint4 *held, int n, float c) {
+  __device__ __forceinline__ void add_share(const Held<E> &H, float c) {
     int i = threadIdx.x;
-    for (; i + (U - 1) * NT < n; i += U * NT) {
+    for (; i + (U - 1) * NT < H.n; i += U * NT) {
       uint4 v[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) v[u] = held[i + u * NT];
+      for (int u = 0; u < U; ++u) v[u] = H.get(i + u * NT);
       add<U>(v, c);
     }
-    for (; i < n; i += NT) {
-      const uint4 v = held[i];
+#pragma unroll 1
+    for (; i < H.n; i += NT) {
+      const uint4 v = H.get(i);
       add<1>(&v, c);
     }
+  }
+  // the warp's, in every lane
+  __device__ __forceinline__ void warp(float c) {
+    const float b = rmax_f(m);
+    z = warp_sum(z * ex2((m - (b == neg_inf() ? 0.f : b)) * c));
+    m = b;
   }
   // the block's, in every thread; wm and wz hold a float per warp
   template <int NW>
   __device__ __forceinline__ void block(float c, float *wm, float *wz) {
-#pragma unroll
-    for (int i = 16; i > 0; i >>= 1) {
-      const float m2 = __shfl_xor_sync(0xffffffffu, m, i), z2 = __shfl_xor_sync(0xffffffffu, z, i);
-      exp_merge(m, z, m2, z2, c);
-    }
+    warp(c);
     if ((threadIdx.x & 31) == 0) {
       wm[threadIdx.x >> 5] = m;
       wz[threadIdx.x >> 5] = z;

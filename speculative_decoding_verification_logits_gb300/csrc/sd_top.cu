@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kTopNT, kHeldCtas) sd_top_kernel(const TopPara
   __shared__ float red[NW], redz[NW];
   __shared__ unsigned long long kth, share;
   __shared__ int n_list;
-  Held<E> H(P.logits, (int64_t)n * P.stride, P.V, rank, cs, held);
+  Held<E> H(P.logits, (int64_t)n * P.stride, P.V, rank, cs, smem_u32(held));
   H.template fetch<NT>();
   const float c2 = log2e_over(P.T);
   cp_wait<0>();
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kTopNT, kHeldCtas) sd_top_kernel(const TopPara
   float m = neg_inf();
   int mi = -1;
   for (int i = tid; i < H.n; i += NT) {
-    const float x = Elt<E>::vmax(held[i]);
+    const float x = Elt<E>::vmax(H.get(i));
     if (x > m) {
       m = x;
       mi = i;
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kTopNT, kHeldCtas) sd_top_kernel(const TopPara
   auto reaching = [&](unsigned long long least_key, auto f) {
     const float bx = key_value(least_key);
     for (int i = tid; i < H.n; i += NT) {
-      const uint4 v = held[i];
+      const uint4 v = H.get(i);
       if (!(Elt<E>::vmax(v) >= bx)) continue;
       float x[VE];
       Elt<E>::unpack(v, x);
@@ -206,12 +206,9 @@ __global__ void __launch_bounds__(kTopNT, kHeldCtas) sd_top_kernel(const TopPara
     cluster.sync();
   }
   // the listed places leave the share, the rest is summed
-  reaching(bound, [&](unsigned long long, int at) {
-    if (VE == 8) reinterpret_cast<uint16_t *>(held)[at] = 0xff80u;
-    else reinterpret_cast<uint32_t *>(held)[at] = 0xff800000u;
-  });
+  reaching(bound, [&](unsigned long long, int at) { H.clear(at); });
   ExpSum<E> sum;
-  sum.template add_share<NT, kTopU>(held, H.n, c2);
+  sum.template add_share<NT, kTopU>(H, c2);
   sum.template block<NW>(c2, red, redz);
   if (tid == 0) *cluster.map_shared_rank(&sums[rank], 0) = make_float2(sum.m, sum.z);
   cluster.sync();
@@ -270,7 +267,7 @@ static cudaError_t launch_top(TopParams &P, cudaStream_t s) {
   smem = std::max(smem, 8 * kTopList);   // the row's list goes there
   static FuncAttrs attrs;
   attrs.apply((const void *)sd_top_kernel<E>, kHeldBytes + 16, true, "the top-logits kernel");
-  return launch_held(sd_top_kernel<E>, P, P.N, P.cs, kTopNT, smem, s);
+  return launch_held(sd_top_kernel<E>, P, P.N, false, P.cs, kTopNT, smem, s);
 }
 
 }  // namespace sdv
