@@ -29,9 +29,6 @@ constexpr int kDistNT = 256;
 constexpr int kDistNW = kDistNT / 32;
 constexpr int kDistU = 4;         // vectors at a time per thread
 
-constexpr int kStreamNT = 384;    // streamed rows: threads, two CTAs per SM
-constexpr int kStreamU = 3;       // vectors of a step per thread
-constexpr int kStreamD = 4;       // steps of the copy ring
 
 struct DistParams {
   sd_distill_args a;
@@ -170,131 +167,97 @@ __device__ __forceinline__ void write_grad(uint8_t *out, const RowView<E> &row, 
 
 // GRAD: write the gradient; SAME: its rows lie on the 16-byte grid as the
 // student's do (whole vectors), otherwise they are written element by element.
-// Rows held on chip: cluster c takes rows c, c + clusters, ...; while it writes
-// one row's gradient, each vector's place is given to the next row at once.
+// Few rows: one cluster per row, which holds it.
 template <typename E, bool GRAD, bool SAME>
 __global__ void __launch_bounds__(kDistNT, kHeldCtas) sd_distill_kernel(const DistParams P) {
   constexpr int NT = kDistNT, NW = kDistNW, U = kDistU;
   const sd_distill_args &a = P.a;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  row_cluster_arrive();
   extern __shared__ uint4 held[];
   cg::cluster_group cluster = cg::this_cluster();
-  const int cs = P.cs, rank = (int)cluster.block_rank();
-  const int tid = threadIdx.x, step = gridDim.x / cs;
-  __shared__ DistStat stat[2][kHeldMaxCS];
+  const int cs = P.cs, rank = (int)cluster.block_rank(), n = blockIdx.x / cs;
+  const int tid = threadIdx.x;
+  __shared__ DistStat stat[kHeldMaxCS];
   __shared__ float wm[NW], wz[NW];
   __shared__ __align__(16) Named named;
   __shared__ Buckets buckets;
   const float c2 = log2e_over(a.T);
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  auto share = [&](int n) {
-    return Held<E>(a.student, (int64_t)n * a.student_s, a.V, rank, cs, smem_u32(held));
-  };
-  auto grad_row = [&](int n) { return (uint8_t *)a.grad + (int64_t)n * a.grad_s * Elt<E>::kSize; };
-  // the first row from n on whose weight is not zero; the others are done with
-  float w_next = 1.f;
-  auto counting = [&](int n) {
-    for (; n < a.N; n += step) {
-      w_next = a.weight ? ld_float(a.weight + n) : 1.f;
-      if (w_next != 0.f) break;
-      if (GRAD) {
-        const Held<E> H = share(n);
-        for (int i = tid; i < H.n; i += NT) write_grad<E, SAME>(grad_row(n), H.row, H.qa + i, zero);
-      }
-      if (a.loss && rank == 0 && tid == 0) a.loss[n] = 0.f;
-    }
-    return n;
-  };
-  int id_next = -1;
-  float t_next = neg_inf(), rest_next = neg_inf();
-  auto ahead = [&](int n) {
-    if (n >= a.N) return;
-    if (tid < a.k) {
-      id_next = ld_int(a.ids + (int64_t)n * a.k + tid);
-      t_next = ld_float(a.vals + (int64_t)n * a.k + tid);
-    }
-    if (a.rest) rest_next = ld_float(a.rest + n);
-  };
-  int n = counting(blockIdx.x / cs);
-  if (n < a.N) share(n).template fetch<NT>();
-  ahead(n);
-  row_cluster_wait();   // every CTA of the cluster has started
-  for (int turn = 0; n < a.N; turn ^= 1) {
-    const Held<E> H = share(n);
-    const int id = id_next;
-    const float t = t_next, w = w_next, rest = rest_next;
-    bool bad = id < -1 || id >= a.V;
-    const bool is = id >= 0 && !bad;
-    const float xs = is ? Row<E>::load(H.row.row, id) : neg_inf();
-    const int n_next = counting(n + step);
-    ahead(n_next);
-    if (tid < SD_MAX_TOP) {
-      named.id[tid] = is ? id : -1;
-      named.t[tid] = t;
-      named.x[tid] = xs;
-    }
-    cp_wait<0>();
-    __syncthreads();   // the share and the named tokens are there
-    const int at = is ? H.place(id) : -1;
-    if (at >= 0) H.clear(at);
-    if (is)   // named before?
-      for (int i = 0; i < tid; i += 4) {
-        const int4 o = *reinterpret_cast<const int4 *>(named.id + i);
-        bad |= o.x == id || (o.y == id && i + 1 < tid) || (o.z == id && i + 2 < tid) ||
-               (o.w == id && i + 3 < tid);
-      }
-    bad = __syncthreads_or(bad) != 0;
-
-    // pass 1: the others' largest logit and sum
-    ExpSum<E> sum;
-    sum.template add_share<NT, U>(H, c2);
-    sum.template block<NW>(c2, wm, wz);
-    if (tid < cs) {
-      DistStat *s = cluster.map_shared_rank(&stat[turn][rank], tid);
-      s->m = sum.m;
-      s->z = sum.z;
-    }
-    __syncwarp();
-    cluster_sync_aligned();
-    if (tid < 32) {
-      float m = neg_inf(), z = 0.f;
-      for (int r = 0; r < cs; ++r) exp_merge(m, z, stat[turn][r].m, stat[turn][r].z, c2);
-      dist_buckets(named, buckets, a.k, rest, a.T, c2, w, m, z, bad,
-                   a.loss && rank == 0 ? a.loss + n : nullptr);
-      if (bad && rank == 0 && tid == 0 && a.status) atomicOr(a.status, (int)SD_STATUS_BAD_TOKEN);
-    }
-    __syncthreads();
-    // pass 2, each place given to the next row as it is done with
-    const Held<E> H_next = share(min(n_next, a.N - 1));
-    const int n_fetch = n_next < a.N ? H_next.n : 0;
-    if (GRAD) {
-      uint8_t *out = grad_row(n);
-      const bool live = buckets.live != 0;
-      const float coef = live ? buckets.coef : 0.f;
-      const ExpBase B(buckets.m, c2);
-      const uint64_t ss = pk2(coef, coef);
-      uint8_t *to = out + (int64_t)H.row.first(H.qa) * Elt<E>::kSize;
-#pragma unroll 2
-      for (int i = tid; i < H.n; i += NT) {
-        uint4 v = H.get(i);
-        v = !live ? zero : !B.far ? VecExp<E>::template scaled<false>(v, B, ss)
-                                  : VecExp<E>::template scaled<true>(v, B, ss);
-        if (SAME && H.inner(i)) *reinterpret_cast<uint4 *>(to + (int64_t)i * 16) = v;
-        else write_grad<E, SAME>(out, H.row, H.qa + i, v);
-        if (i < n_fetch) H_next.fetch(i);
-      }
-      // a share of a row on another place of the grid may be a vector longer
-      for (int i = H.n + (tid - H.n % NT + NT) % NT; i < n_fetch; i += NT) H_next.fetch(i);
-      cp_commit();
-      __syncthreads();  // the named places are written over the pass above
-      if (live && at >= 0) Row<E>::store(out, id, named.g[tid]);
-    } else if (n_fetch > 0) {
-      H_next.template fetch<NT>();
-    }
-    n = n_next;
+  const Held<E> H(a.student, (int64_t)n * a.student_s, a.V, rank, cs, smem_u32(held));
+  const float w = a.weight ? ld_float(a.weight + n) : 1.f;
+  uint8_t *out = GRAD ? (uint8_t *)a.grad + (int64_t)n * a.grad_s * Elt<E>::kSize : nullptr;
+  if (w == 0.f) {   // the same for every CTA of the row
+    if (GRAD)
+      for (int i = tid; i < H.n; i += NT) write_grad<E, SAME>(out, H.row, H.qa + i, zero);
+    if (a.loss && rank == 0 && tid == 0) a.loss[n] = 0.f;
+    return;
   }
+  row_cluster_arrive();
+  H.template fetch<NT>();
+  // the named tokens: one per thread
+  int id = -1;
+  float t = neg_inf(), xs = neg_inf();
+  if (tid < a.k) {
+    id = ld_int(a.ids + (int64_t)n * a.k + tid);
+    t = ld_float(a.vals + (int64_t)n * a.k + tid);
+  }
+  const float rest = a.rest ? ld_float(a.rest + n) : neg_inf();
+  bool bad = id < -1 || id >= a.V;
+  const bool is = id >= 0 && !bad;
+  if (is) xs = Row<E>::load(H.row.row, id);
+  if (tid < SD_MAX_TOP) {
+    named.id[tid] = is ? id : -1;
+    named.t[tid] = t;
+    named.x[tid] = xs;
+  }
+  cp_wait<0>();
+  __syncthreads();   // the share and the named tokens are there
+  const int at = is ? H.place(id) : -1;
+  if (at >= 0) H.clear(at);
+  if (is)   // named before?
+    for (int i = 0; i < tid; i += 4) {
+      const int4 o = *reinterpret_cast<const int4 *>(named.id + i);
+      bad |= o.x == id || (o.y == id && i + 1 < tid) || (o.z == id && i + 2 < tid) ||
+             (o.w == id && i + 3 < tid);
+    }
+  bad = __syncthreads_or(bad) != 0;
+
+  // pass 1: the others' largest logit and sum
+  ExpSum<E> sum;
+  sum.template add_share<NT, U>(H, c2);
+  sum.template block<NW>(c2, wm, wz);
+  row_cluster_wait();   // every CTA of the cluster has started
+  if (tid < cs) {
+    DistStat *s = cluster.map_shared_rank(&stat[rank], tid);
+    s->m = sum.m;
+    s->z = sum.z;
+  }
+  cluster.sync();
+  if (tid < 32) {
+    float m = neg_inf(), z = 0.f;
+    for (int r = 0; r < cs; ++r) exp_merge(m, z, stat[r].m, stat[r].z, c2);
+    dist_buckets(named, buckets, a.k, rest, a.T, c2, w, m, z, bad,
+                 a.loss && rank == 0 ? a.loss + n : nullptr);
+    if (bad && rank == 0 && tid == 0 && a.status) atomicOr(a.status, (int)SD_STATUS_BAD_TOKEN);
+  }
+  if (!GRAD) return;
+  __syncthreads();
+  const bool live = buckets.live != 0;
+  const float coef = live ? buckets.coef : 0.f;
+  const ExpBase B(buckets.m, c2);
+  const uint64_t ss = pk2(coef, coef);
+  uint8_t *to = out + (int64_t)H.row.first(H.qa) * Elt<E>::kSize;
+#pragma unroll 4
+  for (int i = tid; i < H.n; i += NT) {
+    uint4 v = H.get(i);
+    v = !live ? zero : !B.far ? VecExp<E>::template scaled<false>(v, B, ss)
+                              : VecExp<E>::template scaled<true>(v, B, ss);
+    if (SAME && H.inner(i)) *reinterpret_cast<uint4 *>(to + (int64_t)i * 16) = v;
+    else write_grad<E, SAME>(out, H.row, H.qa + i, v);
+  }
+  __syncthreads();  // the named places are written over the pass above
+  if (live && at >= 0) Row<E>::store(out, id, named.g[tid]);
 }
 
 // Many rows: one CTA per row, streamed once for the sum and, for the gradient,
@@ -450,39 +413,25 @@ __global__ void __launch_bounds__(kStreamNT, 2) sd_distill_stream_kernel(const D
 }
 
 template <typename E, bool GRAD, bool SAME>
-static cudaError_t launch_distill_stream(DistParams &P, cudaStream_t s) {
+static cudaError_t launch_distill(DistParams &P, cudaStream_t s) {
+  int smem = 0;
+  P.cs = held_cluster<E>(P.a.N, P.a.V, kDistNT, &smem);
+  if (P.cs > 0) {
+    static FuncAttrs attrs;
+    attrs.apply((const void *)sd_distill_kernel<E, GRAD, SAME>, kHeldBytes + 16, true,
+                "the distillation kernel");
+    return launch_held(sd_distill_kernel<E, GRAD, SAME>, P, P.a.N, P.cs, kDistNT, smem, s);
+  }
   constexpr int VE = Elt<E>::kPerVec;
   using Stream = RowStream<E, kStreamNT, kStreamU, kStreamD>;
   const int64_t nvec = ((int64_t)P.a.V + 2 * VE - 2) / VE;
   P.vec_words = (int)((nvec + Stream::kStep - 1) / Stream::kStep * (Stream::kStep / 32));
   P.bit_words = (int)((nvec * VE + 31) / 32);
   static FuncAttrs attrs;
-  attrs.apply((const void *)sd_distill_stream_kernel<E, GRAD, SAME>, 220 * 1024, false,
+  attrs.apply((const void *)sd_distill_stream_kernel<E, GRAD, SAME>, 200 * 1024, false,
               "the distillation kernel");
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min(P.a.N, 2 * sm_count()), 1, 1);
-  cfg.blockDim = dim3(kStreamNT, 1, 1);
-  cfg.dynamicSmemBytes = (size_t)Stream::kBytes + 4 * (size_t)(P.vec_words + P.bit_words);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sd_distill_stream_kernel<E, GRAD, SAME>, (const DistParams)P);
-}
-
-template <typename E, bool GRAD, bool SAME>
-static cudaError_t launch_distill(DistParams &P, cudaStream_t s) {
-  const int mode = env_int("SDL_STREAM", -1);
-  if (mode != 0 && (mode > 0 || P.a.N >= 2 * sm_count()))
-    return launch_distill_stream<E, GRAD, SAME>(P, s);
-  int smem = 0;
-  P.cs = held_cluster<E>(P.a.N, P.a.V, kDistNT, &smem);
-  static FuncAttrs attrs;
-  attrs.apply((const void *)sd_distill_kernel<E, GRAD, SAME>, kHeldBytes + 16, true,
-              "the distillation kernel");
-  return launch_held(sd_distill_kernel<E, GRAD, SAME>, P, P.a.N, true, P.cs, kDistNT, smem, s);
+  return launch_streamed(sd_distill_stream_kernel<E, GRAD, SAME>, P, P.a.N, kStreamNT,
+                         Stream::kBytes + 4 * (P.vec_words + P.bit_words), s);
 }
 
 template <typename E>

@@ -170,14 +170,14 @@ struct RowView {
 };
 
 // -------------------------------------------------- rows held on chip --
-// A cluster of cs CTAs holds a row in shared memory, each CTA a contiguous
-// share of its vectors, so that the row is read from memory once however
-// often it is used.  (Read again through L2, a row's second pass came from
-// DRAM: the rows in flight and what is written for them exceed L2.)  Three
-// CTAs per SM: while one computes or writes, the others' copies are under way.
+// For few rows, where latency counts: a cluster of cs CTAs holds a row in
+// shared memory, each CTA a contiguous share of its vectors.
 constexpr int kHeldCtas = 3;
 constexpr int kHeldBytes = 66000;   // largest share: three of them and static arrays per SM
 constexpr int kHeldMaxCS = 16;
+constexpr int kStreamNT = 384;      // streamed rows: threads, two CTAs per SM
+constexpr int kStreamU = 3;         // vectors of a step per thread
+constexpr int kStreamD = 4;         // steps of the copy ring
 
 template <typename E>
 struct Held {
@@ -226,28 +226,29 @@ struct Held {
   }
 };
 
-// The cluster size for N rows of V elements: the fewest CTAs that hold a row,
-// more where N rows would leave SMs without their CTAs (down to two vectors
-// per thread).  0: a row does not fit.
+// The cluster size that holds rows of V elements, or 0 where N rows are so many
+// that streaming them is faster: eight CTAs per row (more for rows that need
+// them, fewer for short ones), while the device has room for all of them.
+// Measured for the loss and its gradient, us, held / streamed: 48 rows of
+// 128256 bf16 11.1 / 17.1, 76 rows 18.7 / 17.2, 152 rows 26.1 / 17.6.
 template <typename E>
 static int held_cluster(int64_t N, int V, int NT, int *share_bytes) {
   constexpr int VE = Elt<E>::kPerVec;
   const int64_t nvec = ((int64_t)V + 2 * VE - 2) / VE;
-  int64_t cs = (nvec * 16 + kHeldBytes - 1) / kHeldBytes;
-  if (cs > kHeldMaxCS) return 0;
-  const int64_t slots = (int64_t)kHeldCtas * sm_count();
-  while (cs < 8 && N * (cs + 1) <= slots && nvec / (cs + 1) >= 2 * NT) ++cs;
+  int64_t cs = (nvec * 16 + kHeldBytes - 1) / kHeldBytes;   // at most 16: 1 MB + 16 bytes
+  if (N * std::max<int64_t>(cs, 8) > (int64_t)kHeldCtas * sm_count()) return 0;
+  while (cs < 8 && nvec / (cs + 1) >= 2 * NT) ++cs;
   *share_bytes = (int)((nvec + cs - 1) / cs * 16);
   return (int)cs;
 }
 
-// Launches fn(P) with clusters of cs CTAs, as a programmatic dependent of the
-// stream's previous kernel: `clusters` of them or, where `resident`, no more
-// than the device holds at once (asked once per kernel, size and device).
+// Launches fn(P) with N clusters of cs CTAs, as a programmatic dependent of the
+// stream's previous kernel.
 template <typename P>
-static cudaError_t launch_held(void (*fn)(const P), const P &params, int64_t clusters,
-                               bool resident, int cs, int NT, int smem, cudaStream_t s) {
+static cudaError_t launch_held(void (*fn)(const P), const P &params, int N, int cs, int NT,
+                               int smem, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(N * cs), 1, 1);
   cfg.blockDim = dim3(NT, 1, 1);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
@@ -259,42 +260,29 @@ static cudaError_t launch_held(void (*fn)(const P), const P &params, int64_t clu
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  if (resident) {
-    struct Entry {
-      const void *fn;
-      int dev, cs, smem, n;
-    };
-    static std::mutex mu;
-    static Entry cache[64];
-    static int used, at;
-    const int dev = current_device();
-    std::lock_guard<std::mutex> g(mu);
-    int n = 0;
-    for (int i = 0; i < used; ++i)
-      if (cache[i].fn == (const void *)fn && cache[i].dev == dev && cache[i].cs == cs &&
-          cache[i].smem == smem)
-        n = cache[i].n;
-    if (n == 0) {
-      cfg.gridDim = dim3((unsigned)cs, 1, 1);
-      cfg.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&n, (const void *)fn, &cfg) != cudaSuccess || n < 1) {
-        cudaGetLastError();
-        n = 1;
-      }
-      cache[at] = Entry{(const void *)fn, dev, cs, smem, n};
-      at = (at + 1) % 64;
-      used = std::min(used + 1, 64);
-    }
-    clusters = std::min<int64_t>(clusters, n);
-  }
-  if (clusters * cs > INT32_MAX) return cudaErrorInvalidValue;
-  cfg.gridDim = dim3((unsigned)(clusters * cs), 1, 1);
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, fn, params);
 }
 
+// Launches fn(P) with two CTAs of NT threads per SM, or one per row.
+template <typename P>
+static cudaError_t launch_streamed(void (*fn)(const P), const P &params, int N, int NT, int smem,
+                                   cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min(N, 2 * sm_count()), 1, 1);
+  cfg.blockDim = dim3(NT, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, params);
+}
+
 // ------------------------------------------------------ rows streamed --
-// One CTA takes rows first, first + grid, ... from end to end (each `passes`
+// For many rows: one CTA takes rows first, first + grid, ... from end to end (each `passes`
 // times in a row).  Every thread copies its own vectors, U a step, into its
 // own places of a ring of D steps; the copies run on across the ends of
 // passes and rows, so that what happens there costs no bandwidth.  The second

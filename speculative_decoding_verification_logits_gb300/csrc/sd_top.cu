@@ -1,7 +1,7 @@
 // The top logits of each row and the log-sum-exp of all others: what a
 // teacher gives to a distillation step.
 //
-// One cluster of cs CTAs per row, which holds it in shared memory:
+// Few rows: one cluster of cs CTAs per row, which holds it in shared memory:
 //  1. every thread keeps the best logit of its own vectors; threads side by
 //     side form groups.  The k-th best of a set of groups' maxima bounds the
 //     k-th best logit from below: k groups hold a logit at least as good.  Two
@@ -260,14 +260,244 @@ __global__ void __launch_bounds__(kTopNT, kHeldCtas) sd_top_kernel(const TopPara
   cluster.sync();  // the lists stay until rank 0 has read them
 }
 
+// Many rows: one CTA per row, streamed once.  The bound comes from the
+// threads' best logits so far (k of them at or above it) and is raised as the
+// row goes by: before the first step, from all the steps in the copy ring,
+// and whenever the row has grown by half since.  What reaches it goes to a
+// list, the rest into the sum.  At the row's end the bound from all of the
+// row leaves little more than k of the list; these are ranked, the others'
+// exponentials are added as integers (fixed point below the largest of them:
+// no order changes the sum).  A row that overflows the list (its large logits
+// at its end, or in a few threads' places) is gone over again from memory.
+constexpr int kTopHeap = 2048;     // listed logits of a streamed row
+constexpr float kLowest = -3.402823466e38f;
+
+// The largest value (of the upper 16 bits' grid) that k threads' `best` reach.
+__device__ __forceinline__ float top_bound(float best, int k) {
+  const unsigned key = ((unsigned)ford(best) ^ 0x80000000u) >> 16;
+  unsigned r = 0u;
+#pragma unroll 1
+  for (int bit = 15; bit >= 0; --bit) {
+    const unsigned t = r | (1u << bit);
+    if (__syncthreads_count(key >= t) >= k) r = t;
+  }
+  // 0x007f is -inf's: fewer than k threads have a finite logit
+  return r > 0x007fu ? fdeord((int)((r << 16) ^ 0x80000000u)) : kLowest;
+}
+
+template <typename E>
+__global__ void __launch_bounds__(kStreamNT, 2) sd_top_stream_kernel(const TopParams P) {
+  constexpr int VE = Elt<E>::kPerVec, NT = kStreamNT, NW = NT / 32, U = kStreamU;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  using Stream = RowStream<E, NT, U, kStreamD>;
+  extern __shared__ uint4 ring[];
+  unsigned long long *heap = reinterpret_cast<unsigned long long *>(ring + Stream::kBytes / 16);
+  unsigned long long *kept = heap + kTopHeap;   // the listed ones that may be chosen, then ranked
+  __shared__ float wm[NW], wz[NW];
+  __shared__ unsigned long long less;           // the others' sum
+  __shared__ int n_heap, n_kept, less_max;
+  const int tid = threadIdx.x, lane = tid & 31, k = P.k;
+  const float c2 = log2e_over(P.T);
+  const uint32_t inf = Elt<E>::kNegInfWord;
+  Stream S(ring, P.logits, P.stride, P.N, P.V, 1, nullptr);
+  if (tid == 0) n_heap = 0;
+  for (int n = blockIdx.x; n < P.N; n += gridDim.x) {
+    const RowView<E> row(P.logits, (int64_t)n * P.stride, P.V);
+    // the best of what is in the ring
+    float best = neg_inf();
+    cp_wait<0>();
+#pragma unroll 1
+    for (int d = 0; d < kStreamD - 1; ++d)
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = d * Stream::kStep + Stream::at() + u * 32;
+        if (i < row.nvec) best = fmaxf(best, Elt<E>::vmax(S.peek(d, u)));
+      }
+    float bound = top_bound(best, k);
+    int raise = (kStreamD - 1) * Stream::kStep * 3 / 2;
+    ExpSum<E> sum;
+    for (int q = 0; q < row.nvec; q += Stream::kStep) {
+      uint4 v[U];
+      S.next(v);
+      const int first = q + Stream::at();
+      if (q + Stream::kStep > row.nvec) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (first + u * 32 >= row.nvec) v[u] = make_uint4(inf, inf, inf, inf);
+      }
+      const float m = VecExp<E>::template largest<U>(v);
+      best = fmaxf(best, m);
+      // without a bound yet, as soon as k threads have a finite logit
+      if (q >= raise || (bound == kLowest && __syncthreads_count(best > neg_inf()) >= k)) {
+        bound = top_bound(best, k);
+        raise = q + q / 2;
+      }
+      if (m >= bound) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (!(Elt<E>::vmax(v[u]) >= bound)) continue;
+          float f[VE];
+          Elt<E>::unpack(v[u], f);
+          const int e0 = row.first(first + u * 32);
+          uint32_t stay = (1u << VE) - 1u;
+#pragma unroll
+          for (int e = 0; e < VE; ++e)
+            if (f[e] >= bound) {
+              const int at = atomicAdd(&n_heap, 1);
+              if (at < kTopHeap) heap[at] = top_key(f[e], e0 + e);
+              stay &= ~(1u << e);
+            }
+          v[u] = mask_vec<E>(v[u], stay);
+        }
+      }
+      sum.template add<U>(v, c2);
+    }
+    // what may be chosen: at or above the bound from the whole row
+    bound = top_bound(best, k);   // its barriers: the list is complete
+    int total = n_heap;
+    if (tid == 0) {
+      n_kept = 0;
+      less = 0ull;
+      less_max = (int)0x80000000;
+    }
+    __syncthreads();
+    if (total <= kTopHeap) {
+      for (int i = tid; i < total; i += NT) {
+        const float x = key_value(heap[i]);
+        if (x >= bound) {
+          const int at = atomicAdd(&n_kept, 1);
+          if (at < kTopList) kept[at] = heap[i];
+        } else {
+          atomicMax(&less_max, ford(x));
+        }
+      }
+    }
+    __syncthreads();
+    if (total > kTopHeap || n_kept > kTopList) {
+      // over the row again: halve the range of keys until k .. kTopList of
+      // them reach its lower end (there are more than k logits here)
+      unsigned long long lo = top_key(kLowest, P.V), hi = ~0ull;
+      for (int step = 0; step < 64; ++step) {
+        const unsigned long long mid = lo + (hi - lo) / 2;
+        int here = 0;
+        for (int q = tid; q < row.nvec; q += NT) {
+          float f[VE];
+          Elt<E>::unpack(row.load(q), f);
+#pragma unroll
+          for (int e = 0; e < VE; ++e)
+            here += f[e] > neg_inf() && top_key(f[e], row.first(q) + e) >= mid;
+        }
+        __syncthreads();
+        if (tid == 0) n_heap = 0;
+        __syncthreads();
+        here = __reduce_add_sync(0xffffffffu, here);
+        if (lane == 0) atomicAdd(&n_heap, here);
+        __syncthreads();
+        if (n_heap < k) {
+          hi = mid;
+        } else {
+          lo = mid;
+          if (n_heap <= kTopList) break;
+        }
+      }
+      __syncthreads();
+      if (tid == 0) {
+        n_kept = 0;
+        less_max = (int)0x80000000;
+      }
+      __syncthreads();
+      sum = ExpSum<E>();
+      for (int q = tid; q < row.nvec; q += NT) {
+        uint4 v = row.load(q);
+        float f[VE];
+        Elt<E>::unpack(v, f);
+        uint32_t stay = (1u << VE) - 1u;
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          const unsigned long long key = top_key(f[e], row.first(q) + e);
+          if (f[e] > neg_inf() && key >= lo) {
+            const int at = atomicAdd(&n_kept, 1);
+            if (at < kTopList) kept[at] = key;
+            stay &= ~(1u << e);
+          }
+        }
+        v = mask_vec<E>(v, stay);
+        sum.template add<1>(&v, c2);
+      }
+      total = 0;   // the list is not looked at
+      __syncthreads();
+    }
+    // the others of the list
+    const float top_less = fdeord(less_max);
+    unsigned long long part = 0ull;
+    for (int i = tid; i < total; i += NT) {
+      const float x = key_value(heap[i]);
+      if (!(x >= bound)) part += (unsigned long long)(ex2((x - top_less) * c2) * 17592186044416.f);
+    }
+    if (part) atomicAdd(&less, part);
+    sum.warp(c2);
+    if (lane == 0) {
+      wm[tid >> 5] = sum.m;
+      wz[tid >> 5] = sum.z;
+    }
+    // ranks of those kept: the keys are distinct
+    const int nk = min(n_kept, kTopList);
+    constexpr int kPer = (kTopList + NT - 1) / NT;
+    unsigned long long mine[kPer];
+    int above[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = tid + j * NT;
+      above[j] = 0;
+      mine[j] = 0ull;
+      if (i < nk) {
+        mine[j] = kept[i];
+#pragma unroll 4
+        for (int o = 0; o < nk; ++o) above[j] += kept[o] > mine[j];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (tid + j * NT < nk) kept[above[j]] = mine[j];
+    if (tid == 0) n_heap = 0;
+    __syncthreads();
+    for (int i = tid; i < k; i += NT) {
+      const bool have = i < nk;
+      P.vals[(int64_t)n * k + i] = have ? key_value(kept[i]) : neg_inf();
+      P.ids[(int64_t)n * k + i] = have ? key_index(kept[i]) : -1;
+    }
+    if (P.rest && tid < 32) {
+      sum.m = tid < NW ? wm[tid] : neg_inf();
+      sum.z = tid < NW ? wz[tid] : 0.f;
+      sum.warp(c2);
+      // what is left of the ranked ones, and the others of the list
+      const float b = k < nk ? key_value(kept[k]) : neg_inf();
+      float z = 0.f;
+      for (int i = k + lane; i < nk; i += 32) z += ex2((key_value(kept[i]) - b) * c2);
+      z = warp_sum(z);
+      exp_merge(sum.m, sum.z, b, z, c2);
+      if (less) exp_merge(sum.m, sum.z, top_less, (float)less * (1.f / 17592186044416.f), c2);
+      if (lane == 0) P.rest[n] = sum.z == 0.f ? neg_inf() : sum.m / P.T + logf(sum.z);
+    }
+  }
+}
+
 template <typename E>
 static cudaError_t launch_top(TopParams &P, cudaStream_t s) {
   int smem = 0;
   P.cs = held_cluster<E>(P.N, P.V, kTopNT, &smem);
-  smem = std::max(smem, 8 * kTopList);   // the row's list goes there
+  if (P.cs > 0) {
+    smem = std::max(smem, 8 * kTopList);   // the row's list goes there
+    static FuncAttrs attrs;
+    attrs.apply((const void *)sd_top_kernel<E>, kHeldBytes + 16, true, "the top-logits kernel");
+    return launch_held(sd_top_kernel<E>, P, P.N, P.cs, kTopNT, smem, s);
+  }
+  smem = RowStream<E, kStreamNT, kStreamU, kStreamD>::kBytes + 8 * (kTopHeap + kTopList);
   static FuncAttrs attrs;
-  attrs.apply((const void *)sd_top_kernel<E>, kHeldBytes + 16, true, "the top-logits kernel");
-  return launch_held(sd_top_kernel<E>, P, P.N, false, P.cs, kTopNT, smem, s);
+  attrs.apply((const void *)sd_top_stream_kernel<E>, smem, false, "the top-logits kernel");
+  return launch_streamed(sd_top_stream_kernel<E>, P, P.N, kStreamNT, smem, s);
 }
 
 }  // namespace sdv

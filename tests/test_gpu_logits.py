@@ -322,7 +322,7 @@ def _check_top(x, k, T, dev, xd=None):
     return r
 
 
-TOP = [(1, 1, BF, 1), (2, 5, F32, 3), (3, 17, BF, 128), (4, 1000, BF, 7), (3, 4099, F32, 128),
+TOP = [(300, 151936, BF, 128), (100, 60007, F32, 64), (64, 1, BF, 2), (70, 17, F32, 128), (1, 1, BF, 1), (2, 5, F32, 3), (3, 17, BF, 128), (4, 1000, BF, 7), (3, 4099, F32, 128),
        (2, 50021, BF, 64), (1, 128256, BF, 128), (2, 262144, F32, 100), (40, 8191, BF, 33),
        (350, 9000, BF, 16), (7, 151936, BF, 1)]
 
@@ -352,8 +352,23 @@ def test_top_logits_shapes_of_rows(dev, dtype, k):
         torch.full((V,), torch.finfo(dtype).min),         # masked by the type's lowest value
         torch.where(i % 7 == 0, -0.0, 0.0),               # zeros of both signs are equal
     ]
-    _check_top(torch.stack(rows).to(dtype), k, 1.0, dev)
-    _check_top(torch.stack(rows[7:9] * 200).to(dtype)[:330], k, 2.0, dev)   # one CTA per row
+    rows.append(torch.where(i < V // 2, -math.inf, small))   # nothing in the first half
+    x = torch.stack(rows).to(dtype)
+    _check_top(x, k, 1.0, dev)
+    # many rows are taken differently: every copy of a row comes out as the definition's
+    vals, ids, rest = ref.top(x, k, 2.0)
+    r = sd.top_logits(x.to(dev).repeat(31, 1), k, temperature=2.0)
+    for b in range(31):
+        part = slice(b * len(rows), (b + 1) * len(rows))
+        assert torch.equal(r.ids[part].cpu(), ids) and torch.equal(r.vals[part].cpu(), vals)
+        assert torch.equal(r.rest[part], r.rest[:len(rows)])
+    for n, e in enumerate(rest):
+        got = float(r.rest[n])
+        if math.isinf(e):
+            assert got == float(e)
+        else:
+            tol = ref.rest_tolerance(float(e), float(vals[n, 0]), 2.0, V)
+            assert abs(got - float(e)) <= tol
 
 
 def test_top_logits_nan_and_inf(dev):
@@ -363,6 +378,9 @@ def test_top_logits_nan_and_inf(dev):
     x[2, 100:103] = -math.nan
     r = _check_top(x, 4, 1.0, dev)
     assert int(r.ids[1, 0]) == 5 and not bool(torch.isnan(r.vals).any())
+    many = sd.top_logits(x.to(dev).repeat(100, 1), 4)
+    assert torch.equal(many.ids, r.ids.repeat(100, 1)) and torch.equal(many.vals, r.vals.repeat(100, 1))
+    assert bool(torch.isnan(many.rest.view(100, 3)[:, 0]).all()) and bool(torch.isfinite(many.rest.view(100, 3)[:, 1]).all())
 
 
 def test_top_logits_views(dev):
@@ -424,6 +442,23 @@ def _check_distill(dev, x, ids, vals, rest, T, w):
 DISTILL = [(1, 1, F32, 1), (3, 2, BF, 1), (2, 17, F32, 20), (5, 1000, BF, 16), (4, 4099, BF, 128),
            (3, 4099, F32, 7), (2, 50021, BF, 64), (1, 128256, BF, 32), (2, 262144, F32, 100),
            (330, 5003, BF, 8), (2, 300, F32, 0)]
+
+
+def test_distill_many_rows(dev):
+    # batches that are streamed, several rows to a CTA where rows are short: every copy of
+    # a few rows against the definition (copies lie differently on the 16-byte grid)
+    for V, dtype, k, times in ((1, F32, 1, 131), (5003, BF, 128, 131), (40001, F32, 33, 131),
+                               (128256, BF, 64, 13)):
+        x, ids, vals, r, w = _distill_case(5, V, dtype, k, V, 1.5)
+        w[3] = 0.0
+        x[3, 0] = math.nan
+        more = lambda t: t.repeat(*((times,) + (1,) * (t.dim() - 1)))
+        want = [more(t) for t in _want_distill(x, ids, vals, r, 1.5, w)]
+        a = [more(t).to(dev) for t in (x, ids, vals, r, w)]
+        only = sd.distill_loss(*a[:4], temperature=1.5, weight=a[4])
+        loss, grad = sd.distill_grad(*a[:4], temperature=1.5, weight=a[4])
+        _near_distill(only, None, want)
+        _near_distill(loss, grad, want)
 
 
 @pytest.mark.parametrize("N,V,dtype,k", DISTILL)
