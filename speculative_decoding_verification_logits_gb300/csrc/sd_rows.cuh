@@ -479,10 +479,13 @@ template <typename E>
 struct ExpSum {
   float m, z;
   __device__ __forceinline__ ExpSum() : m(neg_inf()), z(0.f) {}
-  // U vectors at once: one maximum, one rescaling
+  // U vectors at once: one maximum (b), one rescaling
   template <int U>
   __device__ __forceinline__ void add(const uint4 *v, float c) {
-    const float b = VecExp<E>::template largest<U>(v);
+    add<U>(v, c, VecExp<E>::template largest<U>(v));
+  }
+  template <int U>
+  __device__ __forceinline__ void add(const uint4 *v, float c, float b) {
     if (b > m) {
       z *= ex2((m - b) * c);
       m = b;

@@ -263,26 +263,74 @@ __global__ void __launch_bounds__(kTopNT, kHeldCtas) sd_top_kernel(const TopPara
 // Many rows: one CTA per row, streamed once.  The bound comes from the
 // threads' best logits so far (k of them at or above it) and is raised as the
 // row goes by: before the first step, from all the steps in the copy ring,
-// and whenever the row has grown by half since.  What reaches it goes to a
-// list, the rest into the sum.  At the row's end the bound from all of the
-// row leaves little more than k of the list; these are ranked, the others'
-// exponentials are added as integers (fixed point below the largest of them:
-// no order changes the sum).  A row that overflows the list (its large logits
-// at its end, or in a few threads' places) is gone over again from memory.
-constexpr int kTopHeap = 2048;     // listed logits of a streamed row
+// and whenever what has gone by has doubled.  Vectors that hold what
+// reaches it go to a list (index and which places), those places are set to
+// -inf and the rest goes into the sum.  At the row's end the bound from all of
+// the row leaves little more than k logits of the list; these are ranked, the
+// others' exponentials are added as integers (fixed point below the largest
+// of them: no order changes the sum).  A row that overflows the list (its
+// large logits at its end, or in a few threads' places) is gone over again
+// from memory.
+constexpr int kTopHeap = 2048;     // listed vectors of a streamed row
 constexpr float kLowest = -3.402823466e38f;
 
-// The largest value (of the upper 16 bits' grid) that k threads' `best` reach.
-__device__ __forceinline__ float top_bound(float best, int k) {
-  const unsigned key = ((unsigned)ford(best) ^ 0x80000000u) >> 16;
-  unsigned r = 0u;
+// The largest value (of the upper 16 bits' grid) that k threads' `best` reach,
+// found by one warp bit by bit; kLowest where fewer have a finite logit.
+template <int NT>
+__device__ __forceinline__ float top_bound(float best, int k, unsigned short *keys, float *out) {
+  keys[threadIdx.x] = (unsigned short)(((unsigned)ford(best) ^ 0x80000000u) >> 16);
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    constexpr int J = NT / 32;
+    unsigned key[J], r = 0u;
+#pragma unroll
+    for (int j = 0; j < J; ++j) key[j] = keys[j * 32 + threadIdx.x];
 #pragma unroll 1
-  for (int bit = 15; bit >= 0; --bit) {
-    const unsigned t = r | (1u << bit);
-    if (__syncthreads_count(key >= t) >= k) r = t;
+    for (int bit = 15; bit >= 0; --bit) {
+      const unsigned t = r | (1u << bit);
+      int n = 0;
+#pragma unroll
+      for (int j = 0; j < J; ++j) n += key[j] >= t;
+      if (__reduce_add_sync(0xffffffffu, n) >= k) r = t;
+    }
+    // 0x007f is -inf's
+    if (threadIdx.x == 0) *out = r > 0x007fu ? fdeord((int)((r << 16) ^ 0x80000000u)) : kLowest;
   }
-  // 0x007f is -inf's: fewer than k threads have a finite logit
-  return r > 0x007fu ? fdeord((int)((r << 16) ^ 0x80000000u)) : kLowest;
+  __syncthreads();
+  return *out;
+}
+
+// The places of a vector that reach the bound (a value of the upper 16 bits'
+// grid, or kLowest), which become -inf.
+template <typename E>
+__device__ __forceinline__ uint32_t take_reaching(uint4 &v, float bound);
+template <>
+__device__ __forceinline__ uint32_t take_reaching<float>(uint4 &v, float bound) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w}, hit = 0u;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (__uint_as_float(w[e]) >= bound) {
+      hit |= 1u << e;
+      w[e] = 0xff800000u;
+    }
+  v = make_uint4(w[0], w[1], w[2], w[3]);
+  return hit;
+}
+template <>
+__device__ __forceinline__ uint32_t take_reaching<__nv_bfloat16>(uint4 &v, float bound) {
+  // bf16's lowest finite value stands for kLowest, which bf16 does not have
+  const uint32_t half = bound == kLowest ? 0xff7fu : __float_as_uint(bound) >> 16;
+  const uint32_t b2 = half * 0x00010001u;
+  uint32_t w[4] = {v.x, v.y, v.z, v.w}, hit = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const unsigned m = __hge2_mask(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]),
+                                   *reinterpret_cast<const __nv_bfloat162 *>(&b2));
+    w[i] = (w[i] & ~m) | (0xff80ff80u & m);
+    hit |= ((m & 1u) | ((m >> 15) & 2u)) << (2 * i);
+  }
+  v = make_uint4(w[0], w[1], w[2], w[3]);
+  return hit;
 }
 
 template <typename E>
@@ -292,10 +340,13 @@ __global__ void __launch_bounds__(kStreamNT, 2) sd_top_stream_kernel(const TopPa
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   using Stream = RowStream<E, NT, U, kStreamD>;
   extern __shared__ uint4 ring[];
-  unsigned long long *heap = reinterpret_cast<unsigned long long *>(ring + Stream::kBytes / 16);
-  unsigned long long *kept = heap + kTopHeap;   // the listed ones that may be chosen, then ranked
+  // logits that may be chosen, then ranked; the list (vector << 8 | places)
+  unsigned long long *kept = reinterpret_cast<unsigned long long *>(ring + Stream::kBytes / 16);
+  uint32_t *heap = reinterpret_cast<uint32_t *>(kept + kTopList);
+  __shared__ unsigned short keys[NT];
+  __shared__ float bound_s;
   __shared__ float wm[NW], wz[NW];
-  __shared__ unsigned long long less;           // the others' sum
+  __shared__ unsigned long long less[NW];       // the others' sum, a part per warp
   __shared__ int n_heap, n_kept, less_max;
   const int tid = threadIdx.x, lane = tid & 31, k = P.k;
   const float c2 = log2e_over(P.T);
@@ -314,8 +365,8 @@ __global__ void __launch_bounds__(kStreamNT, 2) sd_top_stream_kernel(const TopPa
         const int i = d * Stream::kStep + Stream::at() + u * 32;
         if (i < row.nvec) best = fmaxf(best, Elt<E>::vmax(S.peek(d, u)));
       }
-    float bound = top_bound(best, k);
-    int raise = (kStreamD - 1) * Stream::kStep * 3 / 2;
+    float bound = top_bound<NT>(best, k, keys, &bound_s);
+    int raise = (kStreamD - 1) * Stream::kStep * 2;
     ExpSum<E> sum;
     for (int q = 0; q < row.nvec; q += Stream::kStep) {
       uint4 v[U];
@@ -326,52 +377,61 @@ __global__ void __launch_bounds__(kStreamNT, 2) sd_top_stream_kernel(const TopPa
         for (int u = 0; u < U; ++u)
           if (first + u * 32 >= row.nvec) v[u] = make_uint4(inf, inf, inf, inf);
       }
-      const float m = VecExp<E>::template largest<U>(v);
+      float each[U], m = neg_inf();
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        each[u] = Elt<E>::vmax(v[u]);
+        m = fmaxf(m, each[u]);
+      }
       best = fmaxf(best, m);
-      // without a bound yet, as soon as k threads have a finite logit
       if (q >= raise || (bound == kLowest && __syncthreads_count(best > neg_inf()) >= k)) {
-        bound = top_bound(best, k);
-        raise = q + q / 2;
+        bound = top_bound<NT>(best, k, keys, &bound_s);
+        raise = 2 * q;
       }
       if (m >= bound) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          if (!(Elt<E>::vmax(v[u]) >= bound)) continue;
-          float f[VE];
-          Elt<E>::unpack(v[u], f);
-          const int e0 = row.first(first + u * 32);
-          uint32_t stay = (1u << VE) - 1u;
-#pragma unroll
-          for (int e = 0; e < VE; ++e)
-            if (f[e] >= bound) {
-              const int at = atomicAdd(&n_heap, 1);
-              if (at < kTopHeap) heap[at] = top_key(f[e], e0 + e);
-              stay &= ~(1u << e);
-            }
-          v[u] = mask_vec<E>(v[u], stay);
+          if (!(each[u] >= bound)) continue;
+          const uint32_t hit = take_reaching<E>(v[u], bound);
+          const int at = atomicAdd(&n_heap, 1);
+          if (at < kTopHeap) heap[at] = (uint32_t)(first + u * 32) << 8 | hit;
         }
+        m = VecExp<E>::template largest<U>(v);
       }
-      sum.template add<U>(v, c2);
+      sum.template add<U>(v, c2, m);
     }
     // what may be chosen: at or above the bound from the whole row
-    bound = top_bound(best, k);   // its barriers: the list is complete
+    bound = top_bound<NT>(best, k, keys, &bound_s);   // its barriers: the list is complete
     int total = n_heap;
     if (tid == 0) {
       n_kept = 0;
-      less = 0ull;
       less_max = (int)0x80000000;
     }
     __syncthreads();
-    if (total <= kTopHeap) {
+    // calls f(logit, its index) for the listed ones
+    auto listed = [&](auto f) {
       for (int i = tid; i < total; i += NT) {
-        const float x = key_value(heap[i]);
+        const int vec = (int)(heap[i] >> 8);
+        float x[VE];
+        Elt<E>::unpack(row.load(vec), x);
+#pragma unroll
+        for (int e = 0; e < VE; ++e)
+          if ((heap[i] >> e) & 1u) f(x[e], row.first(vec) + e);
+      }
+    };
+    if (total <= kTopHeap) {
+      int most = (int)0x80000000;
+      listed([&](float x, int i) {
         if (x >= bound) {
           const int at = atomicAdd(&n_kept, 1);
-          if (at < kTopList) kept[at] = heap[i];
+          if (at < kTopList) kept[at] = top_key(x, i);
         } else {
-          atomicMax(&less_max, ford(x));
+          most = max(most, ford(x));
         }
-      }
+      });
+      __syncwarp();
+      most = __reduce_max_sync(0xffffffffu, most);
+      if (lane == 0) atomicMax(&less_max, most);
     }
     __syncthreads();
     if (total > kTopHeap || n_kept > kTopList) {
@@ -431,15 +491,17 @@ __global__ void __launch_bounds__(kStreamNT, 2) sd_top_stream_kernel(const TopPa
     // the others of the list
     const float top_less = fdeord(less_max);
     unsigned long long part = 0ull;
-    for (int i = tid; i < total; i += NT) {
-      const float x = key_value(heap[i]);
+    listed([&](float x, int) {
       if (!(x >= bound)) part += (unsigned long long)(ex2((x - top_less) * c2) * 17592186044416.f);
-    }
-    if (part) atomicAdd(&less, part);
+    });
+    __syncwarp();
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
     sum.warp(c2);
     if (lane == 0) {
       wm[tid >> 5] = sum.m;
       wz[tid >> 5] = sum.z;
+      less[tid >> 5] = part;
     }
     // ranks of those kept: the keys are distinct
     const int nk = min(n_kept, kTopList);
@@ -478,7 +540,10 @@ __global__ void __launch_bounds__(kStreamNT, 2) sd_top_stream_kernel(const TopPa
       for (int i = k + lane; i < nk; i += 32) z += ex2((key_value(kept[i]) - b) * c2);
       z = warp_sum(z);
       exp_merge(sum.m, sum.z, b, z, c2);
-      if (less) exp_merge(sum.m, sum.z, top_less, (float)less * (1.f / 17592186044416.f), c2);
+      unsigned long long all = 0ull;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) all += less[i];
+      if (all) exp_merge(sum.m, sum.z, top_less, (float)all * (1.f / 17592186044416.f), c2);
       if (lane == 0) P.rest[n] = sum.z == 0.f ? neg_inf() : sum.m / P.T + logf(sum.z);
     }
   }
@@ -494,7 +559,7 @@ static cudaError_t launch_top(TopParams &P, cudaStream_t s) {
     attrs.apply((const void *)sd_top_kernel<E>, kHeldBytes + 16, true, "the top-logits kernel");
     return launch_held(sd_top_kernel<E>, P, P.N, P.cs, kTopNT, smem, s);
   }
-  smem = RowStream<E, kStreamNT, kStreamU, kStreamD>::kBytes + 8 * (kTopHeap + kTopList);
+  smem = RowStream<E, kStreamNT, kStreamU, kStreamD>::kBytes + 4 * kTopHeap + 8 * kTopList;
   static FuncAttrs attrs;
   attrs.apply((const void *)sd_top_stream_kernel<E>, smem, false, "the top-logits kernel");
   return launch_streamed(sd_top_stream_kernel<E>, P, P.N, kStreamNT, smem, s);
