@@ -16,7 +16,7 @@ from typing import NamedTuple
 
 import torch
 
-from . import _P, SD_BF16, SD_F32, _check, _need, _on_stream, lib
+from . import _P, SD_BF16, SD_F32, SD_OK, _check, _need, _on_stream, lib
 
 SD_STATUS_BAD_PENALTY = 0x8
 SD_MAX_TOP, SD_MAX_BIAS = 128, 1024
@@ -71,7 +71,13 @@ def _bind(L):
             raise RuntimeError(f"{mirror.__name__} layout differs between library and binding")
 
 
+# the current stream's handle by device index, without making a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_of(device):
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 
@@ -84,9 +90,21 @@ def _rows(t, name, dims):
         raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
     if t.dim() not in dims:
         raise ValueError(f"{name} has {t.dim()} dimensions, expected {' or '.join(map(str, dims))}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must have contiguous rows")
     return dt
+
+
+def _arg(t, name, dtype, shape, device):
+    """The address of a required array; what is wrong with it is said by _need."""
+    if t is None or t.dtype is not dtype or t.device != device or t.shape != shape \
+            or not t.is_contiguous():
+        _need(t, name, dtype, shape, device)
+    return t.data_ptr()
+
+
+def _opt(t, name, dtype, shape, device):
+    return None if t is None else _arg(t, name, dtype, shape, device)
 
 
 def _out_like(x, out, name):
@@ -101,10 +119,6 @@ def _out_like(x, out, name):
         1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))
     if x.numel() and out.data_ptr() < ends(x) and x.data_ptr() < ends(out):
         raise ValueError(f"{name} overlaps the input without being the same tensor")
-
-
-def _opt(t, name, dtype, shape, device):
-    return None if t is None else _need(t, name, dtype, shape, device).data_ptr()
 
 
 @_on_stream
