@@ -16,7 +16,7 @@ from typing import NamedTuple
 
 import torch
 
-from . import _P, SD_BF16, SD_F32, SD_OK, _check, _need, _on_stream, lib
+from . import _P, SD_BF16, SD_F32, _check, _need, _on_stream, lib
 
 SD_STATUS_BAD_PENALTY = 0x8
 SD_MAX_TOP, SD_MAX_BIAS = 128, 1024
@@ -75,6 +75,16 @@ def _bind(L):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+_loaded = None   # the library, once a call has needed it
+
+
+def _lib():
+    global _loaded
+    if _loaded is None:
+        _loaded = lib()
+    return _loaded
+
+
 def _stream_of(device):
     if _raw_stream is not None:
         return _raw_stream(device.index)
@@ -101,10 +111,6 @@ def _arg(t, name, dtype, shape, device):
             or not t.is_contiguous():
         _need(t, name, dtype, shape, device)
     return t.data_ptr()
-
-
-def _opt(t, name, dtype, shape, device):
-    return None if t is None else _arg(t, name, dtype, shape, device)
 
 
 def _out_like(x, out, name):
@@ -138,11 +144,13 @@ def token_counts(history, lengths, V: int, *, prompt_lengths=None, out=None, sta
         out = torch.empty((B, V), dtype=torch.int16, device=dev)
     else:
         _need(out, "out", torch.int16, (B, V), dev)
-    _check(lib().sd_token_counts(B, L, V, history.data_ptr(), lengths.data_ptr(),
-                                 _opt(prompt_lengths, "prompt_lengths", torch.int32, (B,), dev),
-                                 out.data_ptr(),
-                                 _opt(status, "status", torch.int32, (1,), dev),
-                                 _stream_of(dev)), "sd_token_counts")
+    prompt = st = None
+    if prompt_lengths is not None:
+        prompt = _arg(prompt_lengths, "prompt_lengths", torch.int32, (B,), dev)
+    if status is not None:
+        st = _arg(status, "status", torch.int32, (1,), dev)
+    _check(_lib().sd_token_counts(B, L, V, history.data_ptr(), lengths.data_ptr(), prompt,
+                                  out.data_ptr(), st, _stream_of(dev)), "sd_token_counts")
     return out
 
 
@@ -159,10 +167,10 @@ def token_counts_add(counts, tokens, n, *, status=None, stream=None) -> torch.Te
     if tokens.dim() != 2 or tokens.shape[0] != B:
         raise ValueError("tokens must be [B][M]")
     _need(n, "n", torch.int32, (B,), dev)
-    _check(lib().sd_token_counts_add(B, tokens.shape[1], V, tokens.data_ptr(), n.data_ptr(),
-                                     counts.data_ptr(),
-                                     _opt(status, "status", torch.int32, (1,), dev),
-                                     _stream_of(dev)), "sd_token_counts_add")
+    st = None if status is None else _arg(status, "status", torch.int32, (1,), dev)
+    _check(_lib().sd_token_counts_add(B, tokens.shape[1], V, tokens.data_ptr(), n.data_ptr(),
+                                      counts.data_ptr(), st, _stream_of(dev)),
+           "sd_token_counts_add")
     return counts
 
 
@@ -180,56 +188,57 @@ def process_logits(logits, *, counts=None, prev=None, base: int = 0, repetition=
     [B][R][ceil(V / 32)] or [B][ceil(V / 32)] int32, a set bit allows the
     token.  All are optional.  out may be the logits tensor itself."""
     dt = _rows(logits, "logits", (2, 3))
-    dev = logits.device
-    three = logits.dim() == 3
-    B, V = logits.shape[0], logits.shape[-1]
-    R = logits.shape[1] if three else 1
+    dev, shape = logits.device, logits.shape
+    B, V = shape[0], shape[-1]
+    R = shape[1] if len(shape) == 3 else 1
     if out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+        out = torch.empty(shape, dtype=logits.dtype, device=dev)
     else:
         _out_like(logits, out, "out")
-    P = 0
+    xs, ys = logits.stride(), out.stride()
+    a = ProcessArgs(B, R, V, dt, logits.data_ptr(), xs[0], xs[1] if len(xs) == 3 else 0,
+                    out.data_ptr(), ys[0], ys[1] if len(ys) == 3 else 0)
+    if counts is not None:
+        a.counts = _arg(counts, "counts", torch.int16, (B, V), dev)
     if prev is not None:
-        _need(prev, "prev", torch.int32, None, dev)
-        if prev.dim() != 2 or prev.shape[0] != B:
+        if prev.dim() != 2:
             raise ValueError("prev must be [B][P]")
         P = prev.shape[1]
-    if (bias_ids is None) != (bias_vals is None):
-        raise ValueError("bias_ids and bias_vals go together")
-    n_bias = 0
+        a.prev, a.P, a.base = _arg(prev, "prev", torch.int32, (B, P), dev), P, base
+    if repetition is not None:
+        a.repetition = _arg(repetition, "repetition", torch.float32, (B,), dev)
+    if presence is not None:
+        a.presence = _arg(presence, "presence", torch.float32, (B,), dev)
+    if frequency is not None:
+        a.frequency = _arg(frequency, "frequency", torch.float32, (B,), dev)
     if bias_ids is not None:
-        _need(bias_ids, "bias_ids", torch.int32, None, dev)
-        if bias_ids.dim() != 2 or bias_ids.shape[0] != B:
-            raise ValueError("bias_ids must be [B][n]")
-        n_bias = bias_ids.shape[1]
-        _need(bias_vals, "bias_vals", torch.float32, (B, n_bias), dev)
-    mb = mr = 0
+        if bias_vals is None or bias_ids.dim() != 2:
+            raise ValueError("bias_ids must be [B][n], with bias_vals")
+        n = bias_ids.shape[1]
+        ids = _arg(bias_ids, "bias_ids", torch.int32, (B, n), dev)
+        vals = _arg(bias_vals, "bias_vals", torch.float32, (B, n), dev)
+        if n:
+            a.bias_ids, a.bias_vals, a.n_bias = ids, vals, n
+    elif bias_vals is not None:
+        raise ValueError("bias_vals needs bias_ids")
     if mask is not None:
         if not mask.is_cuda or mask.device != dev or mask.dtype != torch.int32:
             raise ValueError(f"mask must be an int32 tensor on {dev}")
         W = (V + 31) // 32
-        shape = tuple(mask.shape)
-        if shape == (B, R, W):
-            mb, mr = mask.stride(0), mask.stride(1)
-        elif shape == (B, W):
-            mb = mask.stride(0)
+        ms = mask.stride()
+        if mask.shape == (B, R, W):
+            a.mask_sb, a.mask_sr = ms[0], ms[1]
+        elif mask.shape == (B, W):
+            a.mask_sb = ms[0]
         else:
-            raise ValueError(f"mask has shape {shape}, expected {(B, R, W)} or {(B, W)}")
-        if W > 1 and mask.stride(-1) != 1:
+            raise ValueError(f"mask has shape {tuple(mask.shape)}, expected {(B, R, W)} "
+                             f"or {(B, W)}")
+        if W > 1 and ms[-1] != 1:
             raise ValueError("mask must have contiguous rows")
-    a = ProcessArgs(B, R, V, dt, logits.data_ptr(), logits.stride(0),
-                    logits.stride(1) if three else 0, out.data_ptr(), out.stride(0),
-                    out.stride(1) if three else 0,
-                    _opt(counts, "counts", torch.int16, (B, V), dev),
-                    None if prev is None else prev.data_ptr(), P, int(base),
-                    _opt(repetition, "repetition", torch.float32, (B,), dev),
-                    _opt(presence, "presence", torch.float32, (B,), dev),
-                    _opt(frequency, "frequency", torch.float32, (B,), dev),
-                    bias_ids.data_ptr() if n_bias else None,
-                    bias_vals.data_ptr() if n_bias else None, n_bias,
-                    None if mask is None else mask.data_ptr(), mb, mr,
-                    _opt(status, "status", torch.int32, (1,), dev))
-    _check(lib().sd_process_logits(a, _stream_of(dev)), "sd_process_logits")
+        a.mask = mask.data_ptr()
+    if status is not None:
+        a.status = _arg(status, "status", torch.int32, (1,), dev)
+    _check(_lib().sd_process_logits(a, _stream_of(dev)), "sd_process_logits")
     return out
 
 
@@ -250,45 +259,48 @@ def top_logits(logits, k: int, *, temperature: float = 1.0, out: TopLogits | Non
     lowest index, -inf never chosen) and the log-sum-exp at `temperature` of
     the others: what distill_loss and distill_grad take of a teacher."""
     dt = _rows(logits, "logits", (2, 3))
-    dev = logits.device
+    dev, shape = logits.device, logits.shape
     N, stride = _row_stride(logits, "logits")
-    lead = tuple(logits.shape[:-1])
+    lead = shape[:-1]
+    kept = (*lead, k)
     if out is None:
-        out = TopLogits(torch.empty((*lead, k), dtype=torch.float32, device=dev),
-                        torch.empty((*lead, k), dtype=torch.int32, device=dev),
+        out = TopLogits(torch.empty(kept, dtype=torch.float32, device=dev),
+                        torch.empty(kept, dtype=torch.int32, device=dev),
                         torch.empty(lead, dtype=torch.float32, device=dev))
     else:
-        _need(out.vals, "out.vals", torch.float32, (*lead, k), dev)
-        _need(out.ids, "out.ids", torch.int32, (*lead, k), dev)
+        _need(out.vals, "out.vals", torch.float32, kept, dev)
+        _need(out.ids, "out.ids", torch.int32, kept, dev)
         _need(out.rest, "out.rest", torch.float32, lead, dev)
-    _check(lib().sd_top_logits(N, logits.shape[-1], dt, logits.data_ptr(), stride, int(k),
-                               float(temperature), out.vals.data_ptr(), out.ids.data_ptr(),
-                               out.rest.data_ptr(), _stream_of(dev)), "sd_top_logits")
+    _check(_lib().sd_top_logits(N, shape[-1], dt, logits.data_ptr(), stride, k, temperature,
+                                out.vals.data_ptr(), out.ids.data_ptr(), out.rest.data_ptr(),
+                                _stream_of(dev)), "sd_top_logits")
     return out
 
 
-def _distill(student, ids, vals, rest, temperature, weight, loss, grad, status):
+def _distill(student, ids, vals, rest, temperature, weight, status, loss, grad):
+    """sd_distill; loss and grad are checked where the caller gave them."""
     dt = _rows(student, "student", (2, 3))
-    dev = student.device
+    dev, shape = student.device, student.shape
     N, stride = _row_stride(student, "student")
-    lead = tuple(student.shape[:-1])
-    if ids.dim() != len(lead) + 1:
+    lead = shape[:-1]
+    if ids.dim() != len(shape):
         raise ValueError("ids must have the student's leading dimensions and k")
     k = ids.shape[-1]
-    _need(ids, "ids", torch.int32, (*lead, k), dev)
-    _need(vals, "vals", torch.float32, (*lead, k), dev)
-    gs = 0
+    kept = (*lead, k)
+    a = DistillArgs(N, shape[-1], k, dt, student.data_ptr(), stride,
+                    _arg(ids, "ids", torch.int32, kept, dev),
+                    _arg(vals, "vals", torch.float32, kept, dev))
+    if rest is not None:
+        a.rest = _arg(rest, "rest", torch.float32, lead, dev)
+    if weight is not None:
+        a.weight = _arg(weight, "weight", torch.float32, lead, dev)
+    a.T = temperature
+    a.loss = loss.data_ptr()
     if grad is not None:
-        if grad is not student:
-            _out_like(student, grad, "grad")
-        gs = _row_stride(grad, "grad")[1]
-    a = DistillArgs(N, student.shape[-1], k, dt, student.data_ptr(), stride, ids.data_ptr(),
-                    vals.data_ptr(), _opt(rest, "rest", torch.float32, lead, dev),
-                    _opt(weight, "weight", torch.float32, lead, dev), float(temperature),
-                    None if loss is None else loss.data_ptr(),
-                    None if grad is None else grad.data_ptr(), gs,
-                    _opt(status, "status", torch.int32, (1,), dev))
-    _check(lib().sd_distill(a, _stream_of(dev)), "sd_distill")
+        a.grad, a.grad_s = grad.data_ptr(), _row_stride(grad, "grad")[1]
+    if status is not None:
+        a.status = _arg(status, "status", torch.int32, (1,), dev)
+    _check(_lib().sd_distill(a, _stream_of(dev)), "sd_distill")
 
 
 @_on_stream
@@ -299,12 +311,12 @@ def distill_loss(student, ids, vals, rest=None, *, temperature: float = 1.0, wei
     the same temperature; without rest the named tokens hold all of the
     teacher's mass): weight times the divergence of the k named tokens and one
     bucket of all others.  Evaluation: reads the logits once."""
-    lead = tuple(student.shape[:-1])
+    lead = student.shape[:-1]
     if out is None:
         out = torch.empty(lead, dtype=torch.float32, device=student.device)
     else:
         _need(out, "out", torch.float32, lead, student.device)
-    _distill(student, ids, vals, rest, temperature, weight, out, None, status)
+    _distill(student, ids, vals, rest, temperature, weight, status, out, None)
     return out
 
 
@@ -315,9 +327,10 @@ def distill_grad(student, ids, vals, rest=None, *, temperature: float = 1.0, wei
     with respect to the student's logits, times `weight` (what reaches each
     row's loss from above: 1 / N for a mean).  grad may be the student tensor
     itself.  To train: student.backward(grad)."""
-    student = student.detach()
     loss = torch.empty(student.shape[:-1], dtype=torch.float32, device=student.device)
     if grad is None:
         grad = torch.empty(student.shape, dtype=student.dtype, device=student.device)
-    _distill(student, ids, vals, rest, temperature, weight, loss, grad, status)
+    elif grad is not student:
+        _out_like(student, grad, "grad")
+    _distill(student, ids, vals, rest, temperature, weight, status, loss, grad)
     return loss, grad
