@@ -2,18 +2,16 @@
 // teacher gives to a distillation step.
 //
 // Few rows: one cluster of cs CTAs per row, which holds it in shared memory:
-//  1. every thread keeps the best logit of its own vectors; threads side by
-//     side form groups.  The k-th best of a set of groups' maxima bounds the
-//     k-th best logit from below: k groups hold a logit at least as good.  Two
-//     such bounds are taken, the better one is used: the largest over the CTAs
-//     of each CTA's k-th best group, and the smallest over the CTAs of each
-//     CTA's ceil(k / cs)-th best.
+//  1. every thread keeps the best logit of its own vectors.  A value that k of
+//     them reach bounds the k-th best logit from below.  Two such bounds are
+//     taken, the better one is used: the largest over the CTAs of what k of
+//     their threads reach, and the smallest over the CTAs of what ceil(k / cs)
+//     of theirs reach.
 //  2. logits at or above the bound (little more than k of them where the
 //     large logits are spread over the row) go to a list and are set to -inf
-//     in the share, whose rest is summed: running (largest, sum of
-//     2^((x - largest) c)).  The first CTA ranks the list, writes the first k and
-//     adds what is left to the sum in rank order, so that nothing depends on
-//     the order in which the list was filled.
+//     in the share, whose rest is summed.  The first CTA ranks the list, writes
+//     the first k and adds what is left to the sum in rank order, so that
+//     nothing depends on the order in which the list was filled.
 // A row whose logits at the bound do not fit the list (large logits all in a
 // few groups) raises its bound first by halving the range of keys until at
 // least k and at most a list of logits are left.
@@ -29,6 +27,8 @@ constexpr int kTopNW = kTopNT / 32;
 constexpr int kTopU = 4;          // vectors at a time per thread
 constexpr int kTopList = 1024;    // listed logits of a row
 
+constexpr float kLowest = -3.402823466e38f;
+
 struct TopParams {
   const void *logits;
   int64_t stride;
@@ -39,10 +39,14 @@ struct TopParams {
   float *rest;
 };
 
-// What the CTAs of a row tell one another.
+// What the CTAs of a row tell one another: values that k and ceil(k / cs) of
+// their threads' best logits reach; what they listed, and the sum of the rest.
 struct TopStat {
-  unsigned long long kth, share;  // keys of the k-th and the ceil(k / cs)-th best group
-  float m;                        // largest logit
+  float kth, share;
+};
+struct TopSum {
+  float m, z;
+  int listed;
 };
 
 __device__ __forceinline__ unsigned long long top_key(float x, int i) {
@@ -51,6 +55,31 @@ __device__ __forceinline__ unsigned long long top_key(float x, int i) {
 __device__ __forceinline__ int key_index(unsigned long long key) { return (int)~(unsigned)key; }
 __device__ __forceinline__ float key_value(unsigned long long key) {
   return fdeord((int)((unsigned)(key >> 32) ^ 0x80000000u));
+}
+
+// The upper 16 bits of a value's ordered image.
+__device__ __forceinline__ unsigned short top_key16(float x) {
+  return (unsigned short)(((unsigned)ford(x) ^ 0x80000000u) >> 16);
+}
+
+// The largest value (of the upper 16 bits' grid) that k of NT keys reach, found
+// by one warp bit by bit; kLowest where fewer are finite.
+template <int NT>
+__device__ __forceinline__ float top_bound_warp(const unsigned short *keys, int k) {
+  constexpr int J = NT / 32;
+  unsigned key[J], r = 0u;
+#pragma unroll
+  for (int j = 0; j < J; ++j) key[j] = keys[j * 32 + (threadIdx.x & 31)];
+#pragma unroll 1
+  for (int bit = 15; bit >= 0; --bit) {
+    const unsigned t = r | (1u << bit);
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) n += key[j] >= t;
+    if (__reduce_add_sync(0xffffffffu, n) >= k) r = t;
+  }
+  // 0x007f is -inf's
+  return r > 0x007fu ? fdeord((int)((r << 16) ^ 0x80000000u)) : kLowest;
 }
 
 template <typename E>
@@ -63,81 +92,42 @@ __global__ void __launch_bounds__(kTopNT, kHeldCtas) sd_top_kernel(const TopPara
   cg::cluster_group cluster = cg::this_cluster();
   const int cs = P.cs, rank = (int)cluster.block_rank(), n = blockIdx.x / cs;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  __shared__ unsigned long long list[kTopList];    // the groups, then this CTA's listed keys
+  __shared__ unsigned long long list[kTopList];    // this CTA's listed keys
   __shared__ TopStat stat[kHeldMaxCS];
-  __shared__ float2 sums[kHeldMaxCS];
-  __shared__ int listed[kHeldMaxCS];
+  __shared__ TopSum sums[kHeldMaxCS];
   __shared__ int counted[2][kHeldMaxCS];
-  __shared__ float red[NW], redz[NW];
-  __shared__ unsigned long long kth, share;
+  __shared__ unsigned short keys[NT];
+  __shared__ float wm[NW], wz[NW];
   __shared__ int n_list;
-  Held<E> H(P.logits, (int64_t)n * P.stride, P.V, rank, cs, smem_u32(held));
+  const Held<E> H(P.logits, (int64_t)n * P.stride, P.V, rank, cs, smem_u32(held));
   H.template fetch<NT>();
   const float c2 = log2e_over(P.T);
+  if (tid == 0) n_list = 0;
   cp_wait<0>();
 
   // 1. the best logit of each thread's own vectors, which it copied itself
-  float m = neg_inf();
-  int mi = -1;
-  for (int i = tid; i < H.n; i += NT) {
-    const float x = Elt<E>::vmax(H.get(i));
-    if (x > m) {
-      m = x;
-      mi = i;
-    }
-  }
-  // keyed by the last index its vector could give: no better than the logit itself
-  unsigned long long key = mi >= 0 ? top_key(m, H.row.first(H.qa + mi) + VE - 1) : 0ull;
-  const int side = P.k > 64 ? 1 : P.k > 32 ? 2 : 4;   // threads of a group
-  for (int o = 1; o < side; o <<= 1) {
-    const unsigned long long other = __shfl_xor_sync(0xffffffffu, key, o);
-    key = other > key ? other : key;
-  }
-  const int groups = NT / side;
-  if (tid % side == 0) list[tid / side] = key;
-  m = warp_max(m);
-  if (lane == 0) red[warp] = m;
-  if (tid == 0) {
-    kth = share = 0ull;
-    n_list = 0;
-  }
-  __syncthreads();
-  const int ks = (P.k + cs - 1) / cs;
-  if (tid < groups) {
-    const unsigned long long g = list[tid];
-    int above = 0;
-#pragma unroll 4
-    for (int j = 0; j < groups; ++j) above += list[j] > g;
-    if (g != 0ull) {
-      if (above == P.k - 1) kth = g;
-      if (above == ks - 1) share = g;
-    }
-  }
-  float cm = neg_inf();
-#pragma unroll
-  for (int w = 0; w < NW; ++w) cm = fmaxf(cm, red[w]);
+  float best = neg_inf();
+  for (int i = tid; i < H.n; i += NT) best = fmaxf(best, Elt<E>::vmax(H.get(i)));
+  keys[tid] = top_key16(best);
   __syncthreads();
   row_cluster_wait();
-  if (tid < cs) {
-    TopStat *s = cluster.map_shared_rank(&stat[rank], tid);
-    s->kth = kth;
-    s->share = share;
-    s->m = cm;
+  if (warp < 2) {   // a warp for each of the two bounds
+    const float b = top_bound_warp<NT>(keys, warp == 0 ? P.k : (P.k + cs - 1) / cs);
+    if (lane < cs) {
+      TopStat *s = cluster.map_shared_rank(&stat[rank], lane);
+      if (warp == 0) s->kth = b;
+      else s->share = b;
+    }
   }
   cluster.sync();
-  unsigned long long bound = 0ull, least = ~0ull;
-  float M = neg_inf();
+  float bound = kLowest, least = INFINITY;
   for (int r = 0; r < cs; ++r) {
-    bound = stat[r].kth > bound ? stat[r].kth : bound;
-    least = stat[r].share < least ? stat[r].share : least;
-    M = fmaxf(M, stat[r].m);
+    bound = fmaxf(bound, stat[r].kth);
+    least = fminf(least, stat[r].share);
   }
-  bound = least > bound ? least : bound;
-  // nothing below every finite logit is ever chosen
-  const unsigned long long lowest = top_key(-3.402823466e38f, P.V);
-  bound = bound > lowest ? bound : lowest;
+  bound = fmaxf(bound, least);
 
-  // calls f(logit, key, vector, place) for what reaches the bound
+  // calls f(key, place) for what has at least this key
   auto reaching = [&](unsigned long long least_key, auto f) {
     const float bx = key_value(least_key);
     for (int i = tid; i < H.n; i += NT) {
@@ -148,78 +138,77 @@ __global__ void __launch_bounds__(kTopNT, kHeldCtas) sd_top_kernel(const TopPara
       const int e0 = H.row.first(H.qa + i);
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
-        const unsigned long long k = top_key(x[e], e0 + e);
-        if (x[e] >= bx && k >= least_key) f(k, i * VE + e);
+        const unsigned long long key = top_key(x[e], e0 + e);
+        if (x[e] >= bx && key >= least_key) f(key, i * VE + e);
       }
     }
   };
-  // how many reach it in the whole row
-  int step = 0;
-  auto count = [&](unsigned long long least_key) {
-    int here = 0;
-    reaching(least_key, [&](unsigned long long, int) { ++here; });
-    here = __reduce_add_sync(0xffffffffu, here);
-    if (tid == 0) n_list = 0;
-    __syncthreads();
-    if (lane == 0) atomicAdd(&n_list, here);
-    __syncthreads();
-    if (tid < cs) *cluster.map_shared_rank(&counted[step & 1][rank], tid) = n_list;
+  // 2. what reaches the bound is listed and leaves the share, whose rest is
+  // summed; every CTA learns of all lists and sums
+  auto list_and_sum = [&](unsigned long long least_key) {
+    reaching(least_key, [&](unsigned long long key, int at) {
+      const int i = atomicAdd(&n_list, 1);
+      if (i < kTopList) list[i] = key;
+      H.clear(at);
+    });
+    __syncwarp();
+    ExpSum<E> sum;
+    sum.template add_share<NT, kTopU>(H, c2);
+    sum.template block<NW>(c2, wm, wz);   // its barrier: the list is complete
+    if (tid < cs) {
+      TopSum *s = cluster.map_shared_rank(&sums[rank], tid);
+      s->m = sum.m;
+      s->z = sum.z;
+      s->listed = n_list;
+    }
     cluster.sync();
-    int all = 0;
-    for (int r = 0; r < cs; ++r) all += counted[step & 1][r];
-    ++step;
-    return all;
+    int total = 0;
+    for (int r = 0; r < cs; ++r) total += sums[r].listed;
+    return total;
   };
-  // 2. list what reaches the bound
-  __syncwarp();
-  reaching(bound, [&](unsigned long long k, int) {
-    const int at = atomicAdd(&n_list, 1);
-    if (at < kTopList) list[at] = k;
-  });
-  __syncthreads();
-  if (tid < cs) *cluster.map_shared_rank(&listed[rank], tid) = n_list;
-  cluster.sync();
-  int total = 0;
-  for (int r = 0; r < cs; ++r) total += listed[r];
+  // the bound as the lowest key of its value
+  int total = list_and_sum(top_key(bound, INT32_MAX));
   if (total > kTopList) {
-    // too many: halve the range of keys until k .. kTopList of them are left
-    unsigned long long lo = bound, hi = top_key(M, 0) + 1;  // more than a list, none
-    for (int i = 0; i < 64; ++i) {
+    // too many: from the row as it was, halve the range of keys until k ..
+    // kTopList of them reach its lower end
+    H.template fetch<NT>();
+    cp_wait<0>();
+    unsigned long long lo = top_key(bound, INT32_MAX), hi = ~0ull;  // more than a list, none
+    for (int step = 0; step < 64; ++step) {
       const unsigned long long mid = lo + (hi - lo) / 2;
-      const int c = count(mid);
-      if (c < P.k) {
+      int here = 0;
+      reaching(mid, [&](unsigned long long, int) { ++here; });
+      __syncwarp();
+      here = __reduce_add_sync(0xffffffffu, here);
+      __syncthreads();
+      if (tid == 0) n_list = 0;
+      __syncthreads();
+      if (lane == 0) atomicAdd(&n_list, here);
+      __syncthreads();
+      if (tid < cs) *cluster.map_shared_rank(&counted[step & 1][rank], tid) = n_list;
+      cluster.sync();
+      int count = 0;
+      for (int r = 0; r < cs; ++r) count += counted[step & 1][r];
+      if (count < P.k) {
         hi = mid;
       } else {
         lo = mid;
-        if (c <= kTopList) break;
+        if (count <= kTopList) break;
       }
     }
-    bound = lo;
+    __syncthreads();
     if (tid == 0) n_list = 0;
     __syncthreads();
-    reaching(bound, [&](unsigned long long k, int) {
-      const int at = atomicAdd(&n_list, 1);
-      if (at < kTopList) list[at] = k;
-    });
-    __syncthreads();
-    if (tid < cs) *cluster.map_shared_rank(&listed[rank], tid) = min(n_list, kTopList);
-    cluster.sync();
+    total = list_and_sum(lo);
   }
-  // the listed places leave the share, the rest is summed
-  reaching(bound, [&](unsigned long long, int at) { H.clear(at); });
-  ExpSum<E> sum;
-  sum.template add_share<NT, kTopU>(H, c2);
-  sum.template block<NW>(c2, red, redz);
-  if (tid == 0) *cluster.map_shared_rank(&sums[rank], 0) = make_float2(sum.m, sum.z);
-  cluster.sync();
   if (rank == 0) {
     // the row's list takes the place of the share
     unsigned long long *all = reinterpret_cast<unsigned long long *>(held);
     int at = 0;
     for (int r = 0; r < cs; ++r) {
       const unsigned long long *l = cluster.map_shared_rank(list, r);
-      for (int i = tid; i < listed[r] && at + i < kTopList; i += NT) all[at + i] = l[i];
-      at += listed[r];
+      for (int i = tid; i < sums[r].listed && at + i < kTopList; i += NT) all[at + i] = l[i];
+      at += sums[r].listed;
     }
     __syncthreads();
     total = min(at, kTopList);
@@ -253,7 +242,7 @@ __global__ void __launch_bounds__(kTopNT, kHeldCtas) sd_top_kernel(const TopPara
       float b = P.k < total ? key_value(all[P.k]) : neg_inf(), z = 0.f;
       for (int i = P.k + lane; i < total; i += 32) z += ex2((key_value(all[i]) - b) * c2);
       z = warp_sum(z);
-      for (int r = 0; r < cs; ++r) exp_merge(b, z, sums[r].x, sums[r].y, c2);
+      for (int r = 0; r < cs; ++r) exp_merge(b, z, sums[r].m, sums[r].z, c2);
       if (lane == 0) P.rest[n] = z == 0.f ? neg_inf() : b / P.T + logf(z);
     }
   }
@@ -272,29 +261,15 @@ __global__ void __launch_bounds__(kTopNT, kHeldCtas) sd_top_kernel(const TopPara
 // large logits at its end, or in a few threads' places) is gone over again
 // from memory.
 constexpr int kTopHeap = 2048;     // listed vectors of a streamed row
-constexpr float kLowest = -3.402823466e38f;
 
-// The largest value (of the upper 16 bits' grid) that k threads' `best` reach,
-// found by one warp bit by bit; kLowest where fewer have a finite logit.
+// top_bound_warp of the block's threads by their `best`, in every thread.
 template <int NT>
 __device__ __forceinline__ float top_bound(float best, int k, unsigned short *keys, float *out) {
-  keys[threadIdx.x] = (unsigned short)(((unsigned)ford(best) ^ 0x80000000u) >> 16);
+  keys[threadIdx.x] = top_key16(best);
   __syncthreads();
   if (threadIdx.x < 32) {
-    constexpr int J = NT / 32;
-    unsigned key[J], r = 0u;
-#pragma unroll
-    for (int j = 0; j < J; ++j) key[j] = keys[j * 32 + threadIdx.x];
-#pragma unroll 1
-    for (int bit = 15; bit >= 0; --bit) {
-      const unsigned t = r | (1u << bit);
-      int n = 0;
-#pragma unroll
-      for (int j = 0; j < J; ++j) n += key[j] >= t;
-      if (__reduce_add_sync(0xffffffffu, n) >= k) r = t;
-    }
-    // 0x007f is -inf's
-    if (threadIdx.x == 0) *out = r > 0x007fu ? fdeord((int)((r << 16) ^ 0x80000000u)) : kLowest;
+    const float b = top_bound_warp<NT>(keys, k);
+    if (threadIdx.x == 0) *out = b;
   }
   __syncthreads();
   return *out;
