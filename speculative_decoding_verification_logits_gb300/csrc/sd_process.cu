@@ -17,7 +17,13 @@
 //     work: read the logit again (from L2), compute, write over it.
 // Computing touched logits where A meets them is what this replaces: nearly
 // every warp then holds a touched one and runs the whole computation for a
-// lane or two (64 x 9 x 151936 bf16, masked: 471 us; large batch 495 us).
+// lane or two (64 x 9 x 151936 bf16, masked: 471 us against 81).
+// Measured on the GPU, with histories that touch most low ids: that case 81 us
+// (66 for part A alone; its bytes alone take 56), 256 x 5 x 128256 bf16 without
+// a mask 130 us (99 for part A; 106 of bytes at the copy rate).  Part B is what
+// is left above the copy: its instructions, not its bytes (L2 holds them).  A
+// single row of 32000 float32: 6 us, nearly all of it part B's chain of
+// barriers and dependent loads (2 us without it).
 
 #include "sd_rows.cuh"
 
@@ -27,10 +33,12 @@ namespace sdv {
 
 constexpr int kProcNT = 256;
 constexpr int kProcU = 3;   // rows in flight per thread
+constexpr int kProcCtas = 6;   // per SM
 
 struct ProcParams {
   sd_process_args a;
   int inplace;
+  int rows;   // of a sequence, per CTA
 };
 
 // Bits e0 .. e0 + VE - 1 of a bit row (word 0 holds bit 0; e0 may be negative
@@ -47,7 +55,7 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t *w, int e0, int W) 
 // VEC: rows move as 16-byte vectors (the output's rows lie on the same place
 // of the 16-byte grid as the input's); otherwise element by element.
 template <typename E, bool VEC>
-__global__ void __launch_bounds__(kProcNT, 6) sd_process_kernel(const ProcParams P) {
+__global__ void __launch_bounds__(kProcNT, kProcCtas) sd_process_kernel(const ProcParams P) {
   constexpr int VE = VEC ? Elt<E>::kPerVec : 1, NT = kProcNT, NW = NT / 32;
   constexpr int SZ = Elt<E>::kSize;
   constexpr uint32_t kAll = (1u << VE) - 1u;
@@ -62,6 +70,7 @@ __global__ void __launch_bounds__(kProcNT, 6) sd_process_kernel(const ProcParams
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ uint16_t hot[kWin];                       // touched tokens of the window
+  __shared__ __align__(16) uint16_t count[kWin];       // the window's counts
   __shared__ float bias[kWin];                         // sum of each token's biases
   __shared__ uint32_t touch[kWords];                   // a bit per token
   __shared__ int prev_i[SD_MAX_K], prev_v[SD_MAX_K];   // drafts inside the window, in order
@@ -73,13 +82,14 @@ __global__ void __launch_bounds__(kProcNT, 6) sd_process_kernel(const ProcParams
   // CTAs' part B is the longest
   const int b = blockIdx.x % a.B, q0 = (blockIdx.x / a.B) * NT;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int V = a.V, R = a.R;
+  const int V = a.V, r_lo = blockIdx.y * P.rows, R = min(P.rows, a.R - r_lo);
+  const int base = a.base + r_lo;   // drafts before this CTA's first row
   const float rep = a.repetition ? ld_float(a.repetition + b) : 1.f;
   const float pres = a.presence ? ld_float(a.presence + b) : 0.f;
   const float freq = a.frequency ? ld_float(a.frequency + b) : 0.f;
   const bool bad = !(rep > 0.f && rep < INFINITY) || !(fabsf(pres) < INFINITY) ||
                    !(fabsf(freq) < INFINITY);
-  const int n_draft = a.prev ? a.base + R - 1 : 0;
+  const int n_draft = a.prev ? base + R - 1 : 0;
   const bool touches = a.counts || n_draft > 0 || a.n_bias > 0;   // part B has work at all
 
   // the window's counts, this round's drafts and the biases are asked for
@@ -120,9 +130,9 @@ __global__ void __launch_bounds__(kProcNT, 6) sd_process_kernel(const ProcParams
 
   // A. copy and mask this thread's vector of every row
   const int W = (V + 31) >> 5, q = q0 + tid;
-  const uint8_t *xb = (const uint8_t *)a.logits + b * a.logits_sb * SZ;
-  uint8_t *yb = (uint8_t *)a.out + b * a.out_sb * SZ;
-  const uint32_t *mb = (const uint32_t *)a.mask + b * a.mask_sb;
+  const uint8_t *xb = (const uint8_t *)a.logits + (b * a.logits_sb + r_lo * a.logits_sr) * SZ;
+  uint8_t *yb = (uint8_t *)a.out + (b * a.out_sb + r_lo * a.out_sr) * SZ;
+  const uint32_t *mb = (const uint32_t *)a.mask + b * a.mask_sb + r_lo * a.mask_sr;
   const int64_t xs = a.logits_sr * SZ, ys = a.out_sr * SZ;
   // INNER: this CTA's vectors lie inside the row whatever its place on the
   // grid; its loop is kept apart from the one with the rows' ends
@@ -228,6 +238,7 @@ __global__ void __launch_bounds__(kProcNT, 6) sd_process_kernel(const ProcParams
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         m |= ((h[e] & 0xffffu ? 1u : 0u) | (h[e] >> 16 ? 2u : 0u)) << (2 * e);
+      reinterpret_cast<uint4 *>(count)[k] = c[i];
     }
     reinterpret_cast<uint8_t *>(touch)[k] = (uint8_t)m;
   }
@@ -316,7 +327,7 @@ __global__ void __launch_bounds__(kProcNT, 6) sd_process_kernel(const ProcParams
   const int groups = NT / tpt, r0 = tid / tpt;
   for (int h = tid & (tpt - 1); h < n_hot; h += tpt) {
     const int j = hot[h], v = w0 + j;
-    const uint32_t word = a.counts ? ld2(cb + v) : 0u;
+    const uint32_t word = a.counts ? count[j] : 0u;
     const int n0 = (int)(word & 0x7fffu);
     const float add = a.n_bias > 0 ? bias[j] : 0.f;
     uint32_t drafts = 0u;   // the drafts that equal the token
@@ -340,7 +351,7 @@ __global__ void __launch_bounds__(kProcNT, 6) sd_process_kernel(const ProcParams
         const int row = r + u * groups;
         float x = f[u];
         if (x == neg_inf()) continue;   // not this CTA's, forbidden, or as it was
-        const int before = a.base + row;
+        const int before = base + row;
         const int n = n0 + __popc(before >= 32 ? drafts : drafts & ((1u << before) - 1u));
         if (n > 0 || (word & 0x8000u)) x = x > 0.f ? x / rep : x * rep;
         if (n > 0) x = x - freq * (float)n - pres;
@@ -352,14 +363,20 @@ __global__ void __launch_bounds__(kProcNT, 6) sd_process_kernel(const ProcParams
 }
 
 template <typename E, bool VEC>
-static cudaError_t launch_process(const ProcParams &P, cudaStream_t s) {
+static cudaError_t launch_process(ProcParams &P, cudaStream_t s) {
   constexpr int VE = VEC ? Elt<E>::kPerVec : 1;
   // vectors of a row that starts anywhere on the 16-byte grid
   const int64_t nvec = ((int64_t)P.a.V + 2 * VE - 2) / VE;
   const int64_t grid = (nvec + kProcNT - 1) / kProcNT * P.a.B;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  // where the windows leave SMs idle, several CTAs share a window's rows, up
+  // to two waves of them (13 x 7 rows of 50021, tight mask, 300 biases: 19.1 us
+  // without, 16.1 with one wave, 14.4 with two, 22.6 with three)
+  const int64_t parts = std::min<int64_t>((P.a.R + kProcU - 1) / kProcU,
+                                          std::max<int64_t>(2 * kProcCtas * sm_count() / grid, 1));
+  P.rows = (int)((P.a.R + parts - 1) / parts);
+  cfg.gridDim = dim3((unsigned)grid, (unsigned)((P.a.R + P.rows - 1) / P.rows), 1);
   cfg.blockDim = dim3(kProcNT, 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
