@@ -260,13 +260,16 @@ __global__ void __launch_bounds__(kTopNT, kHeldCtas) sd_top_kernel(const TopPara
 // of them: no order changes the sum).  A row that overflows the list (its
 // large logits at its end, or in a few threads' places) is gone over again
 // from memory.
-constexpr int kTopHeap = 2048;     // listed vectors of a streamed row
+constexpr int kTopHeap = 2 * kTopList;   // listed vectors of a streamed row
 
-// top_bound_warp of the block's threads by their `best`, in every thread.
-template <int NT>
-__device__ __forceinline__ float top_bound(float best, int k, unsigned short *keys, float *out) {
+// top_bound_warp of the block's threads by their `best`, in every thread;
+// meanwhile() is what the threads do between its barriers.
+template <int NT, typename F>
+__device__ __forceinline__ float top_bound(float best, int k, unsigned short *keys, float *out,
+                                           F meanwhile) {
   keys[threadIdx.x] = top_key16(best);
   __syncthreads();
+  meanwhile();
   if (threadIdx.x < 32) {
     const float b = top_bound_warp<NT>(keys, k);
     if (threadIdx.x == 0) *out = b;
@@ -318,6 +321,7 @@ __global__ void __launch_bounds__(kStreamNT, 2) sd_top_stream_kernel(const TopPa
   // logits that may be chosen, then ranked; the list (vector << 8 | places)
   unsigned long long *kept = reinterpret_cast<unsigned long long *>(ring + Stream::kBytes / 16);
   uint32_t *heap = reinterpret_cast<uint32_t *>(kept + kTopList);
+  unsigned long long *ranked = reinterpret_cast<unsigned long long *>(heap);
   __shared__ unsigned short keys[NT];
   __shared__ float bound_s;
   __shared__ float wm[NW], wz[NW];
@@ -340,7 +344,7 @@ __global__ void __launch_bounds__(kStreamNT, 2) sd_top_stream_kernel(const TopPa
         const int i = d * Stream::kStep + Stream::at() + u * 32;
         if (i < row.nvec) best = fmaxf(best, Elt<E>::vmax(S.peek(d, u)));
       }
-    float bound = top_bound<NT>(best, k, keys, &bound_s);
+    float bound = top_bound<NT>(best, k, keys, &bound_s, [] {});
     int raise = (kStreamD - 1) * Stream::kStep * 2;
     ExpSum<E> sum;
     for (int q = 0; q < row.nvec; q += Stream::kStep) {
@@ -360,7 +364,7 @@ __global__ void __launch_bounds__(kStreamNT, 2) sd_top_stream_kernel(const TopPa
       }
       best = fmaxf(best, m);
       if (q >= raise || (bound == kLowest && __syncthreads_count(best > neg_inf()) >= k)) {
-        bound = top_bound<NT>(best, k, keys, &bound_s);
+        bound = top_bound<NT>(best, k, keys, &bound_s, [] {});
         raise = 2 * q;
       }
       if (m >= bound) {
@@ -376,22 +380,36 @@ __global__ void __launch_bounds__(kStreamNT, 2) sd_top_stream_kernel(const TopPa
       sum.template add<U>(v, c2, m);
     }
     // what may be chosen: at or above the bound from the whole row
-    bound = top_bound<NT>(best, k, keys, &bound_s);   // its barriers: the list is complete
-    int total = n_heap;
-    if (tid == 0) {
-      n_kept = 0;
-      less_max = (int)0x80000000;
-    }
-    __syncthreads();
+    int total = 0;
+    uint32_t h0 = 0u;   // the thread's first vector of the list, asked for at once
+    uint4 v0 = make_uint4(0u, 0u, 0u, 0u);
+    bound = top_bound<NT>(best, k, keys, &bound_s, [&] {   // the list is complete
+      total = n_heap;
+      if (tid < total) {
+        h0 = heap[tid];
+        v0 = row.load((int)(h0 >> 8));
+      }
+      if (tid == 0) {
+        n_kept = 0;
+        less_max = (int)0x80000000;
+      }
+    });
     // calls f(logit, its index) for the listed ones
     auto listed = [&](auto f) {
-      for (int i = tid; i < total; i += NT) {
-        const int vec = (int)(heap[i] >> 8);
+      uint32_t h = h0;
+      uint4 v = v0;
+      for (int i = tid; i < total;) {
         float x[VE];
-        Elt<E>::unpack(row.load(vec), x);
+        Elt<E>::unpack(v, x);
+        const int e0 = row.first((int)(h >> 8));
 #pragma unroll
         for (int e = 0; e < VE; ++e)
-          if ((heap[i] >> e) & 1u) f(x[e], row.first(vec) + e);
+          if ((h >> e) & 1u) f(x[e], e0 + e);
+        i += NT;
+        if (i < total) {
+          h = heap[i];
+          v = row.load((int)(h >> 8));
+        }
       }
     };
     if (total <= kTopHeap) {
@@ -478,41 +496,39 @@ __global__ void __launch_bounds__(kStreamNT, 2) sd_top_stream_kernel(const TopPa
       wz[tid >> 5] = sum.z;
       less[tid >> 5] = part;
     }
-    // ranks of those kept: the keys are distinct
+    // ranks of those kept, four threads to a key: the keys are distinct
     const int nk = min(n_kept, kTopList);
-    constexpr int kPer = (kTopList + NT - 1) / NT;
-    unsigned long long mine[kPer];
-    int above[kPer];
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int i = tid + j * NT;
-      above[j] = 0;
-      mine[j] = 0ull;
-      if (i < nk) {
-        mine[j] = kept[i];
+    __syncthreads();   // the list is done with: the ranked ones take its place
+    for (int i0 = 0; i0 < nk; i0 += NT / 4) {
+      const int i = i0 + (tid >> 2);
+      const unsigned long long key = i < nk ? kept[i] : ~0ull;
+      int above = 0;
 #pragma unroll 4
-        for (int o = 0; o < nk; ++o) above[j] += kept[o] > mine[j];
+      for (int o = tid & 3; o < nk; o += 4) above += kept[o] > key;
+      __syncwarp();
+      above += __shfl_xor_sync(0xffffffffu, above, 1);
+      above += __shfl_xor_sync(0xffffffffu, above, 2);
+      if ((tid & 3) || i >= nk) continue;
+      ranked[above] = key;
+      if (above < k) {
+        P.vals[(int64_t)n * k + above] = key_value(key);
+        P.ids[(int64_t)n * k + above] = key_index(key);
       }
     }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (tid + j * NT < nk) kept[above[j]] = mine[j];
+    for (int i = nk + tid; i < k; i += NT) {   // fewer than k finite ones
+      P.vals[(int64_t)n * k + i] = neg_inf();
+      P.ids[(int64_t)n * k + i] = -1;
+    }
     if (tid == 0) n_heap = 0;
     __syncthreads();
-    for (int i = tid; i < k; i += NT) {
-      const bool have = i < nk;
-      P.vals[(int64_t)n * k + i] = have ? key_value(kept[i]) : neg_inf();
-      P.ids[(int64_t)n * k + i] = have ? key_index(kept[i]) : -1;
-    }
     if (P.rest && tid < 32) {
       sum.m = tid < NW ? wm[tid] : neg_inf();
       sum.z = tid < NW ? wz[tid] : 0.f;
       sum.warp(c2);
       // what is left of the ranked ones, and the others of the list
-      const float b = k < nk ? key_value(kept[k]) : neg_inf();
+      const float b = k < nk ? key_value(ranked[k]) : neg_inf();
       float z = 0.f;
-      for (int i = k + lane; i < nk; i += 32) z += ex2((key_value(kept[i]) - b) * c2);
+      for (int i = k + lane; i < nk; i += 32) z += ex2((key_value(ranked[i]) - b) * c2);
       z = warp_sum(z);
       exp_merge(sum.m, sum.z, b, z, c2);
       unsigned long long all = 0ull;
