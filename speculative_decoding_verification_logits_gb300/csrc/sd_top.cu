@@ -253,11 +253,10 @@ __global__ void __launch_bounds__(kTopNT, kHeldCtas) sd_top_kernel(const TopPara
 // threads' best logits so far (k of them at or above it) and is raised as the
 // row goes by: before the first step, from all the steps in the copy ring,
 // and whenever what has gone by has doubled.  Vectors that hold what
-// reaches it go to a list (index and which places), those places are set to
-// -inf and the rest goes into the sum.  At the row's end the bound from all of
-// the row leaves little more than k logits of the list; these are ranked, the
-// others' exponentials are added as integers (fixed point below the largest
-// of them: no order changes the sum).  A row that overflows the list (its
+// reaches it go to a list, the other ones into the sum.  At the row's end the
+// bound from all of the row leaves little more than k logits of the list's
+// vectors; these are ranked, the others' exponentials are added as integers
+// (fixed point below the largest of them: no order changes the sum).  A row that overflows the list (its
 // large logits at its end, or in a few threads' places) is gone over again
 // from memory.
 constexpr int kTopHeap = 2 * kTopList;   // listed vectors of a streamed row
@@ -278,39 +277,6 @@ __device__ __forceinline__ float top_bound(float best, int k, unsigned short *ke
   return *out;
 }
 
-// The places of a vector that reach the bound (a value of the upper 16 bits'
-// grid, or kLowest), which become -inf.
-template <typename E>
-__device__ __forceinline__ uint32_t take_reaching(uint4 &v, float bound);
-template <>
-__device__ __forceinline__ uint32_t take_reaching<float>(uint4 &v, float bound) {
-  uint32_t w[4] = {v.x, v.y, v.z, v.w}, hit = 0u;
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (__uint_as_float(w[e]) >= bound) {
-      hit |= 1u << e;
-      w[e] = 0xff800000u;
-    }
-  v = make_uint4(w[0], w[1], w[2], w[3]);
-  return hit;
-}
-template <>
-__device__ __forceinline__ uint32_t take_reaching<__nv_bfloat16>(uint4 &v, float bound) {
-  // bf16's lowest finite value stands for kLowest, which bf16 does not have
-  const uint32_t half = bound == kLowest ? 0xff7fu : __float_as_uint(bound) >> 16;
-  const uint32_t b2 = half * 0x00010001u;
-  uint32_t w[4] = {v.x, v.y, v.z, v.w}, hit = 0u;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const unsigned m = __hge2_mask(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]),
-                                   *reinterpret_cast<const __nv_bfloat162 *>(&b2));
-    w[i] = (w[i] & ~m) | (0xff80ff80u & m);
-    hit |= ((m & 1u) | ((m >> 15) & 2u)) << (2 * i);
-  }
-  v = make_uint4(w[0], w[1], w[2], w[3]);
-  return hit;
-}
-
 template <typename E>
 __global__ void __launch_bounds__(kStreamNT, 2) sd_top_stream_kernel(const TopParams P) {
   constexpr int VE = Elt<E>::kPerVec, NT = kStreamNT, NW = NT / 32, U = kStreamU;
@@ -318,9 +284,9 @@ __global__ void __launch_bounds__(kStreamNT, 2) sd_top_stream_kernel(const TopPa
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   using Stream = RowStream<E, NT, U, kStreamD>;
   extern __shared__ uint4 ring[];
-  // logits that may be chosen, then ranked; the list (vector << 8 | places)
+  // logits that may be chosen; the list of vectors, then the ranked logits
   unsigned long long *kept = reinterpret_cast<unsigned long long *>(ring + Stream::kBytes / 16);
-  uint32_t *heap = reinterpret_cast<uint32_t *>(kept + kTopList);
+  int *heap = reinterpret_cast<int *>(kept + kTopList);
   unsigned long long *ranked = reinterpret_cast<unsigned long long *>(heap);
   __shared__ unsigned short keys[NT];
   __shared__ float bound_s;
@@ -368,47 +334,49 @@ __global__ void __launch_bounds__(kStreamNT, 2) sd_top_stream_kernel(const TopPa
         raise = 2 * q;
       }
       if (m >= bound) {
+        m = neg_inf();
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          if (!(each[u] >= bound)) continue;
-          const uint32_t hit = take_reaching<E>(v[u], bound);
+          if (!(each[u] >= bound)) {
+            m = fmaxf(m, each[u]);
+            continue;
+          }
+          v[u] = make_uint4(inf, inf, inf, inf);
           const int at = atomicAdd(&n_heap, 1);
-          if (at < kTopHeap) heap[at] = (uint32_t)(first + u * 32) << 8 | hit;
+          if (at < kTopHeap) heap[at] = first + u * 32;
         }
-        m = VecExp<E>::template largest<U>(v);
       }
       sum.template add<U>(v, c2, m);
     }
     // what may be chosen: at or above the bound from the whole row
     int total = 0;
-    uint32_t h0 = 0u;   // the thread's first vector of the list, asked for at once
+    int h0 = 0;         // the thread's first vector of the list, asked for at once
     uint4 v0 = make_uint4(0u, 0u, 0u, 0u);
     bound = top_bound<NT>(best, k, keys, &bound_s, [&] {   // the list is complete
       total = n_heap;
       if (tid < total) {
         h0 = heap[tid];
-        v0 = row.load((int)(h0 >> 8));
+        v0 = row.load(h0);
       }
       if (tid == 0) {
         n_kept = 0;
         less_max = (int)0x80000000;
       }
     });
-    // calls f(logit, its index) for the listed ones
+    // calls f(logit, its index) for the listed vectors'
     auto listed = [&](auto f) {
-      uint32_t h = h0;
+      int h = h0;
       uint4 v = v0;
       for (int i = tid; i < total;) {
         float x[VE];
         Elt<E>::unpack(v, x);
-        const int e0 = row.first((int)(h >> 8));
+        const int e0 = row.first(h);
 #pragma unroll
-        for (int e = 0; e < VE; ++e)
-          if ((h >> e) & 1u) f(x[e], e0 + e);
+        for (int e = 0; e < VE; ++e) f(x[e], e0 + e);
         i += NT;
         if (i < total) {
           h = heap[i];
-          v = row.load((int)(h >> 8));
+          v = row.load(h);
         }
       }
     };
@@ -418,7 +386,7 @@ __global__ void __launch_bounds__(kStreamNT, 2) sd_top_stream_kernel(const TopPa
         if (x >= bound) {
           const int at = atomicAdd(&n_kept, 1);
           if (at < kTopList) kept[at] = top_key(x, i);
-        } else {
+        } else if (x == x) {   // not a NaN
           most = max(most, ford(x));
         }
       });
@@ -485,7 +453,9 @@ __global__ void __launch_bounds__(kStreamNT, 2) sd_top_stream_kernel(const TopPa
     const float top_less = fdeord(less_max);
     unsigned long long part = 0ull;
     listed([&](float x, int) {
-      if (!(x >= bound)) part += (unsigned long long)(ex2((x - top_less) * c2) * 17592186044416.f);
+      if (x >= bound || x == neg_inf()) return;
+      if (x == x) part += (unsigned long long)(ex2((x - top_less) * c2) * 17592186044416.f);
+      else sum.z = x;
     });
     __syncwarp();
 #pragma unroll
