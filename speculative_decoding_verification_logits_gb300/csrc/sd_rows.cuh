@@ -123,19 +123,6 @@ __device__ __forceinline__ uint4 mask_vec(uint4 v, uint32_t ok) {
 __device__ __forceinline__ void row_async16(uint32_t dst, const void *src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-// The same with an eviction priority in L2: first where the place is read for
-// the last time, which leaves the room to what is still needed.
-__device__ __forceinline__ void row_async16(uint32_t dst, const void *src, uint64_t policy) {
-  asm volatile("cp.async.ca.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "l"(policy)
-               : "memory");
-}
-__device__ __forceinline__ uint64_t l2_policy(bool last_use) {
-  uint64_t first, normal;
-  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(first));
-  asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(normal));
-  return last_use ? first : normal;
-}
 __device__ __forceinline__ uint4 lds16(uint32_t p) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -299,10 +286,8 @@ static cudaError_t launch_streamed(void (*fn)(const P), const P &params, int N, 
 // times in a row).  Every thread copies its own vectors, U a step, into its
 // own places of a ring of D steps; the copies run on across the ends of
 // passes and rows, so that what happens there costs no bandwidth.  The second
-// pass goes backwards: what L2 still holds of the row is its end; the last pass
-// gives the row's lines up (loss and gradient of 2048 x 128256 bf16: 207 us
-// without, 199 with; loss alone of 576 x 151936: 34.8, 33).  Rows of weight 0
-// are left out.  In a step a warp has 32 U vectors side by side:
+// pass goes backwards: what L2 still holds of the row is its end.  Rows of
+// weight 0 are left out.  In a step a warp has 32 U vectors side by side:
 // its vector u of the step that begins at q is q + at() + 32 u.
 template <typename E, int NT, int U, int D>
 struct RowStream {
@@ -317,7 +302,6 @@ struct RowStream {
   RowView<E> view;
   const uint8_t *src;   // this thread's first vector of it, where it is inside the row
   int row, pass, q, put, take;
-  uint64_t policy;      // rows are given up in L2 where they are read for the last time
   static __device__ __forceinline__ int at() {
     return (threadIdx.x >> 5) * 32 * U + (threadIdx.x & 31);
   }
@@ -335,7 +319,6 @@ struct RowStream {
       while (row < N && ld_float(weight + row) == 0.f) row += gridDim.x;
     if (row < N) view = RowView<E>(base, (int64_t)row * stride, V);
     pass = q = 0;
-    policy = l2_policy(passes == 1);
     src = view.row + ((int64_t)at() * RowView<E>::VE - view.hp) * Elt<E>::kSize;
   }
   __device__ __forceinline__ void ask() {
@@ -343,7 +326,7 @@ struct RowStream {
     if (row < N) {
       if (q > 0 && q + kStep < view.nvec) {   // no end of the row in the step
 #pragma unroll
-        for (int u = 0; u < U; ++u) row_async16(to + u * (NT * 16), src + u * 512, policy);
+        for (int u = 0; u < U; ++u) row_async16(to + u * (NT * 16), src + u * 512);
       } else {
 #pragma unroll 1
         for (int u = 0; u < U; ++u) {
@@ -358,7 +341,6 @@ struct RowStream {
       src += (int64_t)way * 16;
       if (q >= view.nvec || q < 0) {
         if (++pass < passes) {   // back over the row, from the step just asked for
-          policy = l2_policy(pass == passes - 1);
           q -= kStep;
           src -= kStep * 16;
         } else {
