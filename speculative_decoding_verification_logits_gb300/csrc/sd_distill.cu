@@ -14,12 +14,19 @@
 // Gradient: named w/T (q - p) = w/T q (1 - e^d); others w/T (q_r - p_r) e_j / Z_r
 // with e_j / Z_r the softmax among the others.
 //
-// One cluster of cs CTAs per row, which holds it in shared memory.  The named
-// places are set to -inf there, so that both passes meet only the others.
-// Pass 1: running maximum and sum.  The cluster exchanges (offset, sum) and
-// every CTA works out the k + 1 buckets.  Pass 2 writes the gradient of its
-// share, then the named places over it.  HBM-bound: 2 or 4 bytes per logit
-// for the loss, twice that with the gradient.
+// Few rows: one cluster of cs CTAs per row, which holds it in shared memory.
+// The named places are set to -inf there, so that both passes meet only the
+// others.  Pass 1: running maximum and sum.  The cluster exchanges (offset,
+// sum) and every CTA works out the k + 1 buckets.  Pass 2 writes the gradient
+// of its share, then the named places over it.
+// Many rows: one CTA per row, streamed (sd_distill_stream_kernel).
+// To move: 2 or 4 bytes per logit for the loss, twice that with the gradient.
+// Measured on the GPU: the loss of 576 x 151936 bf16, k 64, 34 us (5.1 TB/s;
+// two rows per CTA leave its ends uncovered); loss and gradient of 2048 x
+// 128256, 207 us (5.1 TB/s of row bytes; DRAM moves more, since the second
+// pass finds only a part of its row in L2: 304 rows of 256 KB are on their way
+// beside what is written); 48 x 32000 fp32, k 16, 8.5 us.  A row shared by two
+// CTAs, half as many rows on their way, took 228 us, by four 495.
 
 #include "sd_rows.cuh"
 
@@ -28,7 +35,6 @@ namespace sdv {
 constexpr int kDistNT = 256;
 constexpr int kDistNW = kDistNT / 32;
 constexpr int kDistU = 4;         // vectors at a time per thread
-
 
 struct DistParams {
   sd_distill_args a;

@@ -229,8 +229,9 @@ struct Held {
 // The cluster size that holds rows of V elements, or 0 where N rows are so many
 // that streaming them is faster: eight CTAs per row (more for rows that need
 // them, fewer for short ones), while the device has room for all of them.
-// Measured for the loss and its gradient, us, held / streamed: 48 rows of
-// 128256 bf16 11.1 / 17.1, 76 rows 18.7 / 17.2, 152 rows 26.1 / 17.6.
+// Measured, us, held / streamed, rows of 128256 bf16: top logits 8 rows 11.3 /
+// 16.4, 48 rows 15.3 / 16.7, 76 rows 22.5 / 16.7; loss and gradient 8 rows 8.4 /
+// 17.5, 48 rows 11.4 / 17.8, 76 rows 18.1 / 18.0.
 template <typename E>
 static int held_cluster(int64_t N, int V, int NT, int *share_bytes) {
   constexpr int VE = Elt<E>::kPerVec;

@@ -15,8 +15,14 @@
 // A row whose logits at the bound do not fit the list (large logits all in a
 // few groups) raises its bound first by halving the range of keys until at
 // least k and at most a list of logits are left.
+// Many rows: see sd_top_stream_kernel.
 // Keys order logits by value, then by lower index: (ordered image of the
-// value, ~index).  HBM-bound: a row is 2 or 4 V bytes, the results 8 k + 4.
+// value, ~index).  A row is 2 or 4 V bytes to read, the results are 8 k + 4.
+// Measured on the GPU: 576 rows of 151936 bf16, k 64, 45 us (3.9 TB/s; the
+// loss's plain sum over the same rows takes 34): what is above the stream is
+// the row's end (bound, list, ranks), which two CTAs per SM overlap only in
+// part.  7 rows of 128256, k 32: 9.9 us, 33 rows of 50021 fp32, k 128: 14.2 us,
+// chains of one load of the row, two cluster barriers, the ranks.
 
 #include "sd_rows.cuh"
 
