@@ -21,7 +21,7 @@
 // Measured on the GPU: 576 rows of 151936 bf16, k 64, 45 us (3.9 TB/s; the
 // loss's plain sum over the same rows takes 34): what is above the stream is
 // the row's end (bound, list, ranks), which two CTAs per SM overlap only in
-// part.  7 rows of 128256, k 32: 9.9 us, 33 rows of 50021 fp32, k 128: 14.2 us,
+// part.  7 rows of 128256, k 32: 9.9 us, 33 rows of 50021 fp32, k 128: 12.9 us,
 // chains of one load of the row, two cluster barriers, the ranks.
 
 #include "sd_rows.cuh"
@@ -97,8 +97,11 @@ __device__ __forceinline__ float top_bound_warp(const unsigned short *keys, int 
   return r > 0x007fu ? fdeord((int)((r << 16) ^ 0x80000000u)) : kLowest;
 }
 
+// Registers for one CTA per SM more than the rule for held rows counts on:
+// clusters of eight do not fill every group of SMs to the last place (57 rows
+// of 32000 fp32, exactly three CTAs per SM, ran in two waves: 20 us).
 template <typename E>
-__global__ void __launch_bounds__(kTopNT, kHeldCtas) sd_top_kernel(const TopParams P) {
+__global__ void __launch_bounds__(kTopNT, kHeldCtas + 1) sd_top_kernel(const TopParams P) {
   constexpr int VE = Elt<E>::kPerVec, NT = kTopNT, NW = kTopNW;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
