@@ -86,7 +86,7 @@ __device__ __forceinline__ void dist_buckets(Named &N, Buckets &B, int k, float 
   const int lane = threadIdx.x & 31;
   float t[J], x[J];
   bool is[J];
-  float tm = rest * T, sm = m;   // largest logits (rest T is exact in the fused product below)
+  float tm = neg_inf(), sm = m;   // largest logits: of the teacher's named tokens, of the student
   bool taught = rest != neg_inf();
 #pragma unroll
   for (int j = 0; j < J; ++j) {
@@ -109,33 +109,70 @@ __device__ __forceinline__ void dist_buckets(Named &N, Buckets &B, int k, float 
   tm = warp_max(tm);
   sm = warp_max(sm);
   const float s0 = sm == neg_inf() ? 0.f : sm;
+  // log2 of the teacher's rest beside the largest named token's 2^0: a difference
+  // of numbers that may be far larger than itself, and the ratio of the two masses
+  // enters the loss to first order, so it is taken to twice fp32's digits where
+  // both are in range
+  float rl, rlo = 0.f;
+  if (fabsf(tm * c2) < 1e4f && fabsf(rest) < 1e4f) {
+    const float l = 1.44269502f, ll = 1.92596299e-8f;           // log2 e = l + ll
+    const float cl = (fmaf(-c2, T, l) + ll) / T;                // log2 e / T = c2 + cl
+    const float u = rest * l, ul = fmaf(rest, l, -u) + rest * ll;
+    const float v = tm * c2, vl = fmaf(tm, c2, -v) + tm * cl;
+    rl = u - v;
+    const float b = rl - u;
+    rlo = ((u - (rl - b)) - (v + b)) + (ul - vl);
+  } else {
+    tm = fmaxf(tm, rest * T);
+    rl = fmaf(rest, T, -tm) * c2;
+  }
+  // a power of two that keeps the larger of the two in range
+  const float n = fmaxf(ceilf(rl), 0.f);
+  const float down = n < 126.f ? __int_as_float((127 - (int)n) << 23) : 0.f;
+  // the student's likewise: z = zm 2^e, 2^ns is taken out of its masses
+  const int e = z >= 1.f && z < INFINITY ? (__float_as_int(z) >> 23) - 127 : 0;
+  const float zm = __int_as_float(__float_as_int(z) - (e << 23));
+  const float g = m == neg_inf() ? neg_inf() : (m - s0) * c2;
+  const int ns = g > -64.f ? max(e + (int)ceilf(g), 0) : 0;
+  const float sdown = __int_as_float((127 - ns) << 23);
   float te[J], se[J], tsum = 0.f, ssum = 0.f;
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     t[j] = (t[j] - tm) * c2;
     x[j] = (x[j] - s0) * c2;
-    te[j] = ex2(t[j]);
-    se[j] = is[j] ? ex2(x[j]) : 0.f;
+    te[j] = ex2(t[j]) * down;
+    t[j] -= n;
+    se[j] = is[j] ? ex2(x[j]) * sdown : 0.f;
+    x[j] -= (float)ns;
     tsum += te[j];
     ssum += se[j];
   }
-  const float rl = rest == neg_inf() ? neg_inf() : fmaf(rest, T, -tm) * c2, re = ex2(rl);
-  const float ol = m == neg_inf() ? neg_inf() : (m - s0) * c2 + log2f(z);   // the others' log2 sum
-  const float zr = z * ex2((m - s0) * c2);
+  const float ol = (log2f(zm) + g) + (float)(e - ns);   // the others' log2 sum
+  const float zr = z * sdown * ex2(g);
+  const float ln2 = 0.693147180559945309f;
+  const float re = ex2(rl - n) * fmaf(rlo, ln2, 1.f);
   const float zt = warp_sum(tsum) + re, zs = warp_sum(ssum) + zr;
   const float pr = re / zt, qr = zr / zs;
-  const float ln2 = 0.693147180559945309f;
   const float norm = log2f(zt) - log2f(zs);
-  const float dr = ((rl - ol) - norm) * ln2;
+  const float dr = (((rl - n) + rlo - ol) - norm) * ln2;
   const float wt = w / T;
+  // a named token's ln(p / q) from the difference of its two logits: the offsets
+  // of both sides, far from them where the others hold most of the mass, enter
+  // as one number, whose error is the same for all named tokens.  (Offsets apart
+  // by more than any sensible logits: the differences of what was shifted.)
+  const float shift = (tm - s0) * c2 + (n - (float)ns);
+  const bool direct = fabsf(shift) < 1e4f;
+  const float off = direct ? shift + norm : norm;
   float kl = lane == 0 ? dist_term(pr, qr, dr) : 0.f, named = 0.f;
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     if (j * 32 >= k) continue;   // the same for the warp
-    const float p = te[j] / zt, q = se[j] / zs, d = ((t[j] - x[j]) - norm) * ln2;
+    const int i = j * 32 + lane;
+    const float p = te[j] / zt, q = se[j] / zs;
     if (is[j]) {
+      const float d = ((direct ? (N.t[i] - N.x[i]) * c2 : t[j] - x[j]) - off) * ln2;
       kl += dist_term(p, q, d);
-      N.g[j * 32 + lane] = wt * (fabsf(d) < 0.5f ? -q * expm1f(d) : q - p);
+      N.g[i] = wt * (fabsf(d) < 0.5f ? -q * expm1f(d) : q - p);
       named += p - q;
     }
   }
