@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kDistNT, kHeldCtas) sd_distill_kernel(const Di
   const bool live = buckets.live != 0;
   const float coef = live ? buckets.coef : 0.f;
   const ExpBase B(buckets.m, c2);
-  const uint64_t ss = pk2(coef, coef);
+  const uint64_t ss = pk2(coef * B.fix, coef * B.fix);
   uint8_t *to = out + (int64_t)H.row.first(H.qa) * Elt<E>::kSize;
 #pragma unroll 4
   for (int i = tid; i < H.n; i += NT) {
@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kStreamNT, 2) sd_distill_stream_kernel(const D
     const bool live = buckets.live != 0;
     const float coef = live ? buckets.coef : 0.f;
     const ExpBase B(buckets.m, c2);
-    const uint64_t ss = pk2(coef, coef);
+    const uint64_t ss = pk2(coef * B.fix, coef * B.fix);
     const int last = (row.nvec - 1) / Stream::kStep * Stream::kStep;
     uint8_t *to = out + ((int64_t)(last + Stream::at()) * VE - row.hp) * Elt<E>::kSize;
     for (int q = last; q >= 0; q -= Stream::kStep, to -= Stream::kStep * 16) {

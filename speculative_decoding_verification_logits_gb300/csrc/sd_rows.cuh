@@ -371,19 +371,25 @@ struct RowStream {
 };
 
 // ------------------------------------------------- exponentials of vectors --
-// 2^((x - m) c) for the elements of vectors, in packed pairs: as 2^(x c - m c),
-// one fused operation, where m c is far from fp32's range, and with the
-// difference first where it is not (FAR: rows of the type's lowest value, a
-// mask's stand-in for -inf, stay finite).  Errors in m c are the same for
-// every term of a row.
-constexpr float kFar = 1e37f;
+// 2^((x - m) c) for the elements of vectors, in packed pairs.  Where m c is of
+// ordinary size: 2^(x c - h) with h = m c rounded, one fused operation.  What
+// the rounding of h leaves, m c - h, is as large as 2^-24 |m c| and another
+// number for every m (each thread has its own, and the row has one in the second
+// pass): `fix` = 2^(h - m c) takes it out of a sum, or of a factor, of such terms.
+// From |m c| = kFar on (FAR) the difference comes first: fix, by its first two
+// terms, is good to 2^-26 below that, and a finite stand-in for -inf (-1e10,
+// the type's lowest value) would leave an h whose rounding passes 2^128.
+// Either way the term of m itself is 1.
+constexpr float kFar = 4096.f;
 struct ExpBase {
-  uint64_t o, c;   // FAR: (-m, c), else (-m c, c)
+  uint64_t o, c;   // FAR: (-m, c), else (-h, c)
+  float fix;
   bool far;
   __device__ __forceinline__ ExpBase(float m, float cc) {
-    const float s = m == neg_inf() ? 0.f : m;
-    far = fabsf(s * cc) > kFar;
-    const float b = far ? -s : -s * cc;
+    const float s = m == neg_inf() ? 0.f : m, h = s * cc;
+    far = fabsf(h) >= kFar;
+    fix = far ? 1.f : fmaf(fmaf(-s, cc, h), 0.693147180559945309f, 1.f);
+    const float b = far ? -s : -h;
     o = pk2(b, b);
     c = pk2(cc, cc);
   }
@@ -502,7 +508,7 @@ struct ExpSum {
     }
     float x, y;
     upk2(acc, x, y);
-    z += x + y;
+    z = fmaf(x + y, B.fix, z);
   }
   // this thread's vectors of a share: NT apart, U at a time
   template <int NT, int U>
