@@ -158,10 +158,12 @@ __device__ __forceinline__ void dist_buckets(Named &N, Buckets &B, int k, float 
   const float wt = w / T;
   // a named token's ln(p / q) from the difference of its two logits: the offsets
   // of both sides, far from them where the others hold most of the mass, enter
-  // as one number, whose error is the same for all named tokens.  (Offsets apart
-  // by more than any sensible logits: the differences of what was shifted.)
+  // as one number, whose error is the same for all named tokens.  That error, and
+  // the difference's own, grow with the distance between the two sides; from 32
+  // on (in powers of two: about where they pass those of the logits' distances
+  // from their own largest) each side is taken from its own offset instead.
   const float shift = (tm - s0) * c2 + (n - (float)ns);
-  const bool direct = fabsf(shift) < 1e4f;
+  const bool direct = fabsf(shift) < 32.f;
   const float off = direct ? shift + norm : norm;
   float kl = lane == 0 ? dist_term(pr, qr, dr) : 0.f, named = 0.f;
 #pragma unroll

@@ -130,7 +130,7 @@ def _teacher(N, V, k, T, seed, shift=0.0):
 @pytest.mark.parametrize("times", [1, STREAMED])
 def test_distill_among_finite_fills(dev, dtype, T, times):
     V, k, T = 5003, 9, f32(T)
-    for n, fill in enumerate(_fills(dtype)[1:]):
+    for n, fill in enumerate(_fills(dtype)):
         t, vals, ids, rest = _teacher(6, V, k, T, 10 + n)
         g = _g(40 + n)
         x = t + torch.randn(t.shape, generator=g)
@@ -156,7 +156,8 @@ def test_distill_among_finite_fills(dev, dtype, T, times):
 @pytest.mark.parametrize("times", [1, STREAMED])
 @pytest.mark.parametrize("dtype,of_student,of_teacher", [
     (F32, 1000.0, 1000.0), (F32, -1000.0, -1000.0), (F32, 3e4, 3e4), (F32, -3e4, -3e4),
-    (F32, 100.0, 100.0), (BF, 1000.0, 1000.0)])
+    (F32, 100.0, 100.0), (BF, 1000.0, 1000.0), (F32, 1000.0, 0.0), (F32, -1000.0, 0.0),
+    (F32, 0.0, 1000.0), (F32, 60.0, -60.0), (F32, 5000.0, 0.0), (F32, 3e4, -3e4)])
 def test_distill_rows_moved_by_a_constant(dev, dtype, of_student, of_teacher, T, times):
     # the softmax does not know of the constant, and no tolerance here does
     V, k, T = 6007, 24, f32(T)
