@@ -112,9 +112,13 @@ __device__ __forceinline__ void dist_buckets(Named &N, Buckets &B, int k, float 
   // log2 of the teacher's rest beside the largest named token's 2^0: a difference
   // of numbers that may be far larger than itself, and the ratio of the two masses
   // enters the loss to first order, so it is taken to twice fp32's digits where
-  // both are in range
+  // both are in range, and by one fused operation, exact but for its own rounding,
+  // where they are not.  Bounded, so that a finite rest has a finite one.
   float rl, rlo = 0.f;
-  if (fabsf(tm * c2) < 1e4f && fabsf(rest) < 1e4f) {
+  if (tm == neg_inf()) {   // all of the mass with the others
+    tm = 0.f;
+    rl = rest < INFINITY ? 0.f : rest - rest;   // NaN has a NaN loss
+  } else if (fabsf(tm * c2) < 1e4f && fabsf(rest) < 1e4f) {
     const float l = 1.44269502f, ll = 1.92596299e-8f;           // log2 e = l + ll
     const float cl = (fmaf(-c2, T, l) + ll) / T;                // log2 e / T = c2 + cl
     const float u = rest * l, ul = fmaf(rest, l, -u) + rest * ll;
@@ -123,8 +127,8 @@ __device__ __forceinline__ void dist_buckets(Named &N, Buckets &B, int k, float 
     const float b = rl - u;
     rlo = ((u - (rl - b)) - (v + b)) + (ul - vl);
   } else {
-    tm = fmaxf(tm, rest * T);
     rl = fmaf(rest, T, -tm) * c2;
+    if (rl > 1e30f && rest < INFINITY) rl = 1e30f;
   }
   // a power of two that keeps the larger of the two in range
   const float n = fmaxf(ceilf(rl), 0.f);
@@ -174,7 +178,7 @@ __device__ __forceinline__ void dist_buckets(Named &N, Buckets &B, int k, float 
     if (is[j]) {
       const float d = ((direct ? (N.t[i] - N.x[i]) * c2 : t[j] - x[j]) - off) * ln2;
       kl += dist_term(p, q, d);
-      N.g[i] = wt * (fabsf(d) < 0.5f ? -q * expm1f(d) : q - p);
+      N.g[i] = wt * (p > 0.f && fabsf(d) < 0.5f ? -q * expm1f(d) : q - p);
       named += p - q;
     }
   }

@@ -78,15 +78,21 @@ def _want(x, ids, vals, rest, T, w):
     """(loss, gradient, their tolerances): ref.distill and ref.distill_tolerance for rows whose
     others may hold a share of the softmax below 64 bits' smallest.  The gradient is the
     formula's, w/T (q - p) and w/T (q_j - p_r s_j), with s the softmax among the others by
-    itself.  x is moved to a largest logit of zero first, which changes nothing but that 64 bits
-    hold the logarithm of a sum over a row of -1e10 and less."""
+    itself.  Student and teacher are moved to a largest logit of zero first, which changes
+    nothing but that 64 bits hold the logarithms of sums over logits of -1e9 and less."""
     N, V = x.shape
     x = x.to(ref.D)
     x = x - x.max(1, keepdim=True).values
+    at = vals.to(ref.D).max(1).values
+    at = torch.where(at > -math.inf, at, rest.to(ref.D) * T)
+    at = torch.where(at > -math.inf, at, 0.0)      # nothing taught
+    vals, rest = vals.to(ref.D) - at[:, None], rest.to(ref.D) - at / T
     loss, grad, shares = ref.distill(x, ids, vals, rest, T, w)
     lt, gt = ref.distill_tolerance(x, shares, T, w, V)
     E = 2 * ref.lse_error(V) + 2.0 ** -21
     for n in range(N):
+        if shares[n] is None:
+            continue
         p, q, d, named, ls = shares[n]
         others = torch.ones(V, dtype=torch.bool)
         others[named] = False
@@ -164,3 +170,38 @@ def test_distill_rows_moved_by_a_constant(dev, dtype, of_student, of_teacher, T,
     t, vals, ids, rest = _teacher(6, V, k, T, 77, of_teacher)
     x = (t + torch.randn(t.shape, generator=_g(78)) + (of_student - of_teacher)).to(dtype)
     _check(dev, x, ids, vals, rest, T, None, times)
+
+
+@pytest.mark.parametrize("T", [0.3, 0.7, 1.0, 3.0, 7.0])
+@pytest.mark.parametrize("times", [1, STREAMED])
+def test_distill_teacher_rows_of_nothing_but_a_fill(dev, T, times):
+    # the mass of the others, given as its logarithm, and the named tokens' lie on either side
+    # of one another by the roundings of `rest`: hundreds and more of powers of two
+    V, k, T = 700, 5, f32(T)
+    g = _g(5)
+    for base in (1e9, 1e10, 1e12, 1e30, 1.5e38):
+        t = (-base * (1 + torch.rand(8, 1, generator=g))).expand(8, V).contiguous()
+        vals, ids = t[:, :k].contiguous(), torch.arange(k, dtype=torch.int32).repeat(8, 1)
+        rest = (t[:, 0].double() / T + math.log(V - k)).float()
+        ids[3, 2] = -1                               # an empty slot
+        vals[4] = -math.inf                          # all of the mass with the others
+        vals[5, 1:] = -math.inf
+        rest[6] = 3.0                                # named tokens far below the others
+        vals[7, 0] = 2.0                             # and far above
+        x = torch.randn((8, V), generator=g) * 3
+        _check(dev, x, ids, vals, rest, T, None, times)
+
+
+@pytest.mark.parametrize("times", [1, STREAMED])
+def test_distill_teacher_without_a_softmax(dev, times):
+    # a NaN or +inf on the teacher's side (as top_logits hands them on) is not taken for mass
+    V, k = 900, 4
+    t, vals, ids, rest = _teacher(5, V, k, 1.0, 3)
+    vals[0, 1] = math.inf
+    rest[1] = math.nan
+    vals[2], rest[2] = -math.inf, math.nan
+    rest[3] = math.inf
+    x = t + torch.randn(t.shape, generator=_g(4))
+    a = [v.to(dev).repeat(*((times,) + (1,) * (v.dim() - 1))) for v in (x, ids, vals, rest)]
+    loss = sd.distill_loss(*a).view(times, -1)
+    assert bool(torch.isnan(loss[:, :4]).all()) and bool(torch.isfinite(loss[:, 4]).all())
