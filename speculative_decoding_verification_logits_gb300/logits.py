@@ -3,6 +3,9 @@
 masks, a teacher's top logits, and the distillation loss with its gradient.
 
 Like the rest of the package this module only checks and marshals arguments.
+Memory that the caller hands over to be written (out, counts, grad) counts as
+changed in place for autograd: a backward pass that still needs what an
+operation saved of it raises torch's error instead of reading other values.
 
   token_counts(...), token_counts_add(...)   sd_token_counts, sd_token_counts_add
   process_logits(...)                        sd_process_logits
@@ -75,6 +78,8 @@ def _bind(L):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+_written = torch.autograd.graph.increment_version   # of a tensor of the caller's
+
 _loaded = None   # the library, once a call has needed it
 
 
@@ -140,10 +145,11 @@ def token_counts(history, lengths, V: int, *, prompt_lengths=None, out=None, sta
     B, L = history.shape
     dev = history.device
     _need(lengths, "lengths", torch.int32, (B,), dev)
-    if out is None:
-        out = torch.empty((B, V), dtype=torch.int16, device=dev)
-    else:
+    given = out is not None
+    if given:
         _need(out, "out", torch.int16, (B, V), dev)
+    else:
+        out = torch.empty((B, V), dtype=torch.int16, device=dev)
     prompt = st = None
     if prompt_lengths is not None:
         prompt = _arg(prompt_lengths, "prompt_lengths", torch.int32, (B,), dev)
@@ -151,6 +157,8 @@ def token_counts(history, lengths, V: int, *, prompt_lengths=None, out=None, sta
         st = _arg(status, "status", torch.int32, (1,), dev)
     _check(_lib().sd_token_counts(B, L, V, history.data_ptr(), lengths.data_ptr(), prompt,
                                   out.data_ptr(), st, _stream_of(dev)), "sd_token_counts")
+    if given:
+        _written(out)
     return out
 
 
@@ -171,6 +179,7 @@ def token_counts_add(counts, tokens, n, *, status=None, stream=None) -> torch.Te
     _check(_lib().sd_token_counts_add(B, tokens.shape[1], V, tokens.data_ptr(), n.data_ptr(),
                                       counts.data_ptr(), st, _stream_of(dev)),
            "sd_token_counts_add")
+    _written(counts)
     return counts
 
 
@@ -186,15 +195,18 @@ def process_logits(logits, *, counts=None, prev=None, base: int = 0, repetition=
     drafted tokens and base 0); repetition, presence, frequency [B] float32;
     bias_ids [B][n] int32 (-1: empty) with bias_vals [B][n] float32; mask
     [B][R][ceil(V / 32)] or [B][ceil(V / 32)] int32, a set bit allows the
-    token.  All are optional.  out may be the logits tensor itself."""
+    token.  All are optional.  out may be the logits tensor itself; there is no
+    gradient of this step, so logits that are to be trained keep to an output
+    of their own."""
     dt = _rows(logits, "logits", (2, 3))
     dev, shape = logits.device, logits.shape
     B, V = shape[0], shape[-1]
     R = shape[1] if len(shape) == 3 else 1
-    if out is None:
-        out = torch.empty(shape, dtype=logits.dtype, device=dev)
-    else:
+    given = out is not None
+    if given:
         _out_like(logits, out, "out")
+    else:
+        out = torch.empty(shape, dtype=logits.dtype, device=dev)
     xs, ys = logits.stride(), out.stride()
     a = ProcessArgs(B, R, V, dt, logits.data_ptr(), xs[0], xs[1] if len(xs) == 3 else 0,
                     out.data_ptr(), ys[0], ys[1] if len(ys) == 3 else 0)
@@ -239,6 +251,8 @@ def process_logits(logits, *, counts=None, prev=None, base: int = 0, repetition=
     if status is not None:
         a.status = _arg(status, "status", torch.int32, (1,), dev)
     _check(_lib().sd_process_logits(a, _stream_of(dev)), "sd_process_logits")
+    if given:
+        _written(out)
     return out
 
 
@@ -263,7 +277,8 @@ def top_logits(logits, k: int, *, temperature: float = 1.0, out: TopLogits | Non
     N, stride = _row_stride(logits, "logits")
     lead = shape[:-1]
     kept = (*lead, k)
-    if out is None:
+    given = out is not None
+    if not given:
         out = TopLogits(torch.empty(kept, dtype=torch.float32, device=dev),
                         torch.empty(kept, dtype=torch.int32, device=dev),
                         torch.empty(lead, dtype=torch.float32, device=dev))
@@ -274,6 +289,9 @@ def top_logits(logits, k: int, *, temperature: float = 1.0, out: TopLogits | Non
     _check(_lib().sd_top_logits(N, shape[-1], dt, logits.data_ptr(), stride, k, temperature,
                                 out.vals.data_ptr(), out.ids.data_ptr(), out.rest.data_ptr(),
                                 _stream_of(dev)), "sd_top_logits")
+    if given:
+        for t in out:
+            _written(t)
     return out
 
 
@@ -312,11 +330,14 @@ def distill_loss(student, ids, vals, rest=None, *, temperature: float = 1.0, wei
     teacher's mass): weight times the divergence of the k named tokens and one
     bucket of all others.  Evaluation: reads the logits once."""
     lead = student.shape[:-1]
-    if out is None:
-        out = torch.empty(lead, dtype=torch.float32, device=student.device)
-    else:
+    given = out is not None
+    if given:
         _need(out, "out", torch.float32, lead, student.device)
+    else:
+        out = torch.empty(lead, dtype=torch.float32, device=student.device)
     _distill(student, ids, vals, rest, temperature, weight, status, out, None)
+    if given:
+        _written(out)
     return out
 
 
@@ -325,12 +346,17 @@ def distill_grad(student, ids, vals, rest=None, *, temperature: float = 1.0, wei
                  grad=None, status=None, stream=None):
     """(loss, grad): the loss of distill_loss and, in the same call, its gradient
     with respect to the student's logits, times `weight` (what reaches each
-    row's loss from above: 1 / N for a mean).  grad may be the student tensor
-    itself.  To train: student.backward(grad)."""
+    row's loss from above: 1 / N for a mean).  To train: student.backward(grad).
+    grad may be the student tensor itself where no operation saved it for its
+    backward pass (a matrix product does not save its result, a tanh or softmax
+    does, and so does a logsumexp of the same logits): that pass then raises."""
     loss = torch.empty(student.shape[:-1], dtype=torch.float32, device=student.device)
-    if grad is None:
+    given = grad is not None
+    if not given:
         grad = torch.empty(student.shape, dtype=student.dtype, device=student.device)
     elif grad is not student:
         _out_like(student, grad, "grad")
     _distill(student, ids, vals, rest, temperature, weight, status, loss, grad)
+    if given:
+        _written(grad)
     return loss, grad
