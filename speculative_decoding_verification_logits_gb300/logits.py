@@ -118,17 +118,46 @@ def _arg(t, name, dtype, shape, device):
     return t.data_ptr()
 
 
+def _same(x, out):
+    """Whether two tensors of one shape are the same memory, element by element (the stride
+    of a dimension of one says nothing)."""
+    return x.data_ptr() == out.data_ptr() and all(
+        a == b for n, a, b in zip(x.shape, x.stride(), out.stride()) if n > 1)
+
+
+def _apart(x, out):
+    """Whether the ranges of addresses of two tensors are disjoint."""
+    ends = lambda t: t.data_ptr() + t.element_size() * (
+        1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))
+    return not x.numel() or out.data_ptr() >= ends(x) or x.data_ptr() >= ends(out)
+
+
+def _overlap(x, out):
+    """Whether two tensors of contiguous rows, of one shape and type, share an element: rows
+    of one may lie between those of the other."""
+    if _apart(x, out):
+        return False
+
+    def starts(t):   # the rows' addresses, in order
+        a = torch.tensor(t.data_ptr(), device="cpu")
+        for n, s in zip(t.shape[:-1], t.stride()[:-1]):
+            a = a[..., None] + torch.arange(n, device="cpu") * (s * t.element_size())
+        return a.flatten().sort().values
+
+    # a row meets one of the other tensor's only if it meets the next one up or down
+    a, b, size = starts(x), starts(out), x.shape[-1] * x.element_size()
+    up = torch.searchsorted(b, a)
+    above, below = b[up.clamp(max=len(b) - 1)], b[(up - 1).clamp(min=0)]
+    return bool(((above - a).abs() < size).any() or ((a - below).abs() < size).any())
+
+
 def _out_like(x, out, name):
     """Checks an output given by the caller: shape and type of x, rows contiguous,
     either x itself or memory of its own."""
     _rows(out, name, (x.dim(),))
     if out.dtype != x.dtype or out.shape != x.shape or out.device != x.device:
         raise ValueError(f"{name} must have the shape, type and device of the input")
-    if out.data_ptr() == x.data_ptr() and out.stride() == x.stride():
-        return
-    ends = lambda t: t.data_ptr() + t.element_size() * (
-        1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))
-    if x.numel() and out.data_ptr() < ends(x) and x.data_ptr() < ends(out):
+    if not _same(x, out) and _overlap(x, out):
         raise ValueError(f"{name} overlaps the input without being the same tensor")
 
 
