@@ -245,6 +245,8 @@ def process_logits(logits, *, counts=None, prev=None, base: int = 0, repetition=
         if prev.dim() != 2:
             raise ValueError("prev must be [B][P]")
         P = prev.shape[1]
+        if P == 0 and base + R > 1 and B and R:   # has no address: not given, to the library
+            raise ValueError("prev must hold the base + R - 1 drafts that the rows count")
         a.prev, a.P, a.base = _arg(prev, "prev", torch.int32, (B, P), dev), P, base
     if repetition is not None:
         a.repetition = _arg(repetition, "repetition", torch.float32, (B,), dev)

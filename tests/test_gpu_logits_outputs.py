@@ -56,3 +56,16 @@ def test_in_place_with_idle_strides(dev):
     same = torch.as_strided(x, (B, 1, V), (V, 1, 1))
     assert torch.equal(sd.process_logits(x, prev=prev, base=1, presence=pres, out=same), want)
     assert torch.equal(x, want)
+
+
+def test_rows_without_the_drafts_that_they_count_are_refused(dev):
+    # no drafts at all (a tensor of no elements has no address) as well as too few
+    x = _rows((2, 3, 50), F32, dev)
+    prev = lambda n: torch.zeros((2, n), dtype=torch.int32, device=dev)
+    for n, rows, start in ((0, 3, 0), (0, 1, 1), (0, 2, 5), (1, 3, 0), (2, 1, 3)):
+        with pytest.raises((ValueError, sd.SDError)):
+            sd.process_logits(x[:, :rows], prev=prev(n), base=start)
+    for n, rows, start in ((0, 1, 0), (2, 3, 0), (2, 1, 2)):
+        y = sd.process_logits(x[:, :rows], prev=prev(n), base=start)
+        assert torch.equal(y, x[:, :rows])
+    assert sd.process_logits(x[:0], prev=prev(0)[:0], base=1).shape == (0, 3, 50)
