@@ -310,7 +310,8 @@ __global__ void __launch_bounds__(kDistNT, kHeldCtas) sd_distill_kernel(const Di
 }
 
 // Many rows: one CTA per row, streamed once for the sum and, for the gradient,
-// once more from L2.  The named tokens are marked in shared memory, a bit per
+// once more (2048 x 128256 bf16: L2 still holds somewhat more than half of
+// it).  The named tokens are marked in shared memory, a bit per
 // vector (looked at for every vector) and a bit per place.  Nothing but the
 // CTA's own barriers lies between the passes.
 template <typename E, bool GRAD, bool SAME>

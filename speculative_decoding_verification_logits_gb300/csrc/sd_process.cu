@@ -34,9 +34,9 @@ namespace sdv {
 constexpr int kProcNT = 256;
 constexpr int kProcU = 3;   // rows in flight per thread
 constexpr int kProcCtas = 6;   // per SM
-// part B halves the threads into groups until a group holds the listed tokens (its
-// loop over rows would not end with a group larger than the block), a block's
-// threads share the bias list out evenly, and one warp holds the drafts
+// part B doubles its groups of threads until one holds the listed tokens or is
+// the block (a group larger than the block would have a loop over rows without
+// end), the threads share the bias list out evenly, and one warp holds the drafts
 static_assert((kProcNT & (kProcNT - 1)) == 0 && kProcNT % 32 == 0, "threads: a power of two");
 static_assert(SD_MAX_BIAS % kProcNT == 0 && SD_MAX_K <= 32, "lists as the threads take them");
 

@@ -158,7 +158,7 @@ def test_process_logits(dev, B, R, V, dtype):
 @pytest.mark.parametrize("B,R,V,dtype", [(40, 2, 128256, BF), (80, 1, 32000, F32),
                                          (101, 3, 50021, BF)])
 def test_process_logits_many_sequences(dev, B, R, V, dtype, parts):
-    # enough work for two vectors per thread
+    # more CTAs than the device holds at once: a window's rows stay with one CTA
     x, k = _process_case(B, R, V, dtype, 6)
     k = {n: k[n] for n in parts}
     _check_process(sd.process_logits(x.to(dev), **_to(k, dev)), x, k)
