@@ -8,11 +8,13 @@
 // out once.  Counts cannot carry into the neighbouring bin: at most 32768
 // tokens are added to bins of at most 32767 before every bin is cut back.
 // sd_token_counts_add is one thread per emitted token.
-// Measured on the GPU: 256 histories of 16384 tokens over 128256 ids 21.6 us
-// (82 MB in and out, 3.8 TB/s); 3 of 131071 over 151936 ids 12.9 us.  What
-// bounds both is the chain of a CTA's phases (clear, tokens, write) in two to
-// three waves of CTAs, or one: without the atomics the first still takes 22 us,
-// and neither smaller nor larger slices shorten it.
+// Measured on the GPU: 256 histories of 16384 tokens over 128256 ids 22 us
+// (82 MB in and out, 3.7 TB/s); 3 of 131071 over 151936 ids 13 us.  What bounds
+// both is that the vocabulary is shared out and the history is not: each of the
+// first's four slices reads all of a sequence's tokens, in 2.25 waves of CTAs,
+// each of the second's fifty all 131071 of them from L2, four vectors per thread
+// in flight.  Without the atomics the first still takes 22 us, and neither
+// smaller nor larger slices shorten it.
 
 #include "sd_rows.cuh"
 

@@ -23,9 +23,9 @@
 // To move: 2 or 4 bytes per logit for the loss, twice that with the gradient.
 // Measured on the GPU: the loss of 576 x 151936 bf16, k 64, 34 us (5.1 TB/s;
 // two rows per CTA leave its ends uncovered); loss and gradient of 2048 x
-// 128256, 207 us (5.1 TB/s of row bytes; DRAM moves more, since the second
+// 128256, 208 us (5.1 TB/s of row bytes; DRAM moves more, since the second
 // pass finds only a part of its row in L2: 304 rows of 256 KB are on their way
-// beside what is written); 48 x 32000 fp32, k 16, 8.5 us.  A row shared by two
+// beside what is written); 48 x 32000 fp32, k 16, 8.4 us.  A row shared by two
 // CTAs, half as many rows on their way, took 228 us, by four 495.
 
 #include "sd_rows.cuh"

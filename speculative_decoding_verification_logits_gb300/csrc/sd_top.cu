@@ -18,10 +18,10 @@
 // Many rows: see sd_top_stream_kernel.
 // Keys order logits by value, then by lower index: (ordered image of the
 // value, ~index).  A row is 2 or 4 V bytes to read, the results are 8 k + 4.
-// Measured on the GPU: 576 rows of 151936 bf16, k 64, 45 us (3.9 TB/s; the
+// Measured on the GPU: 576 rows of 151936 bf16, k 64, 46 us (3.8 TB/s; the
 // loss's plain sum over the same rows takes 34): what is above the stream is
 // the row's end (bound, list, ranks), which two CTAs per SM overlap only in
-// part.  7 rows of 128256, k 32: 9.9 us, 33 rows of 50021 fp32, k 128: 12.9 us,
+// part.  7 rows of 128256, k 32: 9.8 us, 33 rows of 50021 fp32, k 128: 12.3 us,
 // chains of one load of the row, two cluster barriers, the ranks.
 
 #include "sd_rows.cuh"
