@@ -14,7 +14,9 @@ Entry points (same names as the C ABI):
   uniforms(...)          sd_uniforms
 and, from ``logits.py`` (C ABI in ``include/sd_logits.h``), the logit operators
 around the verify step: token_counts, token_counts_add, process_logits,
-top_logits, distill_loss, distill_grad.
+top_logits, distill_loss, distill_grad; from ``beam.py`` (``include/sd_beam.h``) beam
+search's step: beam_select, beam_reorder; from ``kv.py`` (``include/sd_kv.h``) the pages
+that rows of a paged cache share: kv_fork, kv_extend, kv_free, kv_copy, kv_compact.
 """
 from __future__ import annotations
 
@@ -124,6 +126,8 @@ def lib():
             L.sd_status_string.argtypes = [ctypes.c_int]
             L.sd_status_string.restype = ctypes.c_char_p
             logits._bind(L)
+            kv._bind(L)
+            beam._bind(L)
             _lib = L
     return _lib
 
@@ -637,3 +641,8 @@ from . import logits  # noqa: E402  (uses the names above)
 from .logits import (SD_MAX_BIAS, SD_MAX_TOP, SD_STATUS_BAD_PENALTY, TopLogits,  # noqa: E402,F401
                      distill_grad, distill_loss, process_logits, token_counts, token_counts_add,
                      top_logits)
+from . import beam, kv  # noqa: E402
+from .beam import SD_MAX_BEAMS, SD_MAX_STATES, Beams, beam_reorder, beam_select  # noqa: E402,F401
+from .kv import (SD_MAX_CACHES, SD_MAX_PAGES, SD_MAX_ROWS, SD_STATUS_BAD_PAGE,  # noqa: E402,F401
+                 SD_STATUS_BAD_PARENT, SD_STATUS_NO_PAGE, KVCompact, KVFork, KVMoves, kv_compact,
+                 kv_copy, kv_extend, kv_fork, kv_free)

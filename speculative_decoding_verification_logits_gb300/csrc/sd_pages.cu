@@ -1,0 +1,664 @@
+// Pages of a paged cache: forking and extending block tables, giving pages
+// back, moving the pages in use to the front.  Integer work on page ids and
+// their counts; the contents are sd_kvcopy.cu's.
+//
+// Whatever needs the free pages in order goes in two launches: the first
+// writes one bit per page and the counts of 8192-page chunks (beside it, one
+// CTA plans the rows); in the second every CTA finds the pages of its own ranks
+// from the counts and the bits of one chunk.  So no CTA waits for another, and
+// nothing depends on the order in which they run.
+
+#include "sd_rows.cuh"
+#include "sd_kv.h"
+
+namespace sdv {
+
+constexpr int kPgNT = 1024;              // threads of a chunk's CTA, and of the plan's
+constexpr int kPgChunk = 8192;           // pages of a chunk
+constexpr int kPgWords = kPgChunk / 32;
+constexpr int kRowNT = 128;              // threads of a row's CTA
+constexpr int kRowSlots = 512;           // slots that get pages at a time
+
+static int page_chunks(int N) { return (N + kPgChunk - 1) / kPgChunk; }
+
+__device__ __forceinline__ void pdl() {
+  // a programmatic dependent of the stream's previous kernel: nothing is read
+  // before it has finished; the next launch may be scheduled at once
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+__device__ __forceinline__ void set_status(int32_t *status, unsigned bits) {
+  if (status) atomicOr(status, (int)bits);
+}
+
+// One holder less; a page that nobody holds stays at zero.
+__device__ __forceinline__ bool give_back(int32_t *refs, int page) {
+  if (atomicSub(refs + page, 1) > 0) return true;
+  atomicAdd(refs + page, 1);
+  return false;
+}
+
+// The bits of a chunk's pages that are free (or in use), and how many.
+__device__ __forceinline__ void chunk_bits(int chunk, int N, const int32_t *refs, bool free,
+                                           uint32_t *bits, int32_t *counts) {
+  __shared__ int total;
+  if (threadIdx.x == 0) total = 0;
+  __syncthreads();
+  int mine = 0;
+  int ref[kPgChunk / kPgNT];
+#pragma unroll
+  for (int u = 0; u < kPgChunk / kPgNT; ++u) {
+    const int p = chunk * kPgChunk + u * kPgNT + threadIdx.x;
+    ref[u] = p < N ? ld_int(refs + p) : free ? 1 : 0;
+  }
+#pragma unroll
+  for (int u = 0; u < kPgChunk / kPgNT; ++u) {
+    const uint32_t word = ballot(free ? ref[u] == 0 : ref[u] > 0);
+    if ((threadIdx.x & 31) == 0) {
+      bits[(int64_t)chunk * kPgWords + (u * kPgNT + threadIdx.x) / 32] = word;
+      mine += __popc(word);
+    }
+  }
+  if ((threadIdx.x & 31) == 0) atomicAdd(&total, mine);
+  __syncthreads();
+  if (threadIdx.x == 0) counts[chunk] = total;
+}
+
+// ------------------------------------------------------------------- fork --
+struct ForkRow {
+  int parent, len;     // -1: an empty row
+  int flags;           // kHeir, kLead, kCopy
+  int kids;            // rows with this parent
+  int first, pages;    // rank of the first page it gets, and how many
+  int pair;            // rank of its copy
+  int last;            // the partly filled page
+};
+constexpr int kHeir = 1, kLead = 2, kCopy = 4;
+
+struct ForkParams {
+  int rows_in, R, per_in, per_out, M, page_size, append, keep, N, nchunk;
+  const int32_t *parents, *table, *kv_len;
+  int32_t *refs, *table_out, *len_out, *src, *dst, *fill, *count, *status;
+  // workspace
+  uint32_t *bits;
+  int32_t *counts, *kids;
+  ForkRow *plan;
+};
+
+__device__ __forceinline__ int fork_parent(const ForkParams &P, int r, bool tell) {
+  if (!P.parents) return r;
+  const int p = ld_int(P.parents + r);
+  if (p == -1) return -1;
+  if (p < 0 || p >= P.per_in) {
+    if (tell) set_status(P.status, SD_STATUS_BAD_PARENT);
+    return -1;
+  }
+  return r / P.per_out * P.per_in + p;
+}
+
+struct ForkSpan {
+  int full, part, used, need;   // slots: full pages, entries of the last, all, with room
+  bool cut;                     // the table bounds the room
+  __device__ __forceinline__ ForkSpan(const ForkParams &P, int len) {
+    full = len / P.page_size;
+    part = len - full * P.page_size;
+    used = full + (part > 0);
+    const int64_t want = ((int64_t)len + P.append + P.page_size - 1) / P.page_size;
+    cut = want > P.M;
+    need = (int)min(want, (int64_t)P.M);
+  }
+};
+
+// The rows' plan, by one CTA: heirs, and the ranks of the pages and copies that
+// the rows need.
+__device__ void plan_rows(const ForkParams &P, int *smem) {
+  constexpr int NT = kPgNT, NW = NT / 32;
+  int *first = smem, *kids = smem + P.rows_in;   // of each old row
+  __shared__ unsigned long long warp_sum_s[NW];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int p = tid; p < P.rows_in; p += NT) {
+    first[p] = INT32_MAX;
+    kids[p] = 0;
+  }
+  __syncthreads();
+  for (int r = tid; r < P.R; r += NT) {
+    const int p = fork_parent(P, r, true);
+    if (p < 0) continue;
+    atomicMin(&first[p], r);
+    atomicAdd(&kids[p], 1);
+  }
+  __syncthreads();
+  for (int p = tid; p < P.rows_in; p += NT) P.kids[p] = kids[p];
+  unsigned long long before = 0ull;   // pages, and copies in the upper half
+  for (int r0 = 0; r0 < P.R; r0 += NT) {
+    const int r = r0 + tid;
+    ForkRow row = {-1, 0, 0, 0, 0, 0, 0, -1};
+    if (r < P.R) row.parent = fork_parent(P, r, false);
+    if (row.parent >= 0) {
+      const int p = row.parent;
+      row.len = (int)min((int64_t)max(ld_int(P.kv_len + p), 0), (int64_t)P.M * P.page_size);
+      const ForkSpan s(P, row.len);
+      const int32_t *old = P.table + (int64_t)p * P.M;
+      const bool lead = first[p] == r, heir = lead && !P.keep;
+      row.kids = kids[p];
+      row.flags = (lead ? kLead : 0) | (heir ? kHeir : 0);
+      if (s.cut) set_status(P.status, SD_STATUS_NO_PAGE);
+      if (s.part) {
+        row.last = ld_int(old + s.full);
+        if ((unsigned)row.last < (unsigned)P.N && !(heir && ld_int(P.refs + row.last) == 1)) {
+          row.flags |= kCopy;
+          row.pages = 1;
+        }
+      }
+      if (heir) {
+#pragma unroll 4
+        for (int j = s.used; j < s.need; ++j) row.pages += (unsigned)ld_int(old + j) >= (unsigned)P.N;
+      } else {
+        row.pages += s.need - s.used;
+      }
+    }
+    // the rows before this one
+    const unsigned long long mine =
+        (unsigned)row.pages | (unsigned long long)((row.flags & kCopy) != 0) << 32;
+    unsigned long long x = mine;
+    __syncwarp();
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
+      x += lane >= o ? y : 0ull;
+    }
+    if (lane == 31) warp_sum_s[warp] = x;
+    __syncthreads();
+    unsigned long long all = 0ull, at = before + x - mine;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      at += i < warp ? warp_sum_s[i] : 0ull;
+      all += warp_sum_s[i];
+    }
+    before += all;
+    row.first = (int)(unsigned)at;
+    row.pair = (int)(at >> 32);
+    if (r < P.R) P.plan[r] = row;
+    __syncthreads();
+  }
+  if (tid == 0) *P.count = (int)(before >> 32);
+}
+
+__global__ void __launch_bounds__(kPgNT) sd_kv_plan_kernel(const ForkParams P) {
+  extern __shared__ int plan_smem[];
+  pdl();
+  if (blockIdx.x == 0) plan_rows(P, plan_smem);
+  else chunk_bits(blockIdx.x - 1, P.N, P.refs, true, P.bits, P.counts);
+}
+
+// Calls f(rank, page) for the free pages of ranks [q, end), by one warp; returns
+// the first rank that there is none for (end if there are all).
+template <typename F>
+__device__ __forceinline__ int free_pages(const uint32_t *bits, const int32_t *counts, int nchunk,
+                                          int q, int end, F f) {
+  const int lane = threadIdx.x & 31;
+  int before = 0;   // free pages before chunk c0
+  for (int c0 = 0; c0 < nchunk && q < end; c0 += 32) {
+    const int n = c0 + lane < nchunk ? ld_int(counts + c0 + lane) : 0;
+    int upto = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      upto += lane >= o ? y : 0;
+    }
+    const int all = __shfl_sync(0xffffffffu, upto, 31);
+    while (q < end && q < before + all) {
+      // the chunk that holds rank q
+      const int k = __popc(__ballot_sync(0xffffffffu, before + upto <= q));
+      const int start = before + __shfl_sync(0xffffffffu, upto - n, k);
+      const int stop = before + __shfl_sync(0xffffffffu, upto, k);
+      const uint4 *w = reinterpret_cast<const uint4 *>(bits + (int64_t)(c0 + k) * kPgWords);
+      const uint4 a = ld16(w + lane * 2), b = ld16(w + lane * 2 + 1);
+      const uint32_t word[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      int here = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) here += __popc(word[i]);
+      int rank = here;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, rank, o);
+        rank += lane >= o ? y : 0;
+      }
+      rank += start - here;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int more = __popc(word[i]);
+        if (rank + more > q && rank < end) {
+          uint32_t m = word[i];
+          for (int at = rank; m && at < end; ++at, m &= m - 1)
+            if (at >= q) f(at, (c0 + k) * kPgChunk + (lane * 8 + i) * 32 + __ffs(m) - 1);
+        }
+        rank += more;
+      }
+      q = min(end, stop);
+      __syncwarp();
+    }
+    before += all;
+  }
+  return q;
+}
+
+__global__ void __launch_bounds__(kRowNT) sd_kv_rows_kernel(const ForkParams P) {
+  __shared__ int slots[kRowSlots];
+  pdl();
+  const int i = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+  unsigned bad = 0u;
+  if (i < P.R) {
+    const ForkRow row = P.plan[i];
+    const ForkSpan s(P, row.len);
+    const bool in_place = !P.parents, heir = row.flags & kHeir, copy = row.flags & kCopy;
+    const int32_t *old = P.table + (int64_t)row.parent * P.M;
+    int32_t *out = P.table_out + (int64_t)i * P.M;
+    // whoever leads a parent's rows counts for all of them
+    const int add = !(row.flags & kLead) ? 0 : P.keep ? row.kids : row.kids - 1;
+    if (row.parent < 0) {
+      for (int j = tid; j < P.M; j += kRowNT) out[j] = -1;
+    } else {
+      for (int j = tid; j < P.M; j += kRowNT) {
+        if (in_place && j != s.full) {
+          if (j < s.full && (unsigned)ld_int(old + j) >= (unsigned)P.N) bad |= SD_STATUS_BAD_PAGE;
+          continue;
+        }
+        const int e = ld_int(old + j);
+        const bool page = (unsigned)e < (unsigned)P.N;
+        int to = e;
+        if (j < s.full) {
+          if (!page) bad |= SD_STATUS_BAD_PAGE;
+          else if (add) atomicAdd(P.refs + e, add);
+        } else if (j < s.used) {
+          if (!page) bad |= SD_STATUS_BAD_PAGE;
+          if (copy) {
+            if (heir && !give_back(P.refs, e)) bad |= SD_STATUS_BAD_PAGE;
+            continue;   // gets a page below
+          }
+        } else if (j < s.need) {
+          if (!(heir && page)) continue;   // gets a page below
+        } else if (!heir) {
+          to = -1;
+        }
+        if (!in_place) out[j] = to;
+      }
+    }
+    if (tid == 0 && P.len_out) P.len_out[i] = row.len;
+    if (tid < 32 && row.pages > 0) {
+      // slots that get a page, in order, a batch at a time
+      if (copy && lane == 0) P.fill[row.pair] = s.part;
+      int j0 = s.used, done = 0;
+      bool first = copy;
+      while (done < row.pages) {
+        int n = 0;
+        if (first) {
+          if (lane == 0) slots[0] = s.full;
+          n = 1;
+        }
+        for (; j0 < s.need && n + 32 <= kRowSlots; j0 += 32) {
+          const int j = j0 + lane;
+          const int e = j < s.need && heir ? ld_int(old + j) : -1;
+          const bool want = j < s.need && (unsigned)e >= (unsigned)P.N;
+          if (want && e != -1) bad |= SD_STATUS_BAD_PAGE;
+          const unsigned m = __ballot_sync(0xffffffffu, want);
+          if (want) slots[n + __popc(m & ((1u << lane) - 1u))] = j;
+          n += __popc(m);
+        }
+        __syncwarp();
+        if (n == 0) break;
+        const int q = row.first + done;
+        const int got = free_pages(P.bits, P.counts, P.nchunk, q, q + n, [&](int rank, int page) {
+          out[slots[rank - q]] = page;
+          P.refs[page] = 1;
+          if (first && rank == q) {
+            P.src[row.pair] = row.last;
+            P.dst[row.pair] = page;
+          }
+        });
+        for (int x = got - q + lane; x < n; x += 32) {   // none left
+          out[slots[x]] = -1;
+          bad |= SD_STATUS_NO_PAGE;
+          if (first && x == 0) {
+            P.src[row.pair] = -1;
+            P.dst[row.pair] = -1;
+          }
+        }
+        __syncwarp();
+        done += n;
+        first = false;
+      }
+    }
+    if (tid == 32 && i >= ld_int(P.count)) {
+      P.src[i] = -1;
+      P.dst[i] = -1;
+      P.fill[i] = 0;
+    }
+  }
+  if (i < P.rows_in && !P.keep && ld_int(P.kids + i) == 0) {   // ends without an heir
+    for (int j = tid; j < P.M; j += kRowNT) {
+      const int e = ld_int(P.table + (int64_t)i * P.M + j);
+      if (e == -1) continue;
+      if ((unsigned)e >= (unsigned)P.N || !give_back(P.refs, e)) bad |= SD_STATUS_BAD_PAGE;
+    }
+  }
+  if (bad) set_status(P.status, bad);
+}
+
+// ------------------------------------------------------------------- free --
+constexpr int kFreeNT = 256, kFreeU = 4;
+
+__global__ void __launch_bounds__(kFreeNT) sd_kv_free_kernel(int64_t cols, int parts, int32_t *pages,
+                                                             const uint8_t *which,
+                                                             const int32_t *count, int clear, int N,
+                                                             int32_t *refs, int32_t *status) {
+  pdl();
+  const int64_t row = blockIdx.x / parts;
+  const int64_t c0 = (int64_t)(blockIdx.x % parts) * (kFreeNT * kFreeU) + threadIdx.x;
+  if (which && !ld1(which + row)) return;
+  int64_t end = cols;
+  if (count) end = min(end, (int64_t)ld_int(count) - row * cols);
+  int e[kFreeU];
+#pragma unroll
+  for (int u = 0; u < kFreeU; ++u) {
+    const int64_t c = c0 + u * kFreeNT;
+    e[u] = c < end ? ld_int(pages + row * cols + c) : -1;
+  }
+  bool bad = false;
+#pragma unroll
+  for (int u = 0; u < kFreeU; ++u) {
+    if (e[u] == -1) continue;
+    bad |= (unsigned)e[u] >= (unsigned)N || !give_back(refs, e[u]);
+    if (clear) pages[row * cols + c0 + u * kFreeNT] = -1;
+  }
+  if (bad) set_status(status, SD_STATUS_BAD_PAGE);
+}
+
+// ---------------------------------------------------------------- compact --
+struct CompactParams {
+  int N, nchunk;
+  int64_t n_table;
+  int32_t *refs, *table, *src, *dst, *count, *live, *new_ids, *status;
+  // workspace: bits of the pages in use, counts per chunk, pages in use before
+  // each word; pages in use, those below that many, and the moves
+  uint32_t *bits;
+  int32_t *counts, *before, *meta;
+};
+
+__global__ void __launch_bounds__(kPgNT) sd_kv_live_kernel(const CompactParams P) {
+  pdl();
+  chunk_bits(blockIdx.x, P.N, P.refs, false, P.bits, P.counts);
+}
+
+// The block's sum, in every thread.
+__device__ __forceinline__ int block_sum(int v, int *warps) {
+  __syncwarp();
+  v = __reduce_add_sync(0xffffffffu, v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0;
+#pragma unroll
+  for (int i = 0; i < kPgNT / 32; ++i) v += warps[i];
+  return v;
+}
+
+// Of page p: how many pages in use lie before it.
+__device__ __forceinline__ int used_before(const CompactParams &P, int p, uint32_t word) {
+  return ld_int(P.before + (p >> 5)) + __popc(word & ((1u << (p & 31)) - 1u));
+}
+
+// A page in use at or above L is the source of move `used before it` - `used
+// before L`, a free one below L the destination of move `free before it`.
+__global__ void __launch_bounds__(kPgNT) sd_kv_moves_kernel(const CompactParams P) {
+  __shared__ int warps[kPgNT / 32];
+  __shared__ int before_s[kPgWords];
+  pdl();
+  const int chunk = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int all = 0, ahead = 0;
+  for (int c = tid; c < P.nchunk; c += kPgNT) {
+    const int n = ld_int(P.counts + c);
+    all += n;
+    ahead += c < chunk ? n : 0;
+  }
+  const int L = block_sum(all, warps);
+  ahead = block_sum(ahead, warps);
+  int low = 0;   // in use before page L
+  const int cL = L / kPgChunk;
+  for (int c = tid; c < min(cL, P.nchunk); c += kPgNT) low += ld_int(P.counts + c);
+  if (cL < P.nchunk && tid < kPgWords) {
+    const int bit0 = tid * 32, cut = L - cL * kPgChunk;
+    uint32_t w = ld4(P.bits + (int64_t)cL * kPgWords + tid);
+    if (bit0 + 32 > cut) w = bit0 >= cut ? 0u : w & ((1u << (cut - bit0)) - 1u);
+    low += __popc(w);
+  }
+  low = block_sum(low, warps);
+  // in use before each word of this chunk
+  const uint32_t word = tid < kPgWords ? ld4(P.bits + (int64_t)chunk * kPgWords + tid) : 0u;
+  int upto = __popc(word);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, upto, o);
+    upto += lane >= o ? y : 0;
+  }
+  __syncthreads();
+  if (lane == 31) warps[warp] = upto;
+  __syncthreads();
+  if (tid < kPgWords) {
+    int at = ahead + upto - __popc(word);
+    for (int i = 0; i < warp; ++i) at += warps[i];
+    before_s[tid] = at;
+    P.before[(int64_t)chunk * kPgWords + tid] = at;
+  }
+  __syncthreads();
+  for (int u = 0; u < kPgChunk / kPgNT; ++u) {
+    const int w = (u * kPgNT + tid) / 32, p = chunk * kPgChunk + u * kPgNT + tid;
+    const uint32_t bits = ld4(P.bits + (int64_t)chunk * kPgWords + w);
+    const int used = before_s[w] + __popc(bits & ((1u << lane) - 1u));
+    const bool live = bits >> lane & 1u;
+    if (p >= P.N) continue;
+    if (live && p >= L) P.src[used - low] = p;
+    if (!live && p < L) P.dst[p - used] = p;
+  }
+  if (chunk == 0 && tid == 0) {
+    *P.live = L;
+    *P.count = L - low;
+    P.meta[0] = L;
+    P.meta[1] = low;
+  }
+}
+
+__global__ void __launch_bounds__(256) sd_kv_moved_kernel(const CompactParams P) {
+  pdl();
+  const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+  const int L = ld_int(P.meta), low = ld_int(P.meta + 1);
+  if (i < P.N) {
+    const int p = (int)i;
+    const uint32_t word = ld4(P.bits + (p >> 5));
+    int to = -1;
+    if (word >> (p & 31) & 1u) {
+      to = p;
+      if (p >= L) {
+        to = ld_int(P.dst + used_before(P, p, word) - low);
+        P.refs[to] = ld_int(P.refs + p);
+        P.refs[p] = 0;
+      }
+    }
+    P.new_ids[p] = to;
+    if (p < P.N / 2 && p >= L - low) {
+      P.src[p] = -1;
+      P.dst[p] = -1;
+    }
+  }
+  if (i < P.n_table) {
+    const int e = ld_int(P.table + i);
+    if (e == -1) return;
+    const uint32_t word = (unsigned)e < (unsigned)P.N ? ld4(P.bits + (e >> 5)) : 0u;
+    if (!(word >> (e & 31) & 1u)) set_status(P.status, SD_STATUS_BAD_PAGE);
+    else if (e >= L) P.table[i] = ld_int(P.dst + used_before(P, e, word) - low);
+  }
+}
+
+// Programmatic dependents of the stream's previous kernel.
+struct PageLaunch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  PageLaunch(int64_t grid, int block, int smem, cudaStream_t s) {
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3(block, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+  PageLaunch(const PageLaunch &) = delete;
+};
+
+static size_t round16(size_t n) { return (n + 15) & ~(size_t)15; }
+
+}  // namespace sdv
+
+using namespace sdv;
+
+extern "C" size_t sd_kv_fork_workspace_size(int32_t rows_in, int32_t R, int32_t N) {
+  if (rows_in < 0 || rows_in > SD_MAX_ROWS || R < 0 || R > SD_MAX_ROWS || N < 1 ||
+      N > SD_MAX_PAGES)
+    return 0;
+  const size_t nchunk = (size_t)page_chunks(N);
+  return nchunk * kPgWords * 4 + sizeof(ForkRow) * (size_t)R + round16(4 * nchunk) +
+         round16(4 * (size_t)rows_in);
+}
+
+extern "C" sd_status_t sd_kv_fork(const sd_kv_fork_args *a, void *stream) {
+  sdv::NvtxRange nvtx_range("sd_kv_fork");
+  if (!a) return SD_ERR_INVALID_ARG;
+  const size_t need = sd_kv_fork_workspace_size(a->rows_in, a->R, a->N);
+  if (need == 0 || a->max_pages < 0 || a->page_size < 1 || a->append < 0 || a->groups < 0 ||
+      (a->keep != 0 && a->keep != 1))
+    return SD_ERR_INVALID_ARG;
+  if ((int64_t)a->max_pages * a->page_size > INT32_MAX) return SD_ERR_INVALID_ARG;
+  const bool in_place = !a->parents;
+  if (in_place && a->R > 0 && (a->R != a->rows_in || a->table_out != a->table || a->keep || a->len_out))
+    return SD_ERR_INVALID_ARG;
+  if (a->groups > 0 && (a->R % a->groups || a->rows_in % a->groups)) return SD_ERR_INVALID_ARG;
+  if (!a->count || !a->refs || !a->workspace || (uintptr_t)a->workspace % 16 ||
+      a->workspace_bytes < need)
+    return SD_ERR_INVALID_ARG;
+  if (a->R > 0 && (!a->src || !a->dst || !a->fill || (!in_place && !a->len_out)))
+    return SD_ERR_INVALID_ARG;
+  if ((a->rows_in > 0 && !a->kv_len) ||
+      (a->max_pages > 0 && ((a->rows_in > 0 && !a->table) || (a->R > 0 && !a->table_out))))
+    return SD_ERR_INVALID_ARG;
+  ForkParams P = {};
+  P.rows_in = a->rows_in;
+  P.R = a->R;
+  P.per_in = a->groups > 0 ? a->rows_in / a->groups : a->rows_in;
+  P.per_out = std::max(1, a->groups > 0 ? a->R / a->groups : a->R);
+  P.M = a->max_pages;
+  P.page_size = a->page_size;
+  P.append = a->append;
+  P.keep = a->keep;
+  P.N = a->N;
+  P.nchunk = page_chunks(a->N);
+  P.parents = a->parents;
+  P.table = a->table;
+  P.kv_len = a->kv_len;
+  P.refs = a->refs;
+  P.table_out = a->table_out;
+  P.len_out = a->len_out;
+  P.src = a->src;
+  P.dst = a->dst;
+  P.fill = a->fill;
+  P.count = a->count;
+  P.status = a->status;
+  uint8_t *ws = static_cast<uint8_t *>(a->workspace);
+  P.bits = reinterpret_cast<uint32_t *>(ws);
+  ws += (size_t)P.nchunk * kPgWords * 4;
+  P.plan = reinterpret_cast<ForkRow *>(ws);
+  ws += sizeof(ForkRow) * (size_t)P.R;
+  P.counts = reinterpret_cast<int32_t *>(ws);
+  P.kids = reinterpret_cast<int32_t *>(ws + round16(4 * (size_t)P.nchunk));
+  static FuncAttrs attrs;
+  attrs.apply((const void *)sd_kv_plan_kernel, 8 * SD_MAX_ROWS, false, "the fork's plan kernel");
+  cudaStream_t s = (cudaStream_t)stream;
+  PageLaunch plan(1 + P.nchunk, kPgNT, 8 * P.rows_in, s);
+  cudaError_t e = cudaLaunchKernelEx(&plan.cfg, sd_kv_plan_kernel, P);
+  const int rows = std::max(P.R, P.rows_in);
+  if (e == cudaSuccess && rows > 0) {
+    PageLaunch each(rows, kRowNT, 0, s);
+    e = cudaLaunchKernelEx(&each.cfg, sd_kv_rows_kernel, P);
+  }
+  return e == cudaSuccess ? SD_OK : SD_ERR_CUDA;
+}
+
+extern "C" sd_status_t sd_kv_free(int64_t rows, int64_t cols, int32_t *pages, const uint8_t *which,
+                                  const int32_t *count, int32_t clear, int32_t N, int32_t *refs,
+                                  int32_t *status, void *stream) {
+  sdv::NvtxRange nvtx_range("sd_kv_free");
+  if (rows < 0 || cols < 0 || rows > INT32_MAX || cols > INT32_MAX || N < 1 || N > SD_MAX_PAGES)
+    return SD_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return SD_OK;
+  if (!pages || !refs) return SD_ERR_INVALID_ARG;
+  if (rows > INT64_MAX / 4 / cols) return SD_ERR_INVALID_ARG;
+  if (!which) {   // one long row
+    cols *= rows;
+    rows = 1;
+  }
+  const int64_t parts = (cols + kFreeNT * kFreeU - 1) / (kFreeNT * kFreeU);
+  if (parts > INT32_MAX / rows) return SD_ERR_INVALID_ARG;
+  PageLaunch launch(rows * parts, kFreeNT, 0, (cudaStream_t)stream);
+  const cudaError_t e = cudaLaunchKernelEx(&launch.cfg, sd_kv_free_kernel, cols, (int)parts, pages,
+                                           which, count, (int)clear, (int)N, refs, status);
+  return e == cudaSuccess ? SD_OK : SD_ERR_CUDA;
+}
+
+extern "C" size_t sd_kv_compact_workspace_size(int32_t N) {
+  if (N < 1 || N > SD_MAX_PAGES) return 0;
+  const size_t nchunk = (size_t)page_chunks(N);
+  return nchunk * kPgWords * 8 + round16(4 * nchunk) + 16;
+}
+
+extern "C" sd_status_t sd_kv_compact(int32_t N, int32_t *refs, int64_t n_table, int32_t *table,
+                                     int32_t *src, int32_t *dst, int32_t *count, int32_t *live,
+                                     int32_t *new_ids, int32_t *status, void *workspace,
+                                     size_t workspace_bytes, void *stream) {
+  sdv::NvtxRange nvtx_range("sd_kv_compact");
+  const size_t need = sd_kv_compact_workspace_size(N);
+  if (need == 0 || n_table < 0 || n_table > (int64_t)INT32_MAX * 256) return SD_ERR_INVALID_ARG;
+  if (!refs || !count || !live || !new_ids || (N > 1 && (!src || !dst)) ||
+      (n_table > 0 && !table) || !workspace || (uintptr_t)workspace % 16 || workspace_bytes < need)
+    return SD_ERR_INVALID_ARG;
+  CompactParams P = {};
+  P.N = N;
+  P.nchunk = page_chunks(N);
+  P.n_table = n_table;
+  P.refs = refs;
+  P.table = table;
+  P.src = src;
+  P.dst = dst;
+  P.count = count;
+  P.live = live;
+  P.new_ids = new_ids;
+  P.status = status;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  P.bits = reinterpret_cast<uint32_t *>(ws);
+  ws += (size_t)P.nchunk * kPgWords * 4;
+  P.before = reinterpret_cast<int32_t *>(ws);
+  ws += (size_t)P.nchunk * kPgWords * 4;
+  P.counts = reinterpret_cast<int32_t *>(ws);
+  P.meta = reinterpret_cast<int32_t *>(ws + round16(4 * (size_t)P.nchunk));
+  cudaStream_t s = (cudaStream_t)stream;
+  PageLaunch chunks(P.nchunk, kPgNT, 0, s);
+  cudaError_t e = cudaLaunchKernelEx(&chunks.cfg, sd_kv_live_kernel, P);
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&chunks.cfg, sd_kv_moves_kernel, P);
+  if (e == cudaSuccess) {
+    PageLaunch each((std::max<int64_t>(N, n_table) + 255) / 256, 256, 0, s);
+    e = cudaLaunchKernelEx(&each.cfg, sd_kv_moved_kernel, P);
+  }
+  return e == cudaSuccess ? SD_OK : SD_ERR_CUDA;
+}
+
+extern "C" size_t sd_kv_fork_args_size(void) { return sizeof(sd_kv_fork_args); }

@@ -33,8 +33,6 @@ constexpr int kTopNW = kTopNT / 32;
 constexpr int kTopU = 4;          // vectors at a time per thread
 constexpr int kTopList = 1024;    // listed logits of a row
 
-constexpr float kLowest = -3.402823466e38f;
-
 struct TopParams {
   const void *logits;
   int64_t stride;
@@ -54,48 +52,6 @@ struct TopSum {
   float m, z;
   int listed;
 };
-
-__device__ __forceinline__ unsigned long long top_key(float x, int i) {
-  return ((unsigned long long)((unsigned)ford(x) ^ 0x80000000u) << 32) | (unsigned)~i;
-}
-__device__ __forceinline__ int key_index(unsigned long long key) { return (int)~(unsigned)key; }
-__device__ __forceinline__ float key_value(unsigned long long key) {
-  return fdeord((int)((unsigned)(key >> 32) ^ 0x80000000u));
-}
-
-// The upper 16 bits of a value's ordered image.
-__device__ __forceinline__ unsigned short top_key16(float x) {
-  return (unsigned short)(((unsigned)ford(x) ^ 0x80000000u) >> 16);
-}
-
-// The largest value (of the upper 16 bits' grid) that k of NT keys reach, found
-// by one warp bit by bit; kLowest where fewer are finite.
-template <int NT>
-__device__ __forceinline__ float top_bound_warp(const unsigned short *keys, int k) {
-  constexpr int J = NT / 32;
-  unsigned key[J], lo = 0xffffu, hi = 0u;
-#pragma unroll
-  for (int j = 0; j < J; ++j) {
-    key[j] = keys[j * 32 + (threadIdx.x & 31)];
-    lo = min(lo, key[j]);
-    hi = max(hi, key[j]);
-  }
-  lo = __reduce_min_sync(0xffffffffu, lo);
-  hi = __reduce_max_sync(0xffffffffu, hi);
-  // the bits that all have in common are known
-  const int from = 31 - __clz(lo ^ hi);
-  unsigned r = lo & ~((1u << (from + 1)) - 1u);
-#pragma unroll 1
-  for (int bit = from; bit >= 0; --bit) {
-    const unsigned t = r | (1u << bit);
-    int n = 0;
-#pragma unroll
-    for (int j = 0; j < J; ++j) n += key[j] >= t;
-    if (__reduce_add_sync(0xffffffffu, n) >= k) r = t;
-  }
-  // 0x007f is -inf's
-  return r > 0x007fu ? fdeord((int)((r << 16) ^ 0x80000000u)) : kLowest;
-}
 
 // Registers for one CTA per SM more than the rule for held rows counts on:
 // clusters of eight do not fill every group of SMs to the last place (57 rows
@@ -279,22 +235,6 @@ __global__ void __launch_bounds__(kTopNT, kHeldCtas + 1) sd_top_kernel(const Top
 // large logits at its end, or in a few threads' places) is gone over again
 // from memory.
 constexpr int kTopHeap = 2 * kTopList;   // listed vectors of a streamed row
-
-// top_bound_warp of the block's threads by their `best`, in every thread;
-// meanwhile() is what the threads do between its barriers.
-template <int NT, typename F>
-__device__ __forceinline__ float top_bound(float best, int k, unsigned short *keys, float *out,
-                                           F meanwhile) {
-  keys[threadIdx.x] = top_key16(best);
-  __syncthreads();
-  meanwhile();
-  if (threadIdx.x < 32) {
-    const float b = top_bound_warp<NT>(keys, k);
-    if (threadIdx.x == 0) *out = b;
-  }
-  __syncthreads();
-  return *out;
-}
 
 template <typename E>
 __global__ void __launch_bounds__(kStreamNT, 2) sd_top_stream_kernel(const TopParams P) {

@@ -1,0 +1,368 @@
+"""Binding of the page operators of a paged KV cache (C ABI in ``include/sd_kv.h``): forking and
+extending block tables, giving pages back, copying pages and moving the pages in use to the
+front of the pool.  kv_rollback truncates the same tables.
+
+A pool of N pages is refs [N] (int32): how many table entries hold each page; 0 is a free page.
+Like the rest of the package this module only checks and marshals arguments.
+
+  kv_fork(...), kv_extend(...)   sd_kv_fork
+  kv_free(...)                   sd_kv_free
+  kv_compact(...)                sd_kv_compact
+  kv_copy(...)                   sd_kv_copy
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+from typing import NamedTuple
+
+import torch
+
+from . import _P, _check, _need
+from .logits import _lib, _stream_of, _written
+
+SD_STATUS_BAD_PARENT, SD_STATUS_BAD_PAGE, SD_STATUS_NO_PAGE = 0x10, 0x20, 0x40
+SD_MAX_ROWS, SD_MAX_PAGES, SD_MAX_CACHES = 16384, 1 << 24, 256
+
+_I32, _U8 = torch.int32, torch.uint8
+
+
+class ForkArgs(ctypes.Structure):
+    """Mirror of ``sd_kv_fork_args`` in include/sd_kv.h."""
+    _fields_ = [
+        *((n, ctypes.c_int32) for n in ("rows_in", "R", "groups", "max_pages", "page_size",
+                                        "append", "keep", "N")),
+        ("parents", _P), ("table", _P), ("kv_len", _P), ("refs", _P), ("table_out", _P),
+        ("len_out", _P), ("src", _P), ("dst", _P), ("fill", _P), ("count", _P), ("status", _P),
+        ("workspace", _P), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class CopyArgs(ctypes.Structure):
+    """Mirror of ``sd_kv_copy_args`` in include/sd_kv.h."""
+    _fields_ = [
+        *((n, ctypes.c_int32) for n in ("n_caches", "layers", "N", "parts", "page_size")),
+        ("entry_bytes", ctypes.c_int64), ("layer_stride", ctypes.c_int64),
+        ("page_stride", ctypes.c_int64), ("caches", _P), ("pairs", ctypes.c_int32), ("src", _P),
+        ("dst", _P), ("fill", _P), ("count", _P), ("status", _P),
+    ]
+
+
+class KVFork(NamedTuple):
+    block_table: torch.Tensor   # [R][max_pages] int32
+    kv_len: torch.Tensor        # [R] int32
+    src: torch.Tensor           # [R] int32: pages to copy from, -1 after the last
+    dst: torch.Tensor           # [R] int32: and to
+    fill: torch.Tensor          # [R] int32: entries of each to copy
+    count: torch.Tensor         # [1] int32: how many pairs
+
+
+class KVMoves(NamedTuple):
+    src: torch.Tensor
+    dst: torch.Tensor
+    fill: torch.Tensor
+    count: torch.Tensor
+
+
+class KVCompact(NamedTuple):
+    src: torch.Tensor           # [N // 2] int32: pages that move, -1 after the last
+    dst: torch.Tensor           # [N // 2] int32: where to
+    count: torch.Tensor         # [1] int32: how many
+    new_ids: torch.Tensor       # [N] int32: where each page in use is now, -1: free
+    live: torch.Tensor          # [1] int32: pages in use, now [0, live)
+
+
+def _bind(L):
+    """Argument types of the entry points, and the structs' layouts."""
+    i32, i64, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    L.sd_kv_fork.argtypes = [ctypes.POINTER(ForkArgs), _P]
+    L.sd_kv_copy.argtypes = [ctypes.POINTER(CopyArgs), _P]
+    L.sd_kv_free.argtypes = [i64, i64, _P, _P, _P, i32, i32, _P, _P, _P]
+    L.sd_kv_compact.argtypes = [i32, _P, i64, _P, _P, _P, _P, _P, _P, _P, _P, sz, _P]
+    for fn in (L.sd_kv_fork, L.sd_kv_copy, L.sd_kv_free, L.sd_kv_compact):
+        fn.restype = ctypes.c_int
+    L.sd_kv_fork_workspace_size.argtypes = [i32, i32, i32]
+    L.sd_kv_compact_workspace_size.argtypes = [i32]
+    L.sd_kv_fork_workspace_size.restype = L.sd_kv_compact_workspace_size.restype = sz
+    for fn, mirror in ((L.sd_kv_fork_args_size, ForkArgs), (L.sd_kv_copy_args_size, CopyArgs)):
+        fn.argtypes, fn.restype = [], sz
+        if fn() != ctypes.sizeof(mirror):
+            raise RuntimeError(f"{mirror.__name__} layout differs between library and binding")
+
+
+def _on_device(fn):
+    """Runs a wrapper with its first tensor's device as the current one, and with `stream` (when
+    given) as the current stream: what it allocates belongs to the stream that it launches on."""
+    @functools.wraps(fn)
+    def call(*args, **kwargs):
+        t = args[0] if args else next(iter(kwargs.values()), None)
+        while isinstance(t, (list, tuple)) and t:
+            t = t[0]
+        stream = kwargs.get("stream")
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            return fn(*args, **kwargs)   # which says what is wrong
+        if stream is not None:
+            if stream.device != t.device:
+                raise ValueError(f"stream is on {stream.device}, expected {t.device}")
+            with torch.cuda.stream(stream):
+                return fn(*args, **kwargs)
+        if t.device.index != torch.cuda.current_device():
+            with torch.cuda.device(t.device):
+                return fn(*args, **kwargs)
+        return fn(*args, **kwargs)
+    return call
+
+
+def _i32(t, name, shape, device):
+    """The address of a contiguous int32 array; what is wrong with it is said by _need."""
+    if t is None or t.dtype is not _I32 or t.device != device or t.shape != shape \
+            or not t.is_contiguous():
+        _need(t, name, _I32, shape, device)
+    return t.data_ptr()
+
+
+def _span(t):
+    """The addresses that a tensor reaches over, or none."""
+    if not t.numel():
+        return 0, 0
+    return t.data_ptr(), t.data_ptr() + t.element_size() * (
+        1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))
+
+
+def _meet(a, b):
+    (a0, a1), (b0, b1) = _span(a), _span(b)
+    return a0 < b1 and b0 < a1
+
+
+def _pool(refs, device):
+    if refs.dim() != 1 or refs.numel() < 1:
+        raise ValueError("refs must be [N], with N >= 1")
+    return _i32(refs, "refs", refs.shape, device), refs.numel()
+
+
+def _table(block_table, kv_len):
+    _need(block_table, "block_table", _I32)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [rows][max_pages]")
+    rows, M = block_table.shape
+    return rows, M, _i32(kv_len, "kv_len", (rows,), block_table.device)
+
+
+def _workspace(n, device):
+    """Scratch of one call: the allocator's, so that calls and captured graphs share none."""
+    if n == 0:
+        raise ValueError("sizes out of range")
+    return torch.empty(n, dtype=_U8, device=device)
+
+
+def _fork(a, refs, status, dev):
+    a.refs, a.N = _pool(refs, dev)
+    if status is not None:
+        a.status = _i32(status, "status", (1,), dev)
+    a.workspace_bytes = _lib().sd_kv_fork_workspace_size(a.rows_in, a.R, a.N)
+    ws = _workspace(a.workspace_bytes, dev)
+    a.workspace = ws.data_ptr()
+    _check(_lib().sd_kv_fork(a, _stream_of(dev)), "sd_kv_fork")
+    _written(refs)
+
+
+@_on_device
+def kv_fork(block_table, kv_len, parents, refs, page_size: int, *, append: int = 0,
+            keep: bool = False, out: KVFork | None = None, status=None,
+            stream=None) -> KVFork:
+    """New rows from the rows of block_table [rows][max_pages] and kv_len [rows] (int32): row r
+    shares the pages of its parent and has room for `append` more entries; refs [N] is brought
+    up to date.  parents: int32 [R], rows of the table, or [B][k] relative to each of B groups of
+    rows (beam_select's, for a table of B W rows); -1 makes an empty row.
+
+    The old rows end with the call: pages that no new row holds are given back, and the first
+    row of each parent takes over what is the parent's own.  keep=True leaves the old rows as
+    they are.  Either way the partly filled last page of every new row is its own: kv_copy(caches,
+    f.src, f.dst, count=f.count, fill=f.fill) must follow before the rows are read."""
+    rows, M, lens = _table(block_table, kv_len)
+    dev = block_table.device
+    _need(parents, "parents", _I32, None, dev)
+    if parents.dim() not in (1, 2):
+        raise ValueError("parents must be [R] or [B][k]")
+    R = parents.numel()
+    groups = parents.shape[0] if parents.dim() == 2 else 0
+    if groups and rows % groups:
+        raise ValueError(f"{rows} rows are not {groups} groups")
+    a = ForkArgs(rows, R, groups, M, page_size, append, bool(keep))
+    if R == 0:
+        raise ValueError("parents must name at least one row")
+    if out is None:
+        t, n, src, dst, fill, count = torch.empty(R * M + 4 * R + 1, dtype=_I32, device=dev).split(
+            (R * M, R, R, R, R, 1))
+        out = KVFork(t.view(R, M), n, src, dst, fill, count)
+        given = False
+    else:
+        given = True
+        for x in (out.block_table, out.kv_len):
+            _need(x, "out", _I32, None, dev)
+            if any(_meet(x, y) for y in (block_table, kv_len, parents, refs)):
+                raise ValueError("out overlaps the input")
+    a.parents, a.table, a.kv_len = parents.data_ptr(), block_table.data_ptr(), lens
+    a.table_out = _i32(out.block_table, "out.block_table", (R, M), dev)
+    a.len_out = _i32(out.kv_len, "out.kv_len", (R,), dev)
+    a.src, a.dst, a.fill = (_i32(getattr(out, n), "out." + n, (R,), dev)
+                            for n in ("src", "dst", "fill"))
+    a.count = _i32(out.count, "out.count", (1,), dev)
+    _fork(a, refs, status, dev)
+    if given:
+        for t in out:
+            _written(t)
+    return out
+
+
+@_on_device
+def kv_extend(block_table, kv_len, refs, page_size: int, append: int, *, status=None,
+              stream=None) -> KVMoves:
+    """Room for `append` more entries in every row of block_table, in place: its rows get free
+    pages, and a partly filled last page that others hold too becomes the row's own (kv_copy of
+    the returned pairs must follow where rows may share one)."""
+    rows, M, lens = _table(block_table, kv_len)
+    dev = block_table.device
+    a = ForkArgs(rows, rows, 0, M, page_size, append, 0)
+    m = KVMoves(*torch.empty(3 * rows + 1, dtype=_I32, device=dev).split((rows, rows, rows, 1)))
+    a.table = a.table_out = block_table.data_ptr()
+    a.kv_len = lens
+    a.src, a.dst, a.fill, a.count = (t.data_ptr() for t in m)
+    _fork(a, refs, status, dev)
+    _written(block_table)
+    return m
+
+
+@_on_device
+def kv_free(pages, refs, *, which=None, count=None, clear: bool = False, status=None,
+            stream=None) -> torch.Tensor:
+    """Gives pages back to refs [N], in place: the ids in pages (int32, any shape; -1 is passed
+    over), as kv_rollback lists them (pages=freed, count=free_offsets[-1:]), or the rows of a
+    block table (which [rows] uint8: those whose flag is set).  clear=True makes the entries that
+    are taken -1."""
+    _need(pages, "pages", _I32)
+    dev = pages.device
+    ref, N = _pool(refs, dev)
+    if _meet(pages, refs):
+        raise ValueError("pages overlaps refs")
+    rows, cols, w, n, st = 1, pages.numel(), None, None, None
+    if which is not None:
+        if pages.dim() != 2:
+            raise ValueError("which needs pages [rows][max_pages]")
+        rows, cols = pages.shape
+        _need(which, "which", _U8, (rows,), dev)
+        w = which.data_ptr() if rows else None
+    if count is not None:
+        n = _i32(count, "count", (1,), dev)
+    if status is not None:
+        st = _i32(status, "status", (1,), dev)
+    _check(_lib().sd_kv_free(rows, cols, pages.data_ptr(), w, n, bool(clear), N, ref, st,
+                             _stream_of(dev)), "sd_kv_free")
+    _written(refs)
+    if clear:
+        _written(pages)
+    return refs
+
+
+@_on_device
+def kv_compact(refs, block_table=None, *, status=None, stream=None) -> KVCompact:
+    """Moves the pages in use to the front of the pool: refs [N] and the entries of block_table
+    (int32, any shape) are brought up to date in place; kv_copy(caches, c.src, c.dst,
+    count=c.count) must follow before the pages are read.  Other tables of the same pool take
+    their ids from new_ids."""
+    _need(refs, "refs", _I32)
+    dev = refs.device
+    ref, N = _pool(refs, dev)
+    h = N // 2
+    new, src, dst, count, live = torch.empty(N + 2 * h + 2, dtype=_I32, device=dev).split(
+        (N, h, h, 1, 1))
+    table, n_table, st = None, 0, None
+    if block_table is not None:
+        _need(block_table, "block_table", _I32, None, dev)
+        if _meet(block_table, refs):
+            raise ValueError("block_table overlaps refs")
+        n_table = block_table.numel()
+        table = block_table.data_ptr() if n_table else None
+    if status is not None:
+        st = _i32(status, "status", (1,), dev)
+    need = _lib().sd_kv_compact_workspace_size(N)
+    ws = _workspace(need, dev)
+    _check(_lib().sd_kv_compact(N, ref, n_table, table, src.data_ptr(), dst.data_ptr(),
+                                count.data_ptr(), live.data_ptr(), new.data_ptr(), st,
+                                ws.data_ptr(), need, _stream_of(dev)), "sd_kv_compact")
+    _written(refs)
+    if n_table:
+        _written(block_table)
+    return KVCompact(src, dst, count, new, live)
+
+
+def _page_shape(shape, strides, size, first, name):
+    """Whether the dimensions from `first` on lie contiguous."""
+    want = 1
+    for n, s in zip(reversed(shape[first:]), reversed(strides[first:])):
+        if n > 1 and s != want:
+            raise ValueError(f"{name}: a page must be contiguous")
+        want *= n
+    return want * size
+
+
+@_on_device
+def kv_copy(caches, src, dst, *, count=None, fill=None, heads_first: bool = False, status=None,
+            stream=None) -> None:
+    """Copies page src[i] to page dst[i] (int32 [pairs], the first count [1] of them; -1, -1 is
+    passed over) in every cache, in place.  caches: one tensor [layers][N][...] or a sequence of
+    [N][...] of one shape (keys and values of every layer), any type.  fill [pairs]: only the
+    first fill[i] entries of each page, for pages [page_size][...], or with heads_first
+    [heads][page_size][...].  No page may be both a source and a destination, and none twice a
+    destination."""
+    one = isinstance(caches, torch.Tensor)
+    if one:
+        if caches.dim() < 3:
+            raise ValueError("caches must be [layers][N][...]")
+        base, lead = caches, 1
+        layers, tensors = caches.shape[0], (caches,)
+    else:
+        tensors = tuple(caches)
+        if not tensors:
+            return
+        if len(tensors) > SD_MAX_CACHES:
+            raise ValueError(f"at most {SD_MAX_CACHES} caches")
+        base, lead, layers = tensors[0], 0, 1
+        if base.dim() < 2:
+            raise ValueError("each cache must be [N][...]")
+    dev, shape, strides, size = base.device, base.shape, base.stride(), base.element_size()
+    for t in tensors:
+        if not t.is_cuda:
+            raise ValueError("caches must be CUDA tensors")
+        if t.device != dev or t.shape != shape or t.stride() != strides or t.dtype != base.dtype:
+            raise ValueError("caches must be alike in shape, type, strides and device")
+    page = _page_shape(shape, strides, size, lead + 1, "caches")
+    for d in range(lead + 1):
+        if shape[d] > 1 and strides[d] == 0:
+            raise ValueError("caches must not be expanded")
+    at = lead + 2 if heads_first else lead + 1
+    if fill is not None and len(shape) <= at:
+        raise ValueError("fill needs pages of [page_size][...], or [heads][page_size][...]")
+    parts, entries = 1, 1
+    if fill is not None:
+        entries = shape[at]
+        parts = shape[lead + 1] if heads_first else 1
+    if page == 0 or shape[lead] == 0 or layers == 0:
+        return
+    a = CopyArgs(len(tensors), layers, shape[lead], parts, entries, page // (parts * entries),
+                 strides[0] * size if one else 0, strides[lead] * size)
+    a.caches = ctypes.cast((ctypes.c_void_p * len(tensors))(*(t.data_ptr() for t in tensors)), _P)
+    _need(src, "src", _I32, None, dev)
+    if src.dim() != 1:
+        raise ValueError("src must be [pairs]")
+    a.pairs = src.shape[0]
+    a.src, a.dst = src.data_ptr(), _i32(dst, "dst", src.shape, dev)
+    if fill is not None:
+        a.fill = _i32(fill, "fill", src.shape, dev)
+    if count is not None:
+        a.count = _i32(count, "count", (1,), dev)
+    if status is not None:
+        a.status = _i32(status, "status", (1,), dev)
+    _check(_lib().sd_kv_copy(a, _stream_of(dev)), "sd_kv_copy")
+    for t in tensors:
+        _written(t)
