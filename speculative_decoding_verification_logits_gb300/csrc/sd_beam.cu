@@ -2,15 +2,14 @@
 // over W rows of V logits, by two launches.
 //
 //  1. sd_beam_stream_kernel: every CTA takes one chunk of a row, held in
-//     registers.  It writes the chunk's (largest m, sum of 2^((x - m) c)) and, per
-//     thread, the largest of the thread's own vectors (a group).  No beam's row
-//     is read twice, and nothing depends on other CTAs.
+//     registers.  It writes the chunk's (largest m, sum of 2^((x - m) c)) and the
+//     largest logit of every four threads' vectors (a group).  No beam's row is
+//     read twice, and nothing depends on other CTAs.
 //  2. sd_beam_end_kernel: one CTA per sequence joins the sums of each beam in 64
 //     bits, and finds from the groups' largest logits alone a value that k of
 //     them reach: no candidate below it is among the k best.  The groups that
-//     reach it (about k of them) are read again, their logits that do are ranked
-//     in 64 bits.
-// The groups' largest are 1 / 64 of the row in bf16 and 1 / 32 in fp32.
+//     reach it (little more than k of them) are read again, their logits that
+//     do are ranked in 64 bits.
 // A sequence of which more groups or logits reach the bound than there is room
 // for (thousands of equal logits at the k-th place) takes its beams one by one:
 // see each_beam.
@@ -21,7 +20,10 @@
 namespace sdv {
 
 constexpr int kSelNT = 256;      // threads of a streaming CTA
+constexpr int kSelSet = 4;       // threads of a group
+constexpr int kSelSets = kSelNT / kSelSet;
 constexpr int kEndNT = 512;      // threads of a sequence's end
+constexpr int kEndU = 4;         // vectors of groups that one of them holds
 constexpr int kSelList = 1024;   // listed groups, and candidates, of a sequence
 
 struct SelectParams {
@@ -29,10 +31,11 @@ struct SelectParams {
   int64_t sb, sw;
   int B, W, V, k, nc, share, eos;
   float T;
+  double inv_T;
   const float *scores, *norm;
   const uint8_t *finished;
   float2 *part;      // [B W][nc]: largest logit of a chunk and its sum
-  void *gmax;        // [B W][nc][kSelNT]: largest logit of each thread, in the logits' type
+  float *gmax;       // [B W][nc][kSelSets]: largest logit of each group
   float *out_scores;
   int32_t *parents, *tokens;
   uint8_t *ended;
@@ -148,8 +151,11 @@ __global__ void __launch_bounds__(kSelNT) sd_beam_stream_kernel(const SelectPara
   }
   __shared__ float wm[NW], wz[NW];
   const float best = VecExp<E>::template largest<U>(v);
-  Row<E>::store(reinterpret_cast<uint8_t *>(P.gmax), ((int64_t)n * P.nc + chunk) * NT + tid, best);
-  float m = rmax_f(best);
+  float m = best;
+#pragma unroll
+  for (int o = 1; o < kSelSet; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (tid % kSelSet == 0) P.gmax[((int64_t)n * P.nc + chunk) * kSelSets + tid / kSelSet] = m;
+  m = rmax_f(m);
   if ((tid & 31) == 0) wm[tid >> 5] = m;
   __syncthreads();
 #pragma unroll
@@ -188,10 +194,11 @@ struct SelectEnd {
   // a beam: 0 offers nothing, 1 live, 2 finished; its score less the log of its sum
   int kind[SD_MAX_BEAMS];
   double base[SD_MAX_BEAMS];
-  double norm[SD_MAX_BEAMS];
+  double over[SD_MAX_BEAMS];          // 1 / norm
+  double z[SD_MAX_BEAMS];
   // an fp32 image of the ranked score: max((x - m) c + o, lowest)
   float m[SD_MAX_BEAMS], c[SD_MAX_BEAMS], o[SD_MAX_BEAMS];
-  int list[kSelList];                 // groups: beam, chunk, thread
+  int list[kSelList];                 // groups: beam, chunk, place
   unsigned long long key[kSelList];   // candidates: their order,
   int at[kSelList];                   // w V + v,
   float x[kSelList];                  // and logit
@@ -215,26 +222,28 @@ struct EndView {
   __device__ __forceinline__ ElemRow<E> row(int w) const {
     return ElemRow<E>(P.logits, b * P.sb + w * P.sw, P.V);
   }
-  __device__ __forceinline__ const uint8_t *groups(int w) const {
-    return reinterpret_cast<const uint8_t *>(P.gmax) +
-           ((int64_t)b * P.W + w) * P.nc * kSelNT * Elt<E>::kSize;
+  __device__ __forceinline__ const float *groups(int w) const {
+    return P.gmax + ((int64_t)b * P.W + w) * P.nc * kSelSets;
   }
-  // the row's vector that is number u of group g, or -1
-  __device__ __forceinline__ int vector(const ElemRow<E> &r, int g, int u) const {
-    const int chunk = g / kSelNT, q = chunk * P.share + g % kSelNT + u * kSelNT;
-    return q < min((chunk + 1) * P.share, r.nvec) ? q : -1;
+  // vectors of a group, and the row's vector that is number i of group g, or -1
+  __device__ __forceinline__ int size() const { return kSelSet * U; }
+  __device__ __forceinline__ int vector(const ElemRow<E> &r, int g, int i) const {
+    const int chunk = g / kSelSets;
+    const int at = g % kSelSets * kSelSet + i % kSelSet + i / kSelSet * kSelNT;
+    const int q = chunk * P.share + at;
+    return at < P.share && q < r.nvec ? q : -1;
   }
   __device__ __forceinline__ float approx(int w, float x) const {
     return x > neg_inf() ? fmaxf(fmaf(x - S.m[w], S.c[w], S.o[w]), kLowest) : neg_inf();
   }
   __device__ __forceinline__ double score(int w, float x) const {
     return S.kind[w] == 2 ? S.base[w]
-                          : S.base[w] + ((double)x - (double)S.m[w]) / (double)P.T;
+                          : S.base[w] + ((double)x - (double)S.m[w]) * P.inv_T;
   }
   __device__ __forceinline__ void offer(int w, int v, float x) const {
     const int i = atomicAdd(&S.n_cand, 1);
     if (i < kSelList) {
-      S.key[i] = dord(score(w, x) / S.norm[w]);
+      S.key[i] = dord(score(w, x) * S.over[w]);
       S.at[i] = w * P.V + v;
       S.x[i] = x;
     }
@@ -311,37 +320,27 @@ __device__ __noinline__ void each_beam(const EndView<E> &X) {
       continue;
     }
     const ElemRow<E> row = X.row(w);
-    const uint8_t *gm = X.groups(w);
-    const int nvg = P.nc * kSelNT / VE;
+    const float *gm = X.groups(w);
+    const int ng = P.nc * kSelSets;
     const unsigned low = (unsigned)ford(kLowest) ^ 0x80000000u;
     unsigned r = 0u;
     for (int bit = 31; bit >= 0; --bit) {
       const unsigned t = r | (1u << bit);
       int n = 0;
-      for (int i = tid; i < nvg; i += NT) {
-        float f[VE];
-        Elt<E>::unpack(ld16(gm + (int64_t)i * 16), f);
-#pragma unroll
-        for (int e = 0; e < VE; ++e) n += ((unsigned)ford(f[e]) ^ 0x80000000u) >= t;
-      }
+      for (int i = tid; i < ng; i += NT) n += ((unsigned)ford(ld_float(gm + i)) ^ 0x80000000u) >= t;
       if (block_count(S, n) >= k) r = t;
     }
     const float least = fdeord((int)(max(r, low) ^ 0x80000000u));
-    for (int i = tid; i < nvg; i += NT) {
-      float f[VE];
-      Elt<E>::unpack(ld16(gm + (int64_t)i * 16), f);
-#pragma unroll
-      for (int e = 0; e < VE; ++e)
-        if (f[e] > least) {   // fewer than k
-          const int at = atomicAdd(&S.n_list, 1);
-          if (at < kSelList) S.list[at] = i * VE + e;
-        }
-    }
+    for (int i = tid; i < ng; i += NT)
+      if (ld_float(gm + i) > least) {   // fewer than k
+        const int at = atomicAdd(&S.n_list, 1);
+        if (at < kSelList) S.list[at] = i;
+      }
     __syncthreads();
-    const int items = min(S.n_list, kSelList) * X.U;
+    const int items = min(S.n_list, kSelList) * X.size();
     auto above = [&](unsigned long long from, auto f) {
       for (int i = tid; i < items; i += NT) {
-        const int q = X.vector(row, S.list[i / X.U], i % X.U);
+        const int q = X.vector(row, S.list[i / X.size()], i % X.size());
         if (q < 0) continue;
         float x[VE];
         Elt<E>::unpack(row.load(q), x);
@@ -412,9 +411,18 @@ __global__ void __launch_bounds__(kEndNT) sd_beam_end_kernel(const SelectParams 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) S.n_list = S.n_cand = 0;
+  // the groups' largest, kEndU vectors of four per thread at a time
+  const int per = P.nc * kSelSets / 4, all = W * per;
+  const float *gm = X.groups(0);
+  uint4 held[kEndU];
+#pragma unroll
+  for (int u = 0; u < kEndU; ++u)
+    if (tid + u * NT < all) held[u] = ld16(gm + (int64_t)(tid + u * NT) * 4);
   // a warp per beam: the sum over its chunks, in 64 bits
   for (int w = warp; w < W; w += NW) {
     const int64_t n = b * W + w;
+    const float2 *part = P.part + n * P.nc;
+    float2 p = lane < P.nc ? __ldcg(part + lane) : make_float2(neg_inf(), 0.f);
     const float s = ld_float(P.scores + n), nm = P.norm ? ld_float(P.norm + n) : 1.f;
     int kind = s == neg_inf() ? 0 : P.finished && ld1(P.finished + n) ? 2 : 1;
     int bad = 0;
@@ -427,15 +435,16 @@ __global__ void __launch_bounds__(kEndNT) sd_beam_end_kernel(const SelectParams 
     }
     float m = neg_inf();
     double z = 1.0;
-    if (kind == 1) {
-      const float2 *part = P.part + n * P.nc;
-      for (int i = lane; i < P.nc; i += 32) m = fmaxf(m, __ldcg(part + i).x);
+    if (kind == 1) {   // else the sums were not written
+      m = p.x;
+      for (int i = lane + 32; i < P.nc; i += 32) m = fmaxf(m, __ldcg(part + i).x);
       m = rmax_f(m);
+      const float c2 = log2e_over(P.T);
       z = 0.0;
       for (int i = lane; i < P.nc; i += 32) {
-        const float2 p = __ldcg(part + i);
+        if (i != lane) p = __ldcg(part + i);
         // a chunk of only -inf has a sum of zero, one with a NaN or +inf a NaN
-        if (p.y != 0.f) z += (double)p.y * exp(((double)p.x - (double)m) / (double)P.T);
+        if (p.y != 0.f) z += (double)p.y * (double)ex2((p.x - m) * c2);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
@@ -447,55 +456,64 @@ __global__ void __launch_bounds__(kEndNT) sd_beam_end_kernel(const SelectParams 
       }
     }
     if (lane == 0) {
-      const double base = kind == 1 ? (double)s - log(z) : (double)s;
       S.kind[w] = kind;
-      S.base[w] = base;
-      S.norm[w] = (double)nm;
+      S.base[w] = (double)s;
+      S.z[w] = kind == 1 ? z : 1.0;
+      S.over[w] = (double)nm;
       S.m[w] = m;
-      S.c[w] = (float)(1.0 / ((double)P.T * (double)nm));
-      S.o[w] = (float)(base / (double)nm);
       if (bad && P.status) atomicOr(P.status, bad);
     }
   }
   __syncthreads();
-  // the best of each thread's groups, and what k of them reach
-  const int nvg = P.nc * kSelNT / VE;
-  float best = neg_inf(), size = 0.f;
-  for (int w = 0; w < W; ++w) {
-    if (S.kind[w] != 1) continue;
-    size = fmaxf(size, fabsf(S.o[w]));
-    const uint8_t *gm = X.groups(w);
-    for (int i = tid; i < nvg; i += NT)
-      best = fmaxf(best, X.approx(w, Elt<E>::vmax(ld16(gm + (int64_t)i * 16))));
+  // the slow 64-bit functions, all beams' at once
+  if (warp == 0 && lane < W) {
+    const double over = P.norm ? 1.0 / S.over[lane] : 1.0, base = S.base[lane] - log(S.z[lane]);
+    S.base[lane] = base;
+    S.over[lane] = over;
+    S.c[lane] = (float)(P.inv_T * over);
+    S.o[lane] = (float)(base * over);
   }
+  __syncthreads();
+  float size = 0.f;
+  for (int w = 0; w < W; ++w)
+    if (S.kind[w] == 1) size = fmaxf(size, fabsf(S.o[w]));
+  // calls f(vector, its place) for the groups' largest
+  auto each_vector = [&](auto f) {
+#pragma unroll
+    for (int u = 0; u < kEndU; ++u)
+      if (tid + u * NT < all) f(held[u], tid + u * NT);
+    for (int i = tid + kEndU * NT; i < all; i += NT) f(ld16(gm + (int64_t)i * 4), i);
+  };
+  // the best of each thread's groups, and what k of them reach
+  float best = neg_inf();
+  each_vector([&](const uint4 &v, int i) {
+    const int w = i / per;
+    if (S.kind[w] == 1) best = fmaxf(best, X.approx(w, Elt<float>::vmax(v)));
+  });
   float bound = top_bound<NT>(best, k, S.keys16, &S.bound, [] {});
   // the fp32 image is off by at most three half steps of its own size and o's: the k groups
   // that reach the bound and the logits held against it by at most six together
   if (bound > kLowest) bound = fmaxf(bound - (fabsf(bound) + size) * 9.5367431640625e-7f, kLowest);
-  for (int w = 0; w < W; ++w) {
-    if (S.kind[w] != 1) continue;
-    const uint8_t *gm = X.groups(w);
-    for (int i = tid; i < nvg; i += NT) {
-      const uint4 v = ld16(gm + (int64_t)i * 16);
-      if (!(X.approx(w, Elt<E>::vmax(v)) >= bound)) continue;
-      float f[VE];
-      Elt<E>::unpack(v, f);
+  each_vector([&](const uint4 &v, int i) {
+    const int w = i / per;
+    if (S.kind[w] != 1 || !(X.approx(w, Elt<float>::vmax(v)) >= bound)) return;
+    float f[4];
+    Elt<float>::unpack(v, f);
 #pragma unroll
-      for (int e = 0; e < VE; ++e)
-        if (X.approx(w, f[e]) >= bound) {
-          const int at = atomicAdd(&S.n_list, 1);
-          if (at < kSelList) S.list[at] = w * (P.nc * kSelNT) + i * VE + e;
-        }
-    }
-  }
+    for (int e = 0; e < 4; ++e)
+      if (X.approx(w, f[e]) >= bound) {
+        const int at = atomicAdd(&S.n_list, 1);
+        if (at < kSelList) S.list[at] = i * 4 + e;
+      }
+  });
   __syncthreads();
   bool fits = S.n_list <= kSelList;
   if (fits) {
-    const int items = S.n_list * U;
+    const int size = X.size(), items = S.n_list * size;
     for (int i = tid; i < items; i += NT) {
-      const int g = S.list[i / U], w = g / (P.nc * kSelNT);
+      const int g = S.list[i / size], w = g / (per * 4);
       const ElemRow<E> row = X.row(w);
-      const int q = X.vector(row, g % (P.nc * kSelNT), i % U);
+      const int q = X.vector(row, g - w * (per * 4), i % size);
       if (q < 0) continue;
       float x[VE];
       Elt<E>::unpack(row.load(q), x);
@@ -545,7 +563,7 @@ static cudaError_t launch_select(const SelectParams &P, int U, cudaStream_t s) {
 
 static size_t select_bytes(int64_t rows, int V, int es) {
   const SelectCut c = select_cut(rows, V, es);
-  return (size_t)rows * c.nc * (sizeof(float2) + (size_t)kSelNT * es) + 16;
+  return (size_t)rows * c.nc * (sizeof(float2) + kSelSets * sizeof(float)) + 16;
 }
 
 }  // namespace sdv
@@ -587,12 +605,12 @@ extern "C" sd_status_t sd_beam_select(const sd_beam_select_args *a, void *stream
   P.share = cut.share;
   P.eos = a->eos;
   P.T = a->T;
+  P.inv_T = 1.0 / (double)a->T;
   P.scores = a->scores;
   P.norm = a->norm;
   P.finished = a->finished;
-  P.gmax = a->workspace;   // whole 16-byte vectors; the sums follow
-  P.part = reinterpret_cast<float2 *>(static_cast<uint8_t *>(a->workspace) +
-                                      (size_t)rows * cut.nc * kSelNT * es);
+  P.gmax = static_cast<float *>(a->workspace);   // whole 16-byte vectors; the sums follow
+  P.part = reinterpret_cast<float2 *>(P.gmax + (size_t)rows * cut.nc * kSelSets);
   P.out_scores = a->out_scores;
   P.parents = a->parents;
   P.tokens = a->tokens;

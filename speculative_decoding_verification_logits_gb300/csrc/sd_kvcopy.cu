@@ -1,80 +1,122 @@
 // Pages copied inside a cache's tensors: after a fork (the filled entries of
 // last pages) and after compaction (whole pages).
 //
-// A copy: what bounds it is memory.  The work is cut into pieces of one part of
-// one page of one layer; the number of pairs is read on the device, CTAs take
-// pieces until there are none left.
+// A copy: what bounds it is memory.  The work is cut into pieces of at most
+// 32 kCpU vectors of one part of one page of one layer, one warp each; the number
+// of pairs is read on the device, and warps take pieces until there are none
+// left, with the next piece's page ids already asked for.  A piece's five
+// numbers (pair, cache, layer, part, piece) are counted up by the grid's own,
+// digit by digit, without divisions.
 
 #include "sd_rows.cuh"
 #include "sd_kv.h"
 
 namespace sdv {
 
-constexpr int kCpNT = 256, kCpU = 4;   // a piece: kCpU vectors per thread
+constexpr int kCpNT = 256, kCpCtas = 4;   // threads of a CTA, CTAs per SM
+constexpr int kCpU = 8;                   // vectors of a piece per lane
+constexpr int kCpWarps = kCpNT / 32;
+
+// A piece's place, and how far apart a warp's pieces are.
+struct CopyAt {
+  int piece, part, layer, cache, pair;
+};
 
 struct CopyParams {
-  int n_caches, layers, N, parts, page_size, pairs, width;
+  int n_caches, layers, N, parts, page_size, pairs, width, pieces;
   int64_t entry_bytes, part_bytes, layer_stride, page_stride;
-  int pieces;                 // of a part
-  int64_t per_pair;           // pieces of a pair
+  CopyAt step;
   const int32_t *src, *dst, *fill, *count;
   int32_t *status;
   uint8_t *caches[SD_MAX_CACHES];
 };
 
 template <typename T>
-__device__ __forceinline__ void copy_piece(const uint8_t *from, uint8_t *to, int64_t bytes,
-                                           T (*load)(const uint8_t *)) {
-  const int64_t n = bytes / (int64_t)sizeof(T);
+__host__ __device__ inline CopyAt copy_at(const CopyParams &P, T x) {
+  CopyAt a;
+  a.piece = (int)(x % P.pieces);
+  x /= P.pieces;
+  a.part = (int)(x % P.parts);
+  x /= P.parts;
+  a.layer = (int)(x % P.layers);
+  x /= P.layers;
+  a.cache = (int)(x % P.n_caches);
+  a.pair = (int)(x / P.n_caches);
+  return a;
+}
+__device__ __forceinline__ CopyAt copy_next(const CopyParams &P, CopyAt a) {
+  const auto digit = [](int &at, int more, int end) {
+    at += more;
+    const bool over = at >= end;
+    at -= over ? end : 0;
+    return over ? 1 : 0;
+  };
+  int carry = digit(a.piece, P.step.piece, P.pieces);
+  carry = digit(a.part, P.step.part + carry, P.parts);
+  carry = digit(a.layer, P.step.layer + carry, P.layers);
+  carry = digit(a.cache, P.step.cache + carry, P.n_caches);
+  a.pair += P.step.pair + carry;
+  return a;
+}
+
+template <typename T, typename F>
+__device__ __forceinline__ void copy_piece(const uint8_t *from, uint8_t *to, int bytes, F load) {
+  const int lane = threadIdx.x & 31, n = bytes / (int)sizeof(T);
+  from += lane * sizeof(T);
+  to += lane * sizeof(T);
   T v[kCpU];
 #pragma unroll
-  for (int u = 0; u < kCpU; ++u) {
-    const int64_t i = threadIdx.x + u * kCpNT;
-    if (i < n) v[u] = load(from + i * sizeof(T));
-  }
+  for (int u = 0; u < kCpU; ++u)
+    if (lane + u * 32 < n) v[u] = load(from + u * 32 * sizeof(T));
 #pragma unroll
-  for (int u = 0; u < kCpU; ++u) {
-    const int64_t i = threadIdx.x + u * kCpNT;
-    if (i < n) reinterpret_cast<T *>(to)[i] = v[u];
-  }
+  for (int u = 0; u < kCpU; ++u)
+    if (lane + u * 32 < n) *reinterpret_cast<T *>(to + u * 32 * sizeof(T)) = v[u];
 }
-__device__ __forceinline__ uint4 load16(const uint8_t *p) { return ld16(p); }
-__device__ __forceinline__ uint32_t load4(const uint8_t *p) { return ld4(p); }
-__device__ __forceinline__ uint16_t load2(const uint8_t *p) { return (uint16_t)ld2(p); }
-__device__ __forceinline__ uint8_t load1(const uint8_t *p) { return (uint8_t)ld1(p); }
 
-__global__ void __launch_bounds__(kCpNT) sd_kv_copy_kernel(const __grid_constant__ CopyParams P) {
+__global__ void __launch_bounds__(kCpNT, kCpCtas)
+    sd_kv_copy_kernel(const __grid_constant__ CopyParams P) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int pairs = P.count ? min(max(ld_int(P.count), 0), P.pairs) : P.pairs;
-  const int64_t total = pairs * P.per_pair;
-  const int64_t piece_bytes = (int64_t)kCpNT * kCpU * P.width;
-  for (int64_t x = blockIdx.x; x < total; x += gridDim.x) {
-    const int pair = (int)(x / P.per_pair);
-    int64_t r = x - pair * P.per_pair;
-    const int src = ld_int(P.src + pair), dst = ld_int(P.dst + pair);
-    if ((unsigned)src >= (unsigned)P.N || (unsigned)dst >= (unsigned)P.N) {
-      if ((src != -1 || dst != -1) && r == 0 && threadIdx.x == 0 && P.status)
-        atomicOr(P.status, (int)SD_STATUS_BAD_PAGE);
-      continue;
+  const int piece_bytes = 32 * kCpU * P.width;
+  CopyAt a = copy_at(P, (int)(blockIdx.x * kCpWarps + (threadIdx.x >> 5)));
+  if (a.pair >= pairs) return;
+  int src = ld_int(P.src + a.pair), dst = ld_int(P.dst + a.pair);
+  int fill = P.fill ? ld_int(P.fill + a.pair) : P.page_size;
+  while (true) {
+    const CopyAt next = copy_next(P, a);
+    const bool more = next.pair < pairs;
+    int src1 = 0, dst1 = 0, fill1 = P.page_size;
+    if (more) {
+      src1 = ld_int(P.src + next.pair);
+      dst1 = ld_int(P.dst + next.pair);
+      if (P.fill) fill1 = ld_int(P.fill + next.pair);
     }
-    int64_t bytes = P.part_bytes;
-    if (P.fill) bytes = min(max(ld_int(P.fill + pair), 0), P.page_size) * P.entry_bytes;
-    const int piece = (int)(r % P.pieces);
-    r /= P.pieces;
-    const int part = (int)(r % P.parts);
-    r /= P.parts;
-    const int layer = (int)(r % P.layers), cache = (int)(r / P.layers);
-    const int64_t at = piece * piece_bytes;
-    if (at >= bytes) continue;
-    bytes = min(bytes - at, piece_bytes);
-    uint8_t *base = P.caches[cache] + layer * P.layer_stride + part * P.part_bytes + at;
-    const uint8_t *from = base + src * P.page_stride;
-    uint8_t *to = base + dst * P.page_stride;
-    if (P.width == 16) copy_piece<uint4>(from, to, bytes, load16);
-    else if (P.width == 4) copy_piece<uint32_t>(from, to, bytes, load4);
-    else if (P.width == 2) copy_piece<uint16_t>(from, to, bytes, load2);
-    else copy_piece<uint8_t>(from, to, bytes, load1);
+    if ((unsigned)src < (unsigned)P.N && (unsigned)dst < (unsigned)P.N) {
+      const int64_t at = (int64_t)a.piece * piece_bytes;
+      const int64_t end = P.fill ? min(max(fill, 0), P.page_size) * P.entry_bytes : P.part_bytes;
+      if (at < end) {
+        const int bytes = (int)min(end - at, (int64_t)piece_bytes);
+        uint8_t *base = P.caches[a.cache] + a.layer * P.layer_stride + a.part * P.part_bytes + at;
+        const uint8_t *from = base + src * P.page_stride;
+        uint8_t *to = base + dst * P.page_stride;
+        if (P.width == 16)
+          copy_piece<uint4>(from, to, bytes, [](const uint8_t *p) { return ld16(p); });
+        else if (P.width == 4)
+          copy_piece<uint32_t>(from, to, bytes, [](const uint8_t *p) { return ld4(p); });
+        else if (P.width == 2)
+          copy_piece<uint16_t>(from, to, bytes, [](const uint8_t *p) { return (uint16_t)ld2(p); });
+        else
+          copy_piece<uint8_t>(from, to, bytes, [](const uint8_t *p) { return (uint8_t)ld1(p); });
+      }
+    } else if ((src != -1 || dst != -1) && P.status) {
+      atomicOr(P.status, (int)SD_STATUS_BAD_PAGE);
+    }
+    if (!more) return;
+    a = next;
+    src = src1;
+    dst = dst1;
+    fill = fill1;
   }
 }
 
@@ -118,12 +160,18 @@ extern "C" sd_status_t sd_kv_copy(const sd_kv_copy_args *a, void *stream) {
   }
   const int w = (int)(bits & (~bits + 1));
   P.width = w == 16 ? 16 : w >= 4 ? 4 : w;
-  const int64_t piece = (int64_t)kCpNT * kCpU * P.width;
+  const int64_t piece = (int64_t)32 * kCpU * P.width;
   const int64_t pieces = (P.part_bytes + piece - 1) / piece;
-  if (pieces > INT32_MAX) return SD_ERR_INVALID_ARG;
+  // no digit and no number of pieces overflows
+  constexpr int64_t kMost = (int64_t)1 << 30;
+  if (pieces > kMost || P.parts > kMost || P.layers > kMost || P.pairs > kMost ||
+      pieces * P.parts > kMost || pieces * P.parts * P.layers > kMost * SD_MAX_CACHES)
+    return SD_ERR_INVALID_ARG;
   P.pieces = (int)pieces;
-  P.per_pair = pieces * P.parts * P.layers * P.n_caches;
-  const int64_t most = std::min<int64_t>(P.per_pair * P.pairs, (int64_t)8 * sm_count());
+  const int64_t per_pair = pieces * P.parts * P.layers * P.n_caches;
+  const int64_t most = std::min<int64_t>((per_pair * P.pairs + kCpWarps - 1) / kCpWarps,
+                                         (int64_t)kCpCtas * sm_count());
+  P.step = copy_at(P, most * kCpWarps);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)most, 1, 1);
   cfg.blockDim = dim3(kCpNT, 1, 1);

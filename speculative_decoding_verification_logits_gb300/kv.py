@@ -159,10 +159,12 @@ def _fork(a, refs, status, dev):
     a.refs, a.N = _pool(refs, dev)
     if status is not None:
         a.status = _i32(status, "status", (1,), dev)
-    a.workspace_bytes = _lib().sd_kv_fork_workspace_size(a.rows_in, a.R, a.N)
-    ws = _workspace(a.workspace_bytes, dev)
+    n = a.workspace_bytes = _lib().sd_kv_fork_workspace_size(a.rows_in, a.R, a.N)
+    ws = _workspace(n, dev)
     a.workspace = ws.data_ptr()
-    _check(_lib().sd_kv_fork(a, _stream_of(dev)), "sd_kv_fork")
+    rc = _lib().sd_kv_fork(a, _stream_of(dev))
+    if rc:
+        _check(rc, "sd_kv_fork")
     _written(refs)
 
 
@@ -182,32 +184,36 @@ def kv_fork(block_table, kv_len, parents, refs, page_size: int, *, append: int =
     rows, M, lens = _table(block_table, kv_len)
     dev = block_table.device
     _need(parents, "parents", _I32, None, dev)
-    if parents.dim() not in (1, 2):
+    shape = parents.shape
+    if len(shape) not in (1, 2):
         raise ValueError("parents must be [R] or [B][k]")
     R = parents.numel()
-    groups = parents.shape[0] if parents.dim() == 2 else 0
+    if R == 0:
+        raise ValueError("parents must name at least one row")
+    groups = shape[0] if len(shape) == 2 else 0
     if groups and rows % groups:
         raise ValueError(f"{rows} rows are not {groups} groups")
     a = ForkArgs(rows, R, groups, M, page_size, append, bool(keep))
-    if R == 0:
-        raise ValueError("parents must name at least one row")
-    if out is None:
-        t, n, src, dst, fill, count = torch.empty(R * M + 4 * R + 1, dtype=_I32, device=dev).split(
-            (R * M, R, R, R, R, 1))
-        out = KVFork(t.view(R, M), n, src, dst, fill, count)
-        given = False
-    else:
-        given = True
+    given = out is not None
+    if given:
         for x in (out.block_table, out.kv_len):
             _need(x, "out", _I32, None, dev)
             if any(_meet(x, y) for y in (block_table, kv_len, parents, refs)):
                 raise ValueError("out overlaps the input")
+        a.table_out = _i32(out.block_table, "out.block_table", (R, M), dev)
+        a.len_out = _i32(out.kv_len, "out.kv_len", (R,), dev)
+        a.src, a.dst, a.fill = (_i32(getattr(out, n), "out." + n, (R,), dev)
+                                for n in ("src", "dst", "fill"))
+        a.count = _i32(out.count, "out.count", (1,), dev)
+    else:   # one block of memory
+        buf = torch.empty(R * M + 4 * R + 1, dtype=_I32, device=dev)
+        t, n, src, dst, fill, count = buf.split((R * M, R, R, R, R, 1))
+        out = KVFork(t.view(R, M), n, src, dst, fill, count)
+        a.table_out = at = buf.data_ptr()
+        at += 4 * R * M
+        a.len_out, a.src, a.dst, a.fill, a.count = (at, at + 4 * R, at + 8 * R, at + 12 * R,
+                                                    at + 16 * R)
     a.parents, a.table, a.kv_len = parents.data_ptr(), block_table.data_ptr(), lens
-    a.table_out = _i32(out.block_table, "out.block_table", (R, M), dev)
-    a.len_out = _i32(out.kv_len, "out.kv_len", (R,), dev)
-    a.src, a.dst, a.fill = (_i32(getattr(out, n), "out." + n, (R,), dev)
-                            for n in ("src", "dst", "fill"))
-    a.count = _i32(out.count, "out.count", (1,), dev)
     _fork(a, refs, status, dev)
     if given:
         for t in out:
@@ -224,13 +230,14 @@ def kv_extend(block_table, kv_len, refs, page_size: int, append: int, *, status=
     rows, M, lens = _table(block_table, kv_len)
     dev = block_table.device
     a = ForkArgs(rows, rows, 0, M, page_size, append, 0)
-    m = KVMoves(*torch.empty(3 * rows + 1, dtype=_I32, device=dev).split((rows, rows, rows, 1)))
+    buf = torch.empty(3 * rows + 1, dtype=_I32, device=dev)
+    at = buf.data_ptr()
+    a.src, a.dst, a.fill, a.count = at, at + 4 * rows, at + 8 * rows, at + 12 * rows
     a.table = a.table_out = block_table.data_ptr()
     a.kv_len = lens
-    a.src, a.dst, a.fill, a.count = (t.data_ptr() for t in m)
     _fork(a, refs, status, dev)
     _written(block_table)
-    return m
+    return KVMoves(*buf.split((rows, rows, rows, 1)))
 
 
 @_on_device
@@ -274,8 +281,8 @@ def kv_compact(refs, block_table=None, *, status=None, stream=None) -> KVCompact
     dev = refs.device
     ref, N = _pool(refs, dev)
     h = N // 2
-    new, src, dst, count, live = torch.empty(N + 2 * h + 2, dtype=_I32, device=dev).split(
-        (N, h, h, 1, 1))
+    buf = torch.empty(N + 2 * h + 2, dtype=_I32, device=dev)
+    at = buf.data_ptr()
     table, n_table, st = None, 0, None
     if block_table is not None:
         _need(block_table, "block_table", _I32, None, dev)
@@ -287,12 +294,15 @@ def kv_compact(refs, block_table=None, *, status=None, stream=None) -> KVCompact
         st = _i32(status, "status", (1,), dev)
     need = _lib().sd_kv_compact_workspace_size(N)
     ws = _workspace(need, dev)
-    _check(_lib().sd_kv_compact(N, ref, n_table, table, src.data_ptr(), dst.data_ptr(),
-                                count.data_ptr(), live.data_ptr(), new.data_ptr(), st,
-                                ws.data_ptr(), need, _stream_of(dev)), "sd_kv_compact")
+    rc = _lib().sd_kv_compact(N, ref, n_table, table, at, at + 4 * h, at + 8 * h,
+                              at + 8 * h + 4, at + 8 * h + 8, st, ws.data_ptr(), need,
+                              _stream_of(dev))
+    if rc:
+        _check(rc, "sd_kv_compact")
     _written(refs)
     if n_table:
         _written(block_table)
+    src, dst, count, live, new = buf.split((h, h, 1, 1, N))
     return KVCompact(src, dst, count, new, live)
 
 
