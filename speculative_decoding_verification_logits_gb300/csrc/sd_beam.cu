@@ -1,10 +1,10 @@
 // The k best continuations of each sequence's beams: s + x / T - log sum exp(x / T)
 // over W rows of V logits, by two launches.
 //
-//  1. sd_beam_stream_kernel: every CTA takes one chunk of a row, held in
-//     registers.  It writes the chunk's (largest m, sum of 2^((x - m) c)) and the
-//     largest logit of every four threads' vectors (a group).  No beam's row is
-//     read twice, and nothing depends on other CTAs.
+//  1. sd_beam_stream_kernel: a warp per piece of a row, of up to 4 KB.  It writes
+//     the piece's (largest m, sum of 2^((x - m) c)) and the
+//     largest logit of every four lanes' vectors (a group).  No beam's row is
+//     read twice, and no warp waits for another.
 //  2. sd_beam_end_kernel: one CTA per sequence joins the sums of each beam in 64
 //     bits, and finds from the groups' largest logits alone a value that k of
 //     them reach: no candidate below it is among the k best.  The groups that
@@ -19,22 +19,22 @@
 
 namespace sdv {
 
-constexpr int kSelNT = 256;      // threads of a streaming CTA
-constexpr int kSelSet = 4;       // threads of a group
-constexpr int kSelSets = kSelNT / kSelSet;
+constexpr int kSelNT = 128;      // threads of a streaming CTA
+constexpr int kSelSet = 4;       // lanes of a group
+constexpr int kSelSets = 32 / kSelSet;
 constexpr int kEndNT = 512;      // threads of a sequence's end
-constexpr int kEndU = 4;         // vectors of groups that one of them holds
+constexpr int kEndU = 8;         // vectors of groups that one of them holds
 constexpr int kSelList = 1024;   // listed groups, and candidates, of a sequence
 
 struct SelectParams {
   const void *logits;
   int64_t sb, sw;
-  int B, W, V, k, nc, share, eos;
+  int B, W, V, k, nc, per_row, share, eos;   // per_row: streaming CTAs of a row
   float T;
   double inv_T;
   const float *scores, *norm;
   const uint8_t *finished;
-  float2 *part;      // [B W][nc]: largest logit of a chunk and its sum
+  float2 *part;      // [B W][nc]: largest logit of a piece and its sum
   float *gmax;       // [B W][nc][kSelSets]: largest logit of each group
   float *out_scores;
   int32_t *parents, *tokens;
@@ -42,7 +42,18 @@ struct SelectParams {
   int32_t *status;
 };
 
-// How rows are cut: nc chunks of `share` vectors, at most U of them per thread.
+__device__ __forceinline__ float ld_near(const float *p) {
+  float v;
+  asm volatile("ld.global.ca.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ int ld_near(const uint8_t *p) {
+  unsigned short v;
+  asm volatile("ld.global.ca.u8 %0, [%1];" : "=h"(v) : "l"(p));
+  return v;
+}
+
+// How rows are cut: nc pieces of `share` vectors, at most U of them per lane.
 struct SelectCut {
   int U, nc, share;
 };
@@ -50,8 +61,8 @@ static SelectCut select_cut(int64_t rows, int V, int es) {
   const int ve = 16 / es;
   const int nvec = (int)(((int64_t)V + ve - 1) / ve);
   SelectCut c;
-  c.U = rows * nvec >= (int64_t)2 * 8 * kSelNT * sm_count() ? 8 : 2;
-  c.nc = (nvec + c.U * kSelNT - 1) / (c.U * kSelNT);
+  c.U = rows * nvec >= (int64_t)8 * kSelNT * sm_count() ? 8 : 2;
+  c.nc = (nvec + c.U * 32 - 1) / (c.U * 32);
   c.share = (nvec + c.nc - 1) / c.nc;
   return c;
 }
@@ -106,37 +117,42 @@ struct ElemRow {
   }
 };
 
+// A warp per piece, in registers: warps share nothing, and CTAs are small, so that an SM asks
+// for new pieces whenever one of its warps is done.  The rows' scores come
+// through L1, where the CTAs before left them.
 template <typename E, int U>
 __global__ void __launch_bounds__(kSelNT) sd_beam_stream_kernel(const SelectParams P) {
-  constexpr int NT = kSelNT, NW = NT / 32;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int n = blockIdx.x / P.nc, chunk = blockIdx.x % P.nc, tid = threadIdx.x;
+  const int lane = threadIdx.x & 31;
+  const int n = blockIdx.x / P.per_row, w = n % P.W;
+  const int piece = blockIdx.x % P.per_row * (kSelNT / 32) + (threadIdx.x >> 5);
+  if (piece >= P.nc) return;
   // a beam that is dead or finished has no candidates of its own
-  if (!(fabsf(ld_float(P.scores + n)) < INFINITY)) return;
-  if (P.finished && ld1(P.finished + n)) return;
-  const ElemRow<E> row(P.logits, (n / P.W) * P.sb + (n % P.W) * P.sw, P.V);
-  const int q0 = chunk * P.share, q1 = min(q0 + P.share, row.nvec);
+  if (!(fabsf(ld_near(P.scores + n)) < INFINITY)) return;
+  if (P.finished && ld_near(P.finished + n)) return;
+  const ElemRow<E> row(P.logits, (n / P.W) * P.sb + w * P.sw, P.V);
+  const int q0 = piece * P.share, q1 = min(q0 + P.share, row.nvec);
   const int lo = max(q0, row.lo()), hi = min(q1, row.hi());
-  const uint8_t *src = row.grid(q0 + tid);
+  const uint8_t *src = row.grid(q0 + lane);
   const uint32_t inf = Elt<E>::kNegInfWord;
   uint4 v[U];
   if (row.hp == 0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int q = q0 + tid + u * NT;
+      const int q = q0 + lane + u * 32;
       v[u] = make_uint4(inf, inf, inf, inf);
-      if (q >= lo && q < hi) v[u] = ld16(src + (int64_t)u * NT * 16);
+      if (q >= lo && q < hi) v[u] = ld16(src + u * 512);
     }
   } else {
     uint4 next[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int q = q0 + tid + u * NT;
+      const int q = q0 + lane + u * 32;
       v[u] = next[u] = make_uint4(inf, inf, inf, inf);
       if (q >= lo && q < hi) {
-        v[u] = ld16(src + (int64_t)u * NT * 16);
-        next[u] = ld16(src + (int64_t)u * NT * 16 + 16);
+        v[u] = ld16(src + u * 512);
+        next[u] = ld16(src + u * 512 + 16);
       }
     }
 #pragma unroll
@@ -145,23 +161,17 @@ __global__ void __launch_bounds__(kSelNT) sd_beam_stream_kernel(const SelectPara
   if (lo > q0 || hi < q1) {   // the row's first or last vectors
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int q = q0 + tid + u * NT;
+      const int q = q0 + lane + u * 32;
       if (q < q1 && (q < lo || q >= hi)) v[u] = row.load_edge(q);
     }
   }
-  __shared__ float wm[NW], wz[NW];
-  const float best = VecExp<E>::template largest<U>(v);
-  float m = best;
+  float m = VecExp<E>::template largest<U>(v);
 #pragma unroll
   for (int o = 1; o < kSelSet; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (tid % kSelSet == 0) P.gmax[((int64_t)n * P.nc + chunk) * kSelSets + tid / kSelSet] = m;
+  const int64_t at = (int64_t)n * P.nc + piece;
+  if (lane % kSelSet == 0) P.gmax[at * kSelSets + lane / kSelSet] = m;
   m = rmax_f(m);
-  if ((tid & 31) == 0) wm[tid >> 5] = m;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < NW; ++i) m = fmaxf(m, wm[i]);
-  const float c2 = log2e_over(P.T);
-  const ExpBase B(m, c2);
+  const ExpBase B(m, log2e_over(P.T));
   uint64_t acc = 0ull;
   if (!B.far) {
 #pragma unroll
@@ -173,14 +183,7 @@ __global__ void __launch_bounds__(kSelNT) sd_beam_stream_kernel(const SelectPara
   float x, y;
   upk2(acc, x, y);
   const float z = warp_sum((x + y) * B.fix);
-  if ((tid & 31) == 0) wz[tid >> 5] = z;
-  __syncthreads();
-  if (tid == 0) {
-    float t = 0.f;
-#pragma unroll
-    for (int i = 0; i < NW; ++i) t += wz[i];
-    P.part[(int64_t)n * P.nc + chunk] = make_float2(m, t);
-  }
+  if (lane == 0) P.part[at] = make_float2(m, z);
 }
 
 // A double's order as an unsigned integer (never a NaN here).
@@ -195,76 +198,86 @@ struct SelectEnd {
   int kind[SD_MAX_BEAMS];
   double base[SD_MAX_BEAMS];
   double over[SD_MAX_BEAMS];          // 1 / norm
-  double z[SD_MAX_BEAMS];
+  int top[SD_MAX_BEAMS];              // its largest logit, ordered
+  unsigned hi[SD_MAX_BEAMS];          // its sum in units of 2^-10 and of 2^-31
+  unsigned lo[SD_MAX_BEAMS];
+  int bad[SD_MAX_BEAMS];
   // an fp32 image of the ranked score: max((x - m) c + o, lowest)
   float m[SD_MAX_BEAMS], c[SD_MAX_BEAMS], o[SD_MAX_BEAMS];
-  int list[kSelList];                 // groups: beam, chunk, place
-  unsigned long long key[kSelList];   // candidates: their order,
-  int at[kSelList];                   // w V + v,
-  float x[kSelList];                  // and logit
+  float size[SD_MAX_BEAMS];           // of what entered o
+  int list[kSelList];                 // groups: beam in the upper half, piece and place
+  unsigned long long key[kSelList];   // candidates: the order of their ranked scores,
+  int at[kSelList];                   // beam and token (kTokenBits),
+  float score[kSelList];
   unsigned long long best_key[SD_MAX_TOP];   // the k best, in order
   int best_at[SD_MAX_TOP];
-  float best_x[SD_MAX_TOP];
+  float best_score[SD_MAX_TOP];
   unsigned short keys16[kEndNT];
   int warp_n[kEndNT / 32];
   float bound;
-  int n_list, n_cand, n_best, count;
+  int n_list, n_cand, n_best;
 };
+constexpr int kTokenBits = 18;
+static_assert(SD_MAX_V <= 1 << kTokenBits, "a token and a beam fit an int");
 
-template <typename E>
+template <typename E, int U>
 struct EndView {
   static constexpr int VE = Elt<E>::kPerVec;
+  static constexpr int kSize = kSelSet * U;   // vectors of a group
   const SelectParams &P;
   SelectEnd &S;
-  int b, U;
-  __device__ __forceinline__ EndView(const SelectParams &P_, SelectEnd &S_, int U_)
-      : P(P_), S(S_), b(blockIdx.x), U(U_) {}
+  int b;
+  __device__ __forceinline__ EndView(const SelectParams &P_, SelectEnd &S_)
+      : P(P_), S(S_), b(blockIdx.x) {}
   __device__ __forceinline__ ElemRow<E> row(int w) const {
     return ElemRow<E>(P.logits, b * P.sb + w * P.sw, P.V);
   }
   __device__ __forceinline__ const float *groups(int w) const {
     return P.gmax + ((int64_t)b * P.W + w) * P.nc * kSelSets;
   }
-  // vectors of a group, and the row's vector that is number i of group g, or -1
-  __device__ __forceinline__ int size() const { return kSelSet * U; }
+  // the row's vector that is number i of group g, or -1
   __device__ __forceinline__ int vector(const ElemRow<E> &r, int g, int i) const {
-    const int chunk = g / kSelSets;
-    const int at = g % kSelSets * kSelSet + i % kSelSet + i / kSelSet * kSelNT;
-    const int q = chunk * P.share + at;
+    const int at = g % kSelSets * kSelSet + i % kSelSet + i / kSelSet * 32;
+    const int q = g / kSelSets * P.share + at;
     return at < P.share && q < r.nvec ? q : -1;
   }
   __device__ __forceinline__ float approx(int w, float x) const {
     return x > neg_inf() ? fmaxf(fmaf(x - S.m[w], S.c[w], S.o[w]), kLowest) : neg_inf();
   }
-  __device__ __forceinline__ double score(int w, float x) const {
-    return S.kind[w] == 2 ? S.base[w]
-                          : S.base[w] + ((double)x - (double)S.m[w]) * P.inv_T;
-  }
-  __device__ __forceinline__ void offer(int w, int v, float x) const {
+  // a candidate; logits of a finished beam are not looked at
+  __device__ __noinline__ void offer(int w, int v, float x) const {
+    double c = S.base[w];
+    if (S.kind[w] == 1) c += ((double)x - (double)S.m[w]) * P.inv_T;
     const int i = atomicAdd(&S.n_cand, 1);
     if (i < kSelList) {
-      S.key[i] = dord(score(w, x) * S.over[w]);
-      S.at[i] = w * P.V + v;
-      S.x[i] = x;
+      S.key[i] = dord(c * S.over[w]);
+      S.at[i] = w << kTokenBits | v;
+      S.score[i] = (float)c;
     }
   }
 };
 
-// The k best of the candidates, in order, into S.best_*: their places are how
-// many are better, and no two are alike.  Begins and ends with a barrier.
+// The k best of the candidates, in order, into S.best_*: a warp counts how many are
+// better than one, and no two are alike.  Begins and ends with a barrier.
 __device__ __forceinline__ void rank_candidates(SelectEnd &S, int k) {
   __syncthreads();
-  const int n = min(S.n_cand, kSelList);
-  for (int i = threadIdx.x; i < n; i += kEndNT) {
+  const int n = min(S.n_cand, kSelList), lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int i = threadIdx.x >> 5; i < n; i += kEndNT / 32) {
     const unsigned long long key = S.key[i];
     const int at = S.at[i];
     int above = 0;
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) above += S.key[j] > key || (S.key[j] == key && S.at[j] < at);
-    if (above < k) {
+#pragma unroll 1
+    for (int j = lane; j < n; j += 32) {
+      const unsigned long long other = S.key[j];
+      above += other > key | (other == key & S.at[j] < at);
+    }
+    __syncwarp();
+    above = __reduce_add_sync(0xffffffffu, above);
+    if (lane == 0 && above < k) {
       S.best_key[above] = key;
       S.best_at[above] = at;
-      S.best_x[above] = S.x[i];
+      S.best_score[above] = S.score[i];
     }
   }
   if (threadIdx.x == 0) S.n_best = min(n, k);
@@ -291,9 +304,9 @@ __device__ __forceinline__ int block_count(SelectEnd &S, int n) {
 //    the key (value, index) of the k-th is found bit by bit;
 //  - if they are fewer, logits equal to v* fill up, lowest index first, from the
 //    row's beginning until there are enough.
-template <typename E>
-__device__ __noinline__ void each_beam(const EndView<E> &X) {
-  constexpr int VE = EndView<E>::VE, NT = kEndNT;
+template <typename E, int U>
+__device__ __noinline__ void each_beam(const EndView<E, U> &X) {
+  constexpr int VE = EndView<E, U>::VE, NT = kEndNT, size = EndView<E, U>::kSize;
   SelectEnd &S = X.S;
   const SelectParams &P = X.P;
   const int tid = threadIdx.x, k = P.k;
@@ -307,7 +320,7 @@ __device__ __noinline__ void each_beam(const EndView<E> &X) {
     for (int i = tid; i < kept; i += NT) {
       S.key[i] = S.best_key[i];
       S.at[i] = S.best_at[i];
-      S.x[i] = S.best_x[i];
+      S.score[i] = S.best_score[i];
     }
     if (tid == 0) {
       S.n_cand = kept;
@@ -337,10 +350,10 @@ __device__ __noinline__ void each_beam(const EndView<E> &X) {
         if (at < kSelList) S.list[at] = i;
       }
     __syncthreads();
-    const int items = min(S.n_list, kSelList) * X.size();
+    const int items = min(S.n_list, kSelList) * size;
     auto above = [&](unsigned long long from, auto f) {
       for (int i = tid; i < items; i += NT) {
-        const int q = X.vector(row, S.list[i / X.size()], i % X.size());
+        const int q = X.vector(row, S.list[i / size], i % size);
         if (q < 0) continue;
         float x[VE];
         Elt<E>::unpack(row.load(q), x);
@@ -401,137 +414,184 @@ __device__ __noinline__ void each_beam(const EndView<E> &X) {
   }
 }
 
-template <typename E>
-__global__ void __launch_bounds__(kEndNT) sd_beam_end_kernel(const SelectParams P, int U) {
+template <typename E, int U>
+__global__ void __launch_bounds__(kEndNT, 1) sd_beam_end_kernel(const SelectParams P) {
   constexpr int VE = Elt<E>::kPerVec, NT = kEndNT, NW = NT / 32;
   __shared__ SelectEnd S;
-  const EndView<E> X(P, S, U);
+  const EndView<E, U> X(P, S);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, W = P.W, k = P.k;
   const int64_t b = blockIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (tid == 0) S.n_list = S.n_cand = 0;
-  // the groups' largest, kEndU vectors of four per thread at a time
+  // the groups' largest, kEndU vectors of four per thread
   const int per = P.nc * kSelSets / 4, all = W * per;
   const float *gm = X.groups(0);
   uint4 held[kEndU];
 #pragma unroll
   for (int u = 0; u < kEndU; ++u)
     if (tid + u * NT < all) held[u] = ld16(gm + (int64_t)(tid + u * NT) * 4);
-  // a warp per beam: the sum over its chunks, in 64 bits
-  for (int w = warp; w < W; w += NW) {
-    const int64_t n = b * W + w;
-    const float2 *part = P.part + n * P.nc;
-    float2 p = lane < P.nc ? __ldcg(part + lane) : make_float2(neg_inf(), 0.f);
-    const float s = ld_float(P.scores + n), nm = P.norm ? ld_float(P.norm + n) : 1.f;
-    int kind = s == neg_inf() ? 0 : P.finished && ld1(P.finished + n) ? 2 : 1;
-    int bad = 0;
+  // a lane of the second warp per beam
+  const bool mine = warp == 1 && lane < W;
+  float s = neg_inf(), nm = 1.f;
+  int ended = 0;
+  if (mine) {
+    s = ld_float(P.scores + b * W + lane);
+    if (P.norm) nm = ld_float(P.norm + b * W + lane);
+    if (P.finished) ended = ld1(P.finished + b * W + lane);
+  }
+  // 32 pieces of a beam per warp.  Of a beam that is not read they may be anything.
+  const int blocks = (P.nc + 31) / 32;
+  const auto load_piece = [&](int i) {
+    const int w = i / blocks, at = i % blocks * 32 + lane;
+    return at < P.nc ? __ldcg(P.part + (b * W + w) * P.nc + at) : make_float2(neg_inf(), 0.f);
+  };
+  const auto each_block = [&](const float2 &first, auto f) {
+#pragma unroll 1
+    for (int i = warp; i < W * blocks; i += NW) f(i / blocks, i == warp ? first : load_piece(i));
+  };
+  float2 first = make_float2(neg_inf(), 0.f);
+  if (warp < W * blocks) first = load_piece(warp);
+  if (tid == 0) S.n_list = S.n_cand = 0;
+  if (tid < SD_MAX_BEAMS) {
+    S.top[tid] = ford(neg_inf());
+    S.hi[tid] = S.lo[tid] = 0u;
+    S.bad[tid] = 0;
+  }
+  __syncthreads();
+  // their largest logit, then their sums in whole units, which come out the same in any order
+  each_block(first, [&](int w, const float2 &p) {
+    const int m = __reduce_max_sync(0xffffffffu, ford(p.x));
+    if (lane == 0) atomicMax(&S.top[w], m);
+  });
+  __syncthreads();
+  const float c2 = log2e_over(P.T);
+  each_block(first, [&](int w, const float2 &p) {
+    // at most 2^11; a piece with a NaN or +inf has a sum of NaN
+    const float t = p.y == 0.f ? 0.f : p.y * ex2((p.x - fdeord(S.top[w])) * c2);
+    const float units = t * 1024.f, whole = truncf(units);
+    const bool bad = __any_sync(0xffffffffu, !(t <= 4096.f));
+    const unsigned hi = __reduce_add_sync(0xffffffffu, __float2uint_rn(whole));
+    const unsigned lo = __reduce_add_sync(0xffffffffu, __float2uint_rn((units - whole) * 2097152.f));
+    if (lane == 0) {
+      atomicAdd(&S.hi[w], hi);
+      atomicAdd(&S.lo[w], lo);
+      if (bad) S.bad[w] = 1;
+    }
+  });
+  __syncthreads();
+  double z = 1.0;
+  if (mine) {
+    int kind = s == neg_inf() ? 0 : ended ? 2 : 1, bad = 0;
+    const float m = fdeord(S.top[lane]);
     if (!(fabsf(s) < INFINITY) && s != neg_inf()) {
       kind = 0;
       bad = SD_STATUS_NONFINITE;
     } else if (kind && !(nm > 0.f && nm < INFINITY)) {
       kind = 0;
       bad = SD_STATUS_BAD_PENALTY;
+    } else if (kind == 1 && (S.bad[lane] || m == INFINITY)) {
+      kind = 0;
+      bad = SD_STATUS_NONFINITE;
+    } else if (kind == 1 && m == neg_inf()) {
+      kind = 0;
     }
-    float m = neg_inf();
-    double z = 1.0;
-    if (kind == 1) {   // else the sums were not written
-      m = p.x;
-      for (int i = lane + 32; i < P.nc; i += 32) m = fmaxf(m, __ldcg(part + i).x);
-      m = rmax_f(m);
-      const float c2 = log2e_over(P.T);
-      z = 0.0;
-      for (int i = lane; i < P.nc; i += 32) {
-        if (i != lane) p = __ldcg(part + i);
-        // a chunk of only -inf has a sum of zero, one with a NaN or +inf a NaN
-        if (p.y != 0.f) z += (double)p.y * (double)ex2((p.x - m) * c2);
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-      if (z != z || m == INFINITY) {
-        kind = 0;
-        bad = SD_STATUS_NONFINITE;
-      } else if (m == neg_inf()) {
-        kind = 0;
-      }
-    }
-    if (lane == 0) {
-      S.kind[w] = kind;
-      S.base[w] = (double)s;
-      S.z[w] = kind == 1 ? z : 1.0;
-      S.over[w] = (double)nm;
-      S.m[w] = m;
-      if (bad && P.status) atomicOr(P.status, bad);
-    }
+    if (kind == 1)
+      z = (double)S.hi[lane] * 9.765625e-4 + (double)S.lo[lane] * 4.656612873077393e-10;
+    S.kind[lane] = kind;
+    S.m[lane] = m;
+    // an fp32 image of what follows in 64 bits
+    const float over = __fdividef(1.f, nm);
+    S.c[lane] = __fdividef(over, P.T);
+    const float log_z = 0.693147180559945309f * __log2f((float)z);
+    S.o[lane] = (s - log_z) * over;
+    S.size[lane] = kind == 1 ? (fabsf(s) + log_z + 1.f) * over : 0.f;
+    if (bad && P.status) atomicOr(P.status, bad);
   }
   __syncthreads();
-  // the slow 64-bit functions, all beams' at once
-  if (warp == 0 && lane < W) {
-    const double over = P.norm ? 1.0 / S.over[lane] : 1.0, base = S.base[lane] - log(S.z[lane]);
-    S.base[lane] = base;
-    S.over[lane] = over;
-    S.c[lane] = (float)(P.inv_T * over);
-    S.o[lane] = (float)(base * over);
-  }
-  __syncthreads();
-  float size = 0.f;
-  for (int w = 0; w < W; ++w)
-    if (S.kind[w] == 1) size = fmaxf(size, fabsf(S.o[w]));
-  // calls f(vector, its place) for the groups' largest
-  auto each_vector = [&](auto f) {
+  // calls f(vector, its place, its beam) for the groups' largest of the beams that are read
+  const float inv_per = 1.f / (float)per;
+  const auto each_vector = [&](auto f) {
 #pragma unroll
-    for (int u = 0; u < kEndU; ++u)
-      if (tid + u * NT < all) f(held[u], tid + u * NT);
-    for (int i = tid + kEndU * NT; i < all; i += NT) f(ld16(gm + (int64_t)i * 4), i);
+    for (int u = 0; u < kEndU; ++u) {
+      const int i = tid + u * NT;
+      if (i >= all) break;
+      const int w = (int)(((float)i + 0.5f) * inv_per);
+      if (S.kind[w] == 1) f(held[u], i, w);
+    }
+#pragma unroll 1
+    for (int i = tid + kEndU * NT; i < all; i += NT)
+      if (S.kind[i / per] == 1) f(ld16(gm + (int64_t)i * 4), i, i / per);
   };
   // the best of each thread's groups, and what k of them reach
   float best = neg_inf();
-  each_vector([&](const uint4 &v, int i) {
-    const int w = i / per;
-    if (S.kind[w] == 1) best = fmaxf(best, X.approx(w, Elt<float>::vmax(v)));
+  each_vector([&](const uint4 &v, int, int w) {
+    best = fmaxf(best, X.approx(w, Elt<float>::vmax(v)));
   });
-  float bound = top_bound<NT>(best, k, S.keys16, &S.bound, [] {});
-  // the fp32 image is off by at most three half steps of its own size and o's: the k groups
-  // that reach the bound and the logits held against it by at most six together
-  if (bound > kLowest) bound = fmaxf(bound - (fabsf(bound) + size) * 9.5367431640625e-7f, kLowest);
-  each_vector([&](const uint4 &v, int i) {
-    const int w = i / per;
-    if (S.kind[w] != 1 || !(X.approx(w, Elt<float>::vmax(v)) >= bound)) return;
-    float f[4];
-    Elt<float>::unpack(v, f);
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (X.approx(w, f[e]) >= bound) {
-        const int at = atomicAdd(&S.n_list, 1);
-        if (at < kSelList) S.list[at] = i * 4 + e;
-      }
-  });
+  S.keys16[tid] = top_key16(best);
+  __syncthreads();
+  if (warp == 0) {
+    const float found = top_bound_warp<NT>(S.keys16, k);
+    if (lane == 0) S.bound = found;
+  } else if (mine) {   // meanwhile the beams' numbers in 64 bits
+    S.base[lane] = (double)s - log(z);
+    S.over[lane] = P.norm ? 1.0 / (double)nm : 1.0;
+  }
+  __syncthreads();
+  float bound = S.bound, size = 0.f;
+  for (int w = 0; w < W; ++w) size = fmaxf(size, S.size[w]);
+  // the fp32 image is off by less than 2^-19 of its own size and of what entered o (quotients of two
+  // steps, a logarithm of 2^-22 near one): the groups that reach the bound and the logits
+  // held against it by at most twice that
+  if (bound > kLowest)
+    bound = fmaxf(bound - (fabsf(bound) + size) * 3.814697265625e-6f, kLowest);
+  if (best >= bound)
+    each_vector([&](const uint4 &v, int i, int w) {
+      if (!(X.approx(w, Elt<float>::vmax(v)) >= bound)) return;
+      float f[4];
+      Elt<float>::unpack(v, f);
+#pragma unroll 1
+      for (int e = 0; e < 4; ++e)
+        if (X.approx(w, e == 0 ? f[0] : e == 1 ? f[1] : e == 2 ? f[2] : f[3]) >= bound) {
+          const int at = atomicAdd(&S.n_list, 1);
+          if (at < kSelList) S.list[at] = w << 16 | ((i - w * per) * 4 + e);
+        }
+    });
   __syncthreads();
   bool fits = S.n_list <= kSelList;
   if (fits) {
-    const int size = X.size(), items = S.n_list * size;
+    const int items = S.n_list * X.kSize;
+#pragma unroll 1
     for (int i = tid; i < items; i += NT) {
-      const int g = S.list[i / size], w = g / (per * 4);
+      const int g = S.list[i / X.kSize], w = g >> 16;
       const ElemRow<E> row = X.row(w);
-      const int q = X.vector(row, g - w * (per * 4), i % size);
+      const int q = X.vector(row, g & 0xffff, i % X.kSize);
       if (q < 0) continue;
       float x[VE];
       Elt<E>::unpack(row.load(q), x);
+      unsigned pass = 0u;
 #pragma unroll
-      for (int e = 0; e < VE; ++e)
-        if (X.approx(w, x[e]) >= bound) X.offer(w, row.first(q) + e, x[e]);
+      for (int e = 0; e < VE; ++e) pass |= (X.approx(w, x[e]) >= bound ? 1u : 0u) << e;
+      while (pass) {
+        const int at = __ffs(pass) - 1;
+        pass &= pass - 1;
+        float y = x[0];
+#pragma unroll
+        for (int e = 1; e < VE; ++e) y = at == e ? x[e] : y;
+        X.offer(w, row.first(q) + at, y);
+      }
     }
     if (tid < W && S.kind[tid] == 2) X.offer(tid, P.eos, 0.f);
     __syncthreads();
     fits = S.n_cand <= kSelList;
   }
   if (fits) rank_candidates(S, k);
-  else each_beam<E>(X);
+  else each_beam<E, U>(X);
   for (int i = tid; i < k; i += NT) {
     const int64_t to = b * k + i;
     const bool have = i < S.n_best;
-    const int at = have ? S.best_at[i] : -1, w = have ? at / P.V : -1, v = have ? at % P.V : -1;
-    P.out_scores[to] = have ? (float)X.score(w, S.best_x[i]) : neg_inf();
+    const int at = have ? S.best_at[i] : -1;
+    const int w = at >> kTokenBits, v = have ? at & ((1 << kTokenBits) - 1) : -1;
+    P.out_scores[to] = have ? S.best_score[i] : neg_inf();
     P.parents[to] = w;
     P.tokens[to] = v;
     if (P.ended) P.ended[to] = have && (S.kind[w] == 2 || v == P.eos);
@@ -547,13 +607,13 @@ static cudaError_t launch_select_u(const SelectParams &P, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = s;
-  cfg.gridDim = dim3((unsigned)(P.B * P.W * P.nc), 1, 1);
+  cfg.gridDim = dim3((unsigned)(P.B * P.W * P.per_row), 1, 1);
   cfg.blockDim = dim3(kSelNT, 1, 1);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, sd_beam_stream_kernel<E, U>, P);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, sd_beam_stream_kernel<E, U>, P);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)P.B, 1, 1);
   cfg.blockDim = dim3(kEndNT, 1, 1);
-  return cudaLaunchKernelEx(&cfg, sd_beam_end_kernel<E>, P, U);
+  return cudaLaunchKernelEx(&cfg, sd_beam_end_kernel<E, U>, P);
 }
 
 template <typename E>
@@ -602,6 +662,7 @@ extern "C" sd_status_t sd_beam_select(const sd_beam_select_args *a, void *stream
   P.V = a->V;
   P.k = a->k;
   P.nc = cut.nc;
+  P.per_row = (cut.nc + kSelNT / 32 - 1) / (kSelNT / 32);
   P.share = cut.share;
   P.eos = a->eos;
   P.T = a->T;

@@ -43,8 +43,9 @@ def select(x, scores, k, T=1.0, finished=None, eos=-1, norm=None):
             q = torch.softmax(row, 0)
             far = (m - row).masked_fill(row == -math.inf, 0.0)
             # terms: 2^-22 of the device's power and 4 U of the exponent's rounding for each unit
-            # of it; at most 45 fp32 additions above one another
-            off = max(off, (4 + 45) * U + 4 * U * float((q * far).sum()))
+            # of it, twice (within a piece of the row and between pieces); at most 45 fp32
+            # additions above one another; at most 1024 pieces in whole units of 2^-31
+            off = max(off, (4 + 4 + 45 + 4) * U + 4 * U * float((q * far).sum()))
             lp = s + torch.log_softmax(row, 0)
             y, i = torch.sort(lp, descending=True, stable=True)
             keep = min(V, k + 1)
