@@ -24,6 +24,7 @@ constexpr int kSelSet = 4;       // lanes of a group
 constexpr int kSelSets = 32 / kSelSet;
 constexpr int kEndNT = 512;      // threads of a sequence's end
 constexpr int kEndU = 8;         // vectors of groups that one of them holds
+constexpr int kEndBins = 256;    // steps of the bound below the best
 constexpr int kSelList = 1024;   // listed groups, and candidates, of a sequence
 
 struct SelectParams {
@@ -192,6 +193,25 @@ __device__ __forceinline__ unsigned long long dord(double x) {
   return (unsigned long long)i ^ (i < 0 ? ~0ull : 1ull << 63);
 }
 
+// ln z for z >= 1, to 2^-28: z = 2^e m with m in [3/4, 3/2) and, with r = (m - 1) / (m + 1),
+// ln m = 2 atanh r = 2 (r + r^3 / 3 + r^5 / 5 + ...), whose terms beyond r^11 / 11 are below
+// 2^-33; ln 2 as 11357 / 2^14, whose multiples are exact, and the rest.  The
+// same in fp64 took 0.9 us longer.
+__device__ __forceinline__ ff ff_log(ff z) {
+  const int e = (__float_as_int(z.hi) + 0x00400000 >> 23) - 127;
+  const float scale = __int_as_float(127 - e << 23);
+  const ff m = ff{z.hi * scale, z.lo * scale};
+  const ff num = ff_add_f(m, -1.f), den = ff_add_f(m, 1.f);
+  const float r = __fdiv_rn(num.hi, den.hi);
+  const float rest = __fdiv_rn(fmaf(-r, den.hi, num.hi) + fmaf(-r, den.lo, num.lo), den.hi);
+  const float q = r * r;
+  const float p =
+      q * fmaf(q, fmaf(q, fmaf(q, fmaf(q, 1.f / 11.f, 1.f / 9.f), 1.f / 7.f), 0.2f), 1.f / 3.f);
+  const ff sum = two_sum((float)e * 0.69317626953125f, 2.f * r);
+  return fast_two_sum(sum.hi,
+                      sum.lo + fmaf((float)e, -2.9088971e-5f, 2.f * fmaf(r, p, rest)));
+}
+
 // What a sequence's end holds on chip.
 struct SelectEnd {
   // a beam: 0 offers nothing, 1 live, 2 finished; its score less the log of its sum
@@ -202,9 +222,9 @@ struct SelectEnd {
   unsigned hi[SD_MAX_BEAMS];          // its sum in units of 2^-10 and of 2^-31
   unsigned lo[SD_MAX_BEAMS];
   int bad[SD_MAX_BEAMS];
-  // an fp32 image of the ranked score: max((x - m) c + o, lowest)
-  float m[SD_MAX_BEAMS], c[SD_MAX_BEAMS], o[SD_MAX_BEAMS];
-  float size[SD_MAX_BEAMS];           // of what entered o
+  // an fp32 image of the ranked score, max((x - m) c + o, lowest): m, c, o, and the size of
+  // what entered o (negative: the beam's logits are not read)
+  float4 image[SD_MAX_BEAMS];
   int list[kSelList];                 // groups: beam in the upper half, piece and place
   unsigned long long key[kSelList];   // candidates: the order of their ranked scores,
   int at[kSelList];                   // beam and token (kTokenBits),
@@ -212,7 +232,8 @@ struct SelectEnd {
   unsigned long long best_key[SD_MAX_TOP];   // the k best, in order
   int best_at[SD_MAX_TOP];
   float best_score[SD_MAX_TOP];
-  unsigned short keys16[kEndNT];
+  int hist[kEndBins];                 // threads by how far their best lies below the best
+  int best;
   int warp_n[kEndNT / 32];
   float bound;
   int n_list, n_cand, n_best;
@@ -241,13 +262,13 @@ struct EndView {
     const int q = g / kSelSets * P.share + at;
     return at < P.share && q < r.nvec ? q : -1;
   }
-  __device__ __forceinline__ float approx(int w, float x) const {
-    return x > neg_inf() ? fmaxf(fmaf(x - S.m[w], S.c[w], S.o[w]), kLowest) : neg_inf();
+  static __device__ __forceinline__ float approx(const float4 &f, float x) {
+    return x > neg_inf() ? fmaxf(fmaf(x - f.x, f.y, f.z), kLowest) : neg_inf();
   }
   // a candidate; logits of a finished beam are not looked at
   __device__ __noinline__ void offer(int w, int v, float x) const {
     double c = S.base[w];
-    if (S.kind[w] == 1) c += ((double)x - (double)S.m[w]) * P.inv_T;
+    if (S.kind[w] == 1) c += ((double)x - (double)S.image[w].x) * P.inv_T;
     const int i = atomicAdd(&S.n_cand, 1);
     if (i < kSelList) {
       S.key[i] = dord(c * S.over[w]);
@@ -452,7 +473,9 @@ __global__ void __launch_bounds__(kEndNT, 1) sd_beam_end_kernel(const SelectPara
   float2 first = make_float2(neg_inf(), 0.f);
   if (warp < W * blocks) first = load_piece(warp);
   if (tid == 0) S.n_list = S.n_cand = 0;
+  if (tid < kEndBins) S.hist[tid] = 0;
   if (tid < SD_MAX_BEAMS) {
+    S.best = ford(neg_inf());
     S.top[tid] = ford(neg_inf());
     S.hi[tid] = S.lo[tid] = 0u;
     S.bad[tid] = 0;
@@ -479,7 +502,7 @@ __global__ void __launch_bounds__(kEndNT, 1) sd_beam_end_kernel(const SelectPara
     }
   });
   __syncthreads();
-  double z = 1.0;
+  ff z = ff{1.f, 0.f};
   if (mine) {
     int kind = s == neg_inf() ? 0 : ended ? 2 : 1, bad = 0;
     const float m = fdeord(S.top[lane]);
@@ -495,89 +518,148 @@ __global__ void __launch_bounds__(kEndNT, 1) sd_beam_end_kernel(const SelectPara
     } else if (kind == 1 && m == neg_inf()) {
       kind = 0;
     }
-    if (kind == 1)
-      z = (double)S.hi[lane] * 9.765625e-4 + (double)S.lo[lane] * 4.656612873077393e-10;
+    if (kind == 1) {   // the units' first 24 bits, and the others
+      const unsigned hi = S.hi[lane];
+      const float up = __uint2float_rz(hi), low = __uint2float_rn(hi - (unsigned)up);
+      z = fast_two_sum(up * 9.765625e-4f,
+                       fmaf(low, 9.765625e-4f, __uint2float_rn(S.lo[lane]) * 4.656612873077393e-10f));
+    }
     S.kind[lane] = kind;
-    S.m[lane] = m;
     // an fp32 image of what follows in 64 bits
     const float over = __fdividef(1.f, nm);
-    S.c[lane] = __fdividef(over, P.T);
-    const float log_z = 0.693147180559945309f * __log2f((float)z);
-    S.o[lane] = (s - log_z) * over;
-    S.size[lane] = kind == 1 ? (fabsf(s) + log_z + 1.f) * over : 0.f;
+    const float log_z = 0.693147180559945309f * __log2f(z.hi);
+    S.image[lane] = make_float4(m, __fdividef(over, P.T), (s - log_z) * over,
+                                kind == 1 ? (fabsf(s) + log_z + 1.f) * over : -1.f);
     if (bad && P.status) atomicOr(P.status, bad);
   }
   __syncthreads();
-  // calls f(vector, its place, its beam) for the groups' largest of the beams that are read
+  // the best of each thread's groups
   const float inv_per = 1.f / (float)per;
-  const auto each_vector = [&](auto f) {
+  float best = neg_inf(), size = 0.f;
 #pragma unroll
-    for (int u = 0; u < kEndU; ++u) {
-      const int i = tid + u * NT;
-      if (i >= all) break;
-      const int w = (int)(((float)i + 0.5f) * inv_per);
-      if (S.kind[w] == 1) f(held[u], i, w);
+  for (int u = 0; u < kEndU; ++u) {
+    const int i = tid + u * NT;
+    if (u * NT < all) {
+      const float4 f = S.image[min((int)(((float)i + 0.5f) * inv_per), W - 1)];
+      const float x = X.approx(f, Elt<float>::vmax(held[u]));
+      if (i < all && f.w >= 0.f) best = fmaxf(best, x);
     }
+  }
 #pragma unroll 1
-    for (int i = tid + kEndU * NT; i < all; i += NT)
-      if (S.kind[i / per] == 1) f(ld16(gm + (int64_t)i * 4), i, i / per);
-  };
-  // the best of each thread's groups, and what k of them reach
-  float best = neg_inf();
-  each_vector([&](const uint4 &v, int, int w) {
-    best = fmaxf(best, X.approx(w, Elt<float>::vmax(v)));
-  });
-  S.keys16[tid] = top_key16(best);
+  for (int i = tid + kEndU * NT; i < all; i += NT) {
+    const float4 f = S.image[i / per];
+    if (f.w >= 0.f) best = fmaxf(best, X.approx(f, Elt<float>::vmax(ld16(gm + (int64_t)i * 4))));
+  }
+  if (tid < W) size = S.image[tid].w;
+  const int most = __reduce_max_sync(0xffffffffu, ford(best));
+  if (lane == 0) atomicMax(&S.best, most);
+  __syncthreads();
+  // what k of them reach: of d + 1, d how far one lies below the best of all, the exponent and the
+  // four leading bits are counted (steps of 1/16 at first, of 1/2 from 7 on); no bound is known
+  // where the k-th lies more than 2^16 below
+  const float top = fdeord(S.best);
+  if (best > neg_inf())
+    atomicAdd(&S.hist[min(__float_as_int(top - best + 1.f) - 0x3f800000 >> 19, kEndBins - 1)], 1);
   __syncthreads();
   if (warp == 0) {
-    const float found = top_bound_warp<NT>(S.keys16, k);
-    if (lane == 0) S.bound = found;
+    constexpr int J = kEndBins / 32;
+    int n[J], upto = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) upto += n[j] = S.hist[lane * J + j];
+    const int here = upto;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      upto += lane >= o ? y : 0;
+    }
+    const unsigned enough = __ballot_sync(0xffffffffu, upto >= k);
+    size = rmax_f(size);
+    float bound = kLowest;
+    if (enough) {
+      if (lane == __ffs(enough) - 1) {
+        int j = 0, at = upto - here;
+#pragma unroll
+        for (; j < J - 1; ++j) {
+          at += n[j];
+          if (at >= k) break;
+        }
+        const int bin = lane * J + j;
+        if (bin < kEndBins - 1)
+          bound = top - (__int_as_float((bin + 1 << 19) + 0x3f800000) - 1.f);
+      }
+      bound = __shfl_sync(0xffffffffu, bound, __ffs(enough) - 1);
+    }
+    // the image is off by less than 2^-19 of its own size and of what entered o (quotients of two
+    // steps, a logarithm of 2^-22 near one): the groups that reach the bound and the logits
+    // held against it by at most twice that
+    if (bound > kLowest)
+      bound = fmaxf(bound - (fabsf(bound) + size) * 3.814697265625e-6f, kLowest);
+    if (lane == 0) S.bound = bound;
   } else if (mine) {   // meanwhile the beams' numbers in 64 bits
-    S.base[lane] = (double)s - log(z);
+    const ff log_z = ff_log(z);
+    S.base[lane] = ((double)s - (double)log_z.hi) - (double)log_z.lo;
     S.over[lane] = P.norm ? 1.0 / (double)nm : 1.0;
   }
   __syncthreads();
-  float bound = S.bound, size = 0.f;
-  for (int w = 0; w < W; ++w) size = fmaxf(size, S.size[w]);
-  // the fp32 image is off by less than 2^-19 of its own size and of what entered o (quotients of two
-  // steps, a logarithm of 2^-22 near one): the groups that reach the bound and the logits
-  // held against it by at most twice that
-  if (bound > kLowest)
-    bound = fmaxf(bound - (fabsf(bound) + size) * 3.814697265625e-6f, kLowest);
-  if (best >= bound)
-    each_vector([&](const uint4 &v, int i, int w) {
-      if (!(X.approx(w, Elt<float>::vmax(v)) >= bound)) return;
-      float f[4];
-      Elt<float>::unpack(v, f);
-#pragma unroll 1
+  const float bound = S.bound;
+  if (best >= bound) {
+    const auto list = [&](const uint4 &v, int i, int w) {
+      const float4 f = S.image[w];
+      if (f.w < 0.f || !(X.approx(f, Elt<float>::vmax(v)) >= bound)) return;
+      const float x[4] = {__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                          __uint_as_float(v.w)};
+#pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (X.approx(w, e == 0 ? f[0] : e == 1 ? f[1] : e == 2 ? f[2] : f[3]) >= bound) {
+        if (X.approx(f, x[e]) >= bound) {
           const int at = atomicAdd(&S.n_list, 1);
           if (at < kSelList) S.list[at] = w << 16 | ((i - w * per) * 4 + e);
         }
-    });
+    };
+#pragma unroll
+    for (int u = 0; u < kEndU; ++u)
+      if (tid + u * NT < all) list(held[u], tid + u * NT, (int)((tid + u * NT + 0.5f) * inv_per));
+#pragma unroll 1
+    for (int i = tid + kEndU * NT; i < all; i += NT) list(ld16(gm + (int64_t)i * 4), i, i / per);
+  }
   __syncthreads();
   bool fits = S.n_list <= kSelList;
   if (fits) {
     const int items = S.n_list * X.kSize;
+    constexpr int kAhead = 2;
 #pragma unroll 1
-    for (int i = tid; i < items; i += NT) {
-      const int g = S.list[i / X.kSize], w = g >> 16;
-      const ElemRow<E> row = X.row(w);
-      const int q = X.vector(row, g & 0xffff, i % X.kSize);
-      if (q < 0) continue;
-      float x[VE];
-      Elt<E>::unpack(row.load(q), x);
-      unsigned pass = 0u;
+    for (int i0 = tid; i0 < items; i0 += kAhead * NT) {
+      uint4 v[kAhead];
+      int at[kAhead];
 #pragma unroll
-      for (int e = 0; e < VE; ++e) pass |= (X.approx(w, x[e]) >= bound ? 1u : 0u) << e;
-      while (pass) {
-        const int at = __ffs(pass) - 1;
-        pass &= pass - 1;
-        float y = x[0];
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = i0 + u * NT;
+        at[u] = -1;
+        if (i >= items) continue;
+        const int g = S.list[i / X.kSize];
+        const ElemRow<E> row = X.row(g >> 16);
+        const int q = X.vector(row, g & 0xffff, i % X.kSize);
+        if (q < 0) continue;
+        v[u] = row.load(q);
+        at[u] = (g >> 16) << kTokenBits | row.first(q);
+      }
 #pragma unroll
-        for (int e = 1; e < VE; ++e) y = at == e ? x[e] : y;
-        X.offer(w, row.first(q) + at, y);
+      for (int u = 0; u < kAhead; ++u) {
+        if (at[u] < 0) continue;
+        const int w = at[u] >> kTokenBits;
+        const float4 f = S.image[w];
+        float x[VE];
+        Elt<E>::unpack(v[u], x);
+        unsigned pass = 0u;
+#pragma unroll
+        for (int e = 0; e < VE; ++e) pass |= (X.approx(f, x[e]) >= bound ? 1u : 0u) << e;
+        while (pass) {
+          const int j = __ffs(pass) - 1;
+          pass &= pass - 1;
+          float y = x[0];
+#pragma unroll
+          for (int e = 1; e < VE; ++e) y = j == e ? x[e] : y;
+          X.offer(w, (at[u] & ((1 << kTokenBits) - 1)) + j, y);
+        }
       }
     }
     if (tid < W && S.kind[tid] == 2) X.offer(tid, P.eos, 0.f);
