@@ -24,6 +24,7 @@ constexpr int kSelSet = 4;       // lanes of a group
 constexpr int kSelSets = 32 / kSelSet;
 constexpr int kEndNT = 512;      // threads of a sequence's end
 constexpr int kEndU = 8;         // vectors of groups that one of them holds
+constexpr int kEndPieces = 2;    // pieces that a lane holds
 constexpr int kEndBins = 256;    // steps of the bound below the best
 constexpr int kSelList = 1024;   // listed groups, and candidates, of a sequence
 
@@ -466,12 +467,17 @@ __global__ void __launch_bounds__(kEndNT, 1) sd_beam_end_kernel(const SelectPara
     const int w = i / blocks, at = i % blocks * 32 + lane;
     return at < P.nc ? __ldcg(P.part + (b * W + w) * P.nc + at) : make_float2(neg_inf(), 0.f);
   };
-  const auto each_block = [&](const float2 &first, auto f) {
+  float2 piece[kEndPieces];
+#pragma unroll
+  for (int u = 0; u < kEndPieces; ++u)
+    if (warp + u * NW < W * blocks) piece[u] = load_piece(warp + u * NW);
+  const auto each_block = [&](auto f) {
+#pragma unroll
+    for (int u = 0; u < kEndPieces; ++u)
+      if (warp + u * NW < W * blocks) f((warp + u * NW) / blocks, piece[u]);
 #pragma unroll 1
-    for (int i = warp; i < W * blocks; i += NW) f(i / blocks, i == warp ? first : load_piece(i));
+    for (int i = warp + kEndPieces * NW; i < W * blocks; i += NW) f(i / blocks, load_piece(i));
   };
-  float2 first = make_float2(neg_inf(), 0.f);
-  if (warp < W * blocks) first = load_piece(warp);
   if (tid == 0) S.n_list = S.n_cand = 0;
   if (tid < kEndBins) S.hist[tid] = 0;
   if (tid < SD_MAX_BEAMS) {
@@ -482,13 +488,13 @@ __global__ void __launch_bounds__(kEndNT, 1) sd_beam_end_kernel(const SelectPara
   }
   __syncthreads();
   // their largest logit, then their sums in whole units, which come out the same in any order
-  each_block(first, [&](int w, const float2 &p) {
+  each_block([&](int w, const float2 &p) {
     const int m = __reduce_max_sync(0xffffffffu, ford(p.x));
     if (lane == 0) atomicMax(&S.top[w], m);
   });
   __syncthreads();
   const float c2 = log2e_over(P.T);
-  each_block(first, [&](int w, const float2 &p) {
+  each_block([&](int w, const float2 &p) {
     // at most 2^11; a piece with a NaN or +inf has a sum of NaN
     const float t = p.y == 0.f ? 0.f : p.y * ex2((p.x - fdeord(S.top[w])) * c2);
     const float units = t * 1024.f, whole = truncf(units);
