@@ -15,7 +15,7 @@ from typing import NamedTuple
 import torch
 
 from . import _P, _check, _need
-from .kv import _i32, _meet, _on_device, _workspace
+from .kv import _i32, _meet, _on_device, _scratch
 from .logits import _lib, _rows, _same, _stream_of, _written
 
 SD_MAX_BEAMS, SD_MAX_STATES = 32, 16
@@ -63,7 +63,7 @@ def _bind(L):
 
 @_on_device
 def beam_select(logits, scores, k: int, *, temperature: float = 1.0, finished=None, eos: int = -1,
-                norm=None, out: Beams | None = None, status=None, stream=None) -> Beams:
+                norm=None, out: Beams | None = None, status=None) -> Beams:
     """The k best continuations of each sequence's beams: of scores [B][W] (float32, -inf: a
     beam that is dead) plus the log-softmax at `temperature` of logits [B][W][V] (float32 or
     bfloat16, contiguous rows), ranked by their score over norm [B][W] (float32, optional), ties
@@ -73,7 +73,9 @@ def beam_select(logits, scores, k: int, *, temperature: float = 1.0, finished=No
     dev = logits.device
     B, W, V = logits.shape
     a = SelectArgs(B, W, V, k, dt, logits.data_ptr(), logits.stride(0), logits.stride(1))
-    _need(scores, "scores", torch.float32, (B, W), dev)
+    if scores.dtype is not torch.float32 or scores.device != dev or scores.shape != (B, W) \
+            or not scores.is_contiguous():
+        _need(scores, "scores", torch.float32, (B, W), dev)
     a.scores, a.eos, a.T = scores.data_ptr(), eos, temperature
     if finished is not None:
         _need(finished, "finished", torch.uint8, (B, W), dev)
@@ -82,29 +84,33 @@ def beam_select(logits, scores, k: int, *, temperature: float = 1.0, finished=No
     if norm is not None:
         _need(norm, "norm", torch.float32, (B, W), dev)
         a.norm = norm.data_ptr()
-    given = out is not None
-    if given:
+    if status is not None:
+        a.status = _i32(status, "status", (1,), dev)
+    n = _scratch("sd_beam_select_workspace_size", dev.index, B, W, V, dt) if B else 0
+    ws = torch.empty(n, dtype=torch.int32, device=dev)
+    given = ()
+    if out is None:
+        out = Beams(torch.empty((B, k), dtype=torch.float32, device=dev),
+                    torch.empty((B, k), dtype=torch.int32, device=dev),
+                    torch.empty((B, k), dtype=torch.int32, device=dev),
+                    torch.empty((B, k), dtype=torch.uint8, device=dev))
+        a.parents, a.tokens = out.parents.data_ptr(), out.tokens.data_ptr()
+    else:
         _need(out.scores, "out.scores", torch.float32, (B, k), dev)
         _need(out.finished, "out.finished", torch.uint8, (B, k), dev)
+        a.parents = _i32(out.parents, "out.parents", (B, k), dev)
+        a.tokens = _i32(out.tokens, "out.tokens", (B, k), dev)
+        given = out
         for t in out:
             if any(_meet(t, x) for x in (logits, scores, finished, norm) if x is not None):
                 raise ValueError("out overlaps the input")
-    else:
-        e = lambda t: torch.empty((B, k), dtype=t, device=dev)
-        out = Beams(e(torch.float32), e(torch.int32), e(torch.int32), e(torch.uint8))
     a.out_scores, a.ended = out.scores.data_ptr(), out.finished.data_ptr()
-    a.parents = _i32(out.parents, "out.parents", (B, k), dev)
-    a.tokens = _i32(out.tokens, "out.tokens", (B, k), dev)
-    if status is not None:
-        a.status = _i32(status, "status", (1,), dev)
-    if B:
-        a.workspace_bytes = _lib().sd_beam_select_workspace_size(B, W, V, dt)
-        ws = _workspace(a.workspace_bytes, dev)
-        a.workspace = ws.data_ptr()
-    _check(_lib().sd_beam_select(a, _stream_of(dev)), "sd_beam_select")
-    if given:
-        for t in out:
-            _written(t)
+    a.workspace, a.workspace_bytes = ws.data_ptr(), 4 * n
+    rc = _lib().sd_beam_select(a, _stream_of(dev))
+    if rc:
+        _check(rc, "sd_beam_select")
+    for t in given:
+        _written(t)
     return out
 
 
@@ -123,7 +129,7 @@ def _state(x, name, B, W, dev):
 
 
 @_on_device
-def beam_reorder(states, parents, *, out=None, status=None, stream=None):
+def beam_reorder(states, parents, *, out=None, status=None):
     """States [B][W][...] (a tensor or a sequence of up to 16, any types, rows contiguous) in the
     order of parents [B][k] (int32, beam_select's): row i of a sequence is row parents[b][i], and
     for -1 row i itself.  Returns new tensors [B][k][...], or `out`: the same tensors (k = W), to
@@ -161,8 +167,10 @@ def beam_reorder(states, parents, *, out=None, status=None, stream=None):
                                  y.stride(0) * y.element_size(), y.stride(1) * y.element_size(), r)
                                 for x, y, r in zip(xs, ys, rows)))
     st = None if status is None else _i32(status, "status", (1,), dev)
-    _check(_lib().sd_beam_reorder(B, W, k, parents.data_ptr(), len(xs), ctypes.addressof(a), st,
-                                  _stream_of(dev)), "sd_beam_reorder")
+    rc = _lib().sd_beam_reorder(B, W, k, parents.data_ptr(), len(xs), ctypes.addressof(a), st,
+                                _stream_of(dev))
+    if rc:
+        _check(rc, "sd_beam_reorder")
     if out is not None:
         for y in ys:
             _written(y)

@@ -16,7 +16,8 @@ namespace sdv {
 constexpr int kPgNT = 1024;              // threads of a chunk's CTA, and of the plan's
 constexpr int kPgChunk = 8192;           // pages of a chunk
 constexpr int kPgWords = kPgChunk / 32;
-constexpr int kRowNT = 128;              // threads of a row's CTA
+constexpr int kRowNT = 128;              // threads for the slots of a row
+constexpr int kRowU = 4;                 // slots of one of them in flight
 constexpr int kRowSlots = 512;           // slots that get pages at a time
 
 static int page_chunks(int N) { return (N + kPgChunk - 1) / kPgChunk; }
@@ -37,6 +38,19 @@ __device__ __forceinline__ bool give_back(int32_t *refs, int page) {
   if (atomicSub(refs + page, 1) > 0) return true;
   atomicAdd(refs + page, 1);
   return false;
+}
+
+// The same of U pages at a time, -1 and ids that are none passed over; held: how many held each.
+template <int U>
+__device__ __forceinline__ void give_back(int32_t *refs, int N, const int (&e)[U], int (&held)[U]) {
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    held[u] = 0;
+    if ((unsigned)e[u] < (unsigned)N) held[u] = atomicSub(refs + e[u], 1);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if ((unsigned)e[u] < (unsigned)N && held[u] <= 0) atomicAdd(refs + e[u], 1);
 }
 
 // The bits of a chunk's pages that are free (or in use), and how many.
@@ -110,6 +124,21 @@ struct ForkSpan {
   }
 };
 
+// What a row's plan reads of its parent.
+struct ForkLook {
+  int parent, len, last, refs;   // refs: of the last page
+};
+__device__ __forceinline__ ForkLook fork_look(const ForkParams &P, int r) {
+  ForkLook k = {r < P.R ? fork_parent(P, r, true) : -1, 0, -1, 0};
+  if (k.parent >= 0) {
+    k.len = (int)min((int64_t)max(ld_int(P.kv_len + k.parent), 0), (int64_t)P.M * P.page_size);
+    const ForkSpan s(P, k.len);
+    if (s.part) k.last = ld_int(P.table + (int64_t)k.parent * P.M + s.full);
+    if ((unsigned)k.last < (unsigned)P.N) k.refs = ld_int(P.refs + k.last);
+  }
+  return k;
+}
+
 // The rows' plan, by one CTA: heirs, and the ranks of the pages and copies that
 // the rows need.
 __device__ void plan_rows(const ForkParams &P, int *smem) {
@@ -117,13 +146,14 @@ __device__ void plan_rows(const ForkParams &P, int *smem) {
   int *first = smem, *kids = smem + P.rows_in;   // of each old row
   __shared__ unsigned long long warp_sum_s[NW];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const ForkLook look0 = fork_look(P, tid);   // under way meanwhile
   for (int p = tid; p < P.rows_in; p += NT) {
     first[p] = INT32_MAX;
     kids[p] = 0;
   }
   __syncthreads();
   for (int r = tid; r < P.R; r += NT) {
-    const int p = fork_parent(P, r, true);
+    const int p = r == tid ? look0.parent : fork_parent(P, r, false);
     if (p < 0) continue;
     atomicMin(&first[p], r);
     atomicAdd(&kids[p], 1);
@@ -133,23 +163,19 @@ __device__ void plan_rows(const ForkParams &P, int *smem) {
   unsigned long long before = 0ull;   // pages, and copies in the upper half
   for (int r0 = 0; r0 < P.R; r0 += NT) {
     const int r = r0 + tid;
-    ForkRow row = {-1, 0, 0, 0, 0, 0, 0, -1};
-    if (r < P.R) row.parent = fork_parent(P, r, false);
+    const ForkLook look = r0 == 0 ? look0 : fork_look(P, r);
+    ForkRow row = {look.parent, look.len, 0, 0, 0, 0, 0, look.last};
     if (row.parent >= 0) {
       const int p = row.parent;
-      row.len = (int)min((int64_t)max(ld_int(P.kv_len + p), 0), (int64_t)P.M * P.page_size);
       const ForkSpan s(P, row.len);
       const int32_t *old = P.table + (int64_t)p * P.M;
       const bool lead = first[p] == r, heir = lead && !P.keep;
       row.kids = kids[p];
       row.flags = (lead ? kLead : 0) | (heir ? kHeir : 0);
       if (s.cut) set_status(P.status, SD_STATUS_NO_PAGE);
-      if (s.part) {
-        row.last = ld_int(old + s.full);
-        if ((unsigned)row.last < (unsigned)P.N && !(heir && ld_int(P.refs + row.last) == 1)) {
-          row.flags |= kCopy;
-          row.pages = 1;
-        }
+      if (s.part && (unsigned)row.last < (unsigned)P.N && !(heir && look.refs == 1)) {
+        row.flags |= kCopy;
+        row.pages = 1;
       }
       if (heir) {
 #pragma unroll 4
@@ -244,51 +270,57 @@ __device__ __forceinline__ int free_pages(const uint32_t *bits, const int32_t *c
   return q;
 }
 
-__global__ void __launch_bounds__(kRowNT) sd_kv_rows_kernel(const ForkParams P) {
+// A CTA per row, new and old: four warps share the new row's slots out and give the old one's
+// pages back, the fifth finds the new row's own pages.
+__global__ void __launch_bounds__(kRowNT + 32) sd_kv_rows_kernel(const ForkParams P) {
   __shared__ int slots[kRowSlots];
   pdl();
   const int i = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
   unsigned bad = 0u;
+  const int kids = i < P.rows_in ? ld_int(P.kids + i) : 1;
   if (i < P.R) {
     const ForkRow row = P.plan[i];
-    const ForkSpan s(P, row.len);
+    ForkSpan s(P, row.len);
+    if (row.parent < 0) s.need = 0;   // an empty row has no room either
     const bool in_place = !P.parents, heir = row.flags & kHeir, copy = row.flags & kCopy;
     const int32_t *old = P.table + (int64_t)row.parent * P.M;
     int32_t *out = P.table_out + (int64_t)i * P.M;
-    // whoever leads a parent's rows counts for all of them
-    const int add = !(row.flags & kLead) ? 0 : P.keep ? row.kids : row.kids - 1;
-    if (row.parent < 0) {
-      for (int j = tid; j < P.M; j += kRowNT) out[j] = -1;
-    } else {
-      for (int j = tid; j < P.M; j += kRowNT) {
-        if (in_place && j != s.full) {
-          if (j < s.full && (unsigned)ld_int(old + j) >= (unsigned)P.N) bad |= SD_STATUS_BAD_PAGE;
-          continue;
+    if (tid < kRowNT) {
+      // whoever leads a parent's rows counts for all of them
+      const int add = !(row.flags & kLead) ? 0 : P.keep ? row.kids : row.kids - 1;
+      for (int j0 = tid; j0 < P.M; j0 += kRowU * kRowNT) {
+        int e[kRowU];
+#pragma unroll
+        for (int u = 0; u < kRowU; ++u) {
+          const int j = j0 + u * kRowNT;
+          e[u] = j < P.M && row.parent >= 0 ? ld_int(old + j) : -1;
         }
-        const int e = ld_int(old + j);
-        const bool page = (unsigned)e < (unsigned)P.N;
-        int to = e;
-        if (j < s.full) {
-          if (!page) bad |= SD_STATUS_BAD_PAGE;
-          else if (add) atomicAdd(P.refs + e, add);
-        } else if (j < s.used) {
-          if (!page) bad |= SD_STATUS_BAD_PAGE;
-          if (copy) {
-            if (heir && !give_back(P.refs, e)) bad |= SD_STATUS_BAD_PAGE;
-            continue;   // gets a page below
+#pragma unroll
+        for (int u = 0; u < kRowU; ++u) {
+          const int j = j0 + u * kRowNT;
+          if (j >= P.M) break;
+          const bool page = (unsigned)e[u] < (unsigned)P.N;
+          if (j < s.used && !page) bad |= SD_STATUS_BAD_PAGE;
+          if (j < s.full && page && add) atomicAdd(P.refs + e[u], add);
+          if (j >= s.full && j < s.used && copy) {   // gets a page of its own
+            if (heir && !give_back(P.refs, e[u])) bad |= SD_STATUS_BAD_PAGE;
+            continue;
           }
-        } else if (j < s.need) {
-          if (!(heir && page)) continue;   // gets a page below
-        } else if (!heir) {
-          to = -1;
+          if (j >= s.used && j < s.need && !(heir && page)) continue;   // gets a page
+          if (!in_place) out[j] = j < s.need || heir ? e[u] : -1;
         }
-        if (!in_place) out[j] = to;
       }
-    }
-    if (tid == 0 && P.len_out) P.len_out[i] = row.len;
-    if (tid < 32 && row.pages > 0) {
+    } else {
+      if (lane == 0) {
+        if (P.len_out) P.len_out[i] = row.len;
+        if (i >= ld_int(P.count)) {
+          P.src[i] = -1;
+          P.dst[i] = -1;
+          P.fill[i] = 0;
+        }
+        if (copy) P.fill[row.pair] = s.part;
+      }
       // slots that get a page, in order, a batch at a time
-      if (copy && lane == 0) P.fill[row.pair] = s.part;
       int j0 = s.used, done = 0;
       bool first = copy;
       while (done < row.pages) {
@@ -330,17 +362,17 @@ __global__ void __launch_bounds__(kRowNT) sd_kv_rows_kernel(const ForkParams P) 
         first = false;
       }
     }
-    if (tid == 32 && i >= ld_int(P.count)) {
-      P.src[i] = -1;
-      P.dst[i] = -1;
-      P.fill[i] = 0;
-    }
   }
-  if (i < P.rows_in && !P.keep && ld_int(P.kids + i) == 0) {   // ends without an heir
-    for (int j = tid; j < P.M; j += kRowNT) {
-      const int e = ld_int(P.table + (int64_t)i * P.M + j);
-      if (e == -1) continue;
-      if ((unsigned)e >= (unsigned)P.N || !give_back(P.refs, e)) bad |= SD_STATUS_BAD_PAGE;
+  if (tid < kRowNT && !P.keep && kids == 0) {   // ends without an heir
+    const int32_t *old = P.table + (int64_t)i * P.M;
+    for (int j0 = tid; j0 < P.M; j0 += kRowU * kRowNT) {
+      int e[kRowU], held[kRowU];
+#pragma unroll
+      for (int u = 0; u < kRowU; ++u) e[u] = j0 + u * kRowNT < P.M ? ld_int(old + j0 + u * kRowNT) : -1;
+      give_back(P.refs, P.N, e, held);
+#pragma unroll
+      for (int u = 0; u < kRowU; ++u)
+        if (e[u] != -1 && held[u] <= 0) bad |= SD_STATUS_BAD_PAGE;
     }
   }
   if (bad) set_status(P.status, bad);
@@ -366,10 +398,12 @@ __global__ void __launch_bounds__(kFreeNT) sd_kv_free_kernel(int64_t cols, int p
     e[u] = c < end ? ld_int(pages + row * cols + c) : -1;
   }
   bool bad = false;
+  int held[kFreeU];
+  give_back(refs, N, e, held);
 #pragma unroll
   for (int u = 0; u < kFreeU; ++u) {
     if (e[u] == -1) continue;
-    bad |= (unsigned)e[u] >= (unsigned)N || !give_back(refs, e[u]);
+    bad |= held[u] <= 0;
     if (clear) pages[row * cols + c0 + u * kFreeNT] = -1;
   }
   if (bad) set_status(status, SD_STATUS_BAD_PAGE);
@@ -588,7 +622,7 @@ extern "C" sd_status_t sd_kv_fork(const sd_kv_fork_args *a, void *stream) {
   cudaError_t e = cudaLaunchKernelEx(&plan.cfg, sd_kv_plan_kernel, P);
   const int rows = std::max(P.R, P.rows_in);
   if (e == cudaSuccess && rows > 0) {
-    PageLaunch each(rows, kRowNT, 0, s);
+    PageLaunch each(rows, kRowNT + 32, 0, s);
     e = cudaLaunchKernelEx(&each.cfg, sd_kv_rows_kernel, P);
   }
   return e == cudaSuccess ? SD_OK : SD_ERR_CUDA;

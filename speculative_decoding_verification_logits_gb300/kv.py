@@ -90,15 +90,17 @@ def _bind(L):
             raise RuntimeError(f"{mirror.__name__} layout differs between library and binding")
 
 
+_device = torch._C._cuda_getDevice   # the current one's index
+
+
 def _on_device(fn):
     """Runs a wrapper with its first tensor's device as the current one, and with `stream` (when
     given) as the current stream: what it allocates belongs to the stream that it launches on."""
     @functools.wraps(fn)
-    def call(*args, **kwargs):
+    def call(*args, stream=None, **kwargs):
         t = args[0] if args else next(iter(kwargs.values()), None)
         while isinstance(t, (list, tuple)) and t:
             t = t[0]
-        stream = kwargs.get("stream")
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             return fn(*args, **kwargs)   # which says what is wrong
         if stream is not None:
@@ -106,7 +108,7 @@ def _on_device(fn):
                 raise ValueError(f"stream is on {stream.device}, expected {t.device}")
             with torch.cuda.stream(stream):
                 return fn(*args, **kwargs)
-        if t.device.index != torch.cuda.current_device():
+        if t.get_device() != _device():
             with torch.cuda.device(t.device):
                 return fn(*args, **kwargs)
         return fn(*args, **kwargs)
@@ -123,10 +125,12 @@ def _i32(t, name, shape, device):
 
 def _span(t):
     """The addresses that a tensor reaches over, or none."""
-    if not t.numel():
+    n, at = t.numel(), t.data_ptr()
+    if not n:
         return 0, 0
-    return t.data_ptr(), t.data_ptr() + t.element_size() * (
-        1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))
+    if not t.is_contiguous():
+        n = 1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+    return at, at + t.element_size() * n
 
 
 def _meet(a, b):
@@ -135,43 +139,58 @@ def _meet(a, b):
 
 
 def _pool(refs, device):
-    if refs.dim() != 1 or refs.numel() < 1:
+    shape = refs.shape
+    if len(shape) != 1 or shape[0] < 1:
         raise ValueError("refs must be [N], with N >= 1")
-    return _i32(refs, "refs", refs.shape, device), refs.numel()
+    return _i32(refs, "refs", shape, device), shape[0]
 
 
 def _table(block_table, kv_len):
-    _need(block_table, "block_table", _I32)
-    if block_table.dim() != 2:
+    dev, shape = block_table.device, block_table.shape
+    if len(shape) != 2:
         raise ValueError("block_table must be [rows][max_pages]")
-    rows, M = block_table.shape
-    return rows, M, _i32(kv_len, "kv_len", (rows,), block_table.device)
+    return (*shape, _i32(block_table, "block_table", shape, dev if block_table.is_cuda else None),
+            _i32(kv_len, "kv_len", shape[:1], dev), dev)
 
 
-def _workspace(n, device):
-    """Scratch of one call: the allocator's, so that calls and captured graphs share none."""
+@functools.lru_cache(256)
+def _scratch(which, device, *sizes):
+    """int32s of scratch that a call needs on a device (by index).  It lies beside the call's
+    outputs, in one block of the allocator's: calls and captured graphs share none."""
+    n = getattr(_lib(), which)(*sizes)
     if n == 0:
         raise ValueError("sizes out of range")
-    return torch.empty(n, dtype=_U8, device=device)
+    return (n + 15) // 16 * 4
 
 
-def _fork(a, refs, status, dev):
+def _fork(a, refs, status, dev, sizes):
+    """Runs sd_kv_fork with new outputs of these sizes (in the struct's order) where there are
+    any; returns them."""
     a.refs, a.N = _pool(refs, dev)
     if status is not None:
         a.status = _i32(status, "status", (1,), dev)
-    n = a.workspace_bytes = _lib().sd_kv_fork_workspace_size(a.rows_in, a.R, a.N)
-    ws = _workspace(n, dev)
-    a.workspace = ws.data_ptr()
+    n = _scratch("sd_kv_fork_workspace_size", dev.index, a.rows_in, a.R, a.N)
+    sizes = (n, *sizes)
+    buf = torch.empty(sum(sizes), dtype=_I32, device=dev)
+    at = buf.data_ptr()
+    a.workspace, a.workspace_bytes = at, 4 * n
+    if len(sizes) > 1:
+        at += 4 * n
+        if len(sizes) == 7:
+            a.table_out, a.len_out = at, at + 4 * sizes[1]
+            at += 4 * (sizes[1] + sizes[2])
+        R = 4 * a.R
+        a.src, a.dst, a.fill, a.count = at, at + R, at + 2 * R, at + 3 * R
     rc = _lib().sd_kv_fork(a, _stream_of(dev))
     if rc:
         _check(rc, "sd_kv_fork")
     _written(refs)
+    return buf.split_with_sizes(sizes)
 
 
 @_on_device
 def kv_fork(block_table, kv_len, parents, refs, page_size: int, *, append: int = 0,
-            keep: bool = False, out: KVFork | None = None, status=None,
-            stream=None) -> KVFork:
+            keep: bool = False, out: KVFork | None = None, status=None) -> KVFork:
     """New rows from the rows of block_table [rows][max_pages] and kv_len [rows] (int32): row r
     shares the pages of its parent and has room for `append` more entries; refs [N] is brought
     up to date.  parents: int32 [R], rows of the table, or [B][k] relative to each of B groups of
@@ -181,9 +200,7 @@ def kv_fork(block_table, kv_len, parents, refs, page_size: int, *, append: int =
     row of each parent takes over what is the parent's own.  keep=True leaves the old rows as
     they are.  Either way the partly filled last page of every new row is its own: kv_copy(caches,
     f.src, f.dst, count=f.count, fill=f.fill) must follow before the rows are read."""
-    rows, M, lens = _table(block_table, kv_len)
-    dev = block_table.device
-    _need(parents, "parents", _I32, None, dev)
+    rows, M, table, lens, dev = _table(block_table, kv_len)
     shape = parents.shape
     if len(shape) not in (1, 2):
         raise ValueError("parents must be [R] or [B][k]")
@@ -194,77 +211,64 @@ def kv_fork(block_table, kv_len, parents, refs, page_size: int, *, append: int =
     if groups and rows % groups:
         raise ValueError(f"{rows} rows are not {groups} groups")
     a = ForkArgs(rows, R, groups, M, page_size, append, bool(keep))
-    given = out is not None
-    if given:
-        for x in (out.block_table, out.kv_len):
-            _need(x, "out", _I32, None, dev)
-            if any(_meet(x, y) for y in (block_table, kv_len, parents, refs)):
-                raise ValueError("out overlaps the input")
-        a.table_out = _i32(out.block_table, "out.block_table", (R, M), dev)
-        a.len_out = _i32(out.kv_len, "out.kv_len", (R,), dev)
-        a.src, a.dst, a.fill = (_i32(getattr(out, n), "out." + n, (R,), dev)
-                                for n in ("src", "dst", "fill"))
-        a.count = _i32(out.count, "out.count", (1,), dev)
-    else:   # one block of memory
-        buf = torch.empty(R * M + 4 * R + 1, dtype=_I32, device=dev)
-        t, n, src, dst, fill, count = buf.split((R * M, R, R, R, R, 1))
-        out = KVFork(t.view(R, M), n, src, dst, fill, count)
-        a.table_out = at = buf.data_ptr()
-        at += 4 * R * M
-        a.len_out, a.src, a.dst, a.fill, a.count = (at, at + 4 * R, at + 8 * R, at + 12 * R,
-                                                    at + 16 * R)
-    a.parents, a.table, a.kv_len = parents.data_ptr(), block_table.data_ptr(), lens
-    _fork(a, refs, status, dev)
-    if given:
-        for t in out:
-            _written(t)
+    a.parents, a.table, a.kv_len = _i32(parents, "parents", shape, dev), table, lens
+    if out is None:
+        _, t, n, src, dst, fill, count = _fork(a, refs, status, dev, (R * M, R, R, R, R, 1))
+        return KVFork(t.view(R, M), n, src, dst, fill, count)
+    for x in (out.block_table, out.kv_len):
+        _need(x, "out", _I32, None, dev)
+        if any(_meet(x, y) for y in (block_table, kv_len, parents, refs)):
+            raise ValueError("out overlaps the input")
+    a.table_out = _i32(out.block_table, "out.block_table", (R, M), dev)
+    a.len_out = _i32(out.kv_len, "out.kv_len", (R,), dev)
+    a.src, a.dst, a.fill = (_i32(getattr(out, n), "out." + n, (R,), dev)
+                            for n in ("src", "dst", "fill"))
+    a.count = _i32(out.count, "out.count", (1,), dev)
+    _fork(a, refs, status, dev, ())
+    for t in out:
+        _written(t)
     return out
 
 
 @_on_device
-def kv_extend(block_table, kv_len, refs, page_size: int, append: int, *, status=None,
-              stream=None) -> KVMoves:
+def kv_extend(block_table, kv_len, refs, page_size: int, append: int, *, status=None) -> KVMoves:
     """Room for `append` more entries in every row of block_table, in place: its rows get free
     pages, and a partly filled last page that others hold too becomes the row's own (kv_copy of
     the returned pairs must follow where rows may share one)."""
-    rows, M, lens = _table(block_table, kv_len)
-    dev = block_table.device
+    rows, M, table, lens, dev = _table(block_table, kv_len)
     a = ForkArgs(rows, rows, 0, M, page_size, append, 0)
-    buf = torch.empty(3 * rows + 1, dtype=_I32, device=dev)
-    at = buf.data_ptr()
-    a.src, a.dst, a.fill, a.count = at, at + 4 * rows, at + 8 * rows, at + 12 * rows
-    a.table = a.table_out = block_table.data_ptr()
+    a.table = a.table_out = table
     a.kv_len = lens
-    _fork(a, refs, status, dev)
+    m = _fork(a, refs, status, dev, (rows, rows, rows, 1))
     _written(block_table)
-    return KVMoves(*buf.split((rows, rows, rows, 1)))
+    return KVMoves(*m[1:])
 
 
 @_on_device
-def kv_free(pages, refs, *, which=None, count=None, clear: bool = False, status=None,
-            stream=None) -> torch.Tensor:
+def kv_free(pages, refs, *, which=None, count=None, clear: bool = False, status=None) -> torch.Tensor:
     """Gives pages back to refs [N], in place: the ids in pages (int32, any shape; -1 is passed
     over), as kv_rollback lists them (pages=freed, count=free_offsets[-1:]), or the rows of a
     block table (which [rows] uint8: those whose flag is set).  clear=True makes the entries that
     are taken -1."""
-    _need(pages, "pages", _I32)
-    dev = pages.device
+    dev, shape = pages.device, pages.shape
+    p = _i32(pages, "pages", shape, dev if pages.is_cuda else None)
     ref, N = _pool(refs, dev)
     if _meet(pages, refs):
         raise ValueError("pages overlaps refs")
     rows, cols, w, n, st = 1, pages.numel(), None, None, None
     if which is not None:
-        if pages.dim() != 2:
+        if len(shape) != 2:
             raise ValueError("which needs pages [rows][max_pages]")
-        rows, cols = pages.shape
+        rows, cols = shape
         _need(which, "which", _U8, (rows,), dev)
         w = which.data_ptr() if rows else None
     if count is not None:
         n = _i32(count, "count", (1,), dev)
     if status is not None:
         st = _i32(status, "status", (1,), dev)
-    _check(_lib().sd_kv_free(rows, cols, pages.data_ptr(), w, n, bool(clear), N, ref, st,
-                             _stream_of(dev)), "sd_kv_free")
+    rc = _lib().sd_kv_free(rows, cols, p, w, n, bool(clear), N, ref, st, _stream_of(dev))
+    if rc:
+        _check(rc, "sd_kv_free")
     _written(refs)
     if clear:
         _written(pages)
@@ -272,37 +276,36 @@ def kv_free(pages, refs, *, which=None, count=None, clear: bool = False, status=
 
 
 @_on_device
-def kv_compact(refs, block_table=None, *, status=None, stream=None) -> KVCompact:
+def kv_compact(refs, block_table=None, *, status=None) -> KVCompact:
     """Moves the pages in use to the front of the pool: refs [N] and the entries of block_table
     (int32, any shape) are brought up to date in place; kv_copy(caches, c.src, c.dst,
     count=c.count) must follow before the pages are read.  Other tables of the same pool take
     their ids from new_ids."""
-    _need(refs, "refs", _I32)
     dev = refs.device
-    ref, N = _pool(refs, dev)
-    h = N // 2
-    buf = torch.empty(N + 2 * h + 2, dtype=_I32, device=dev)
-    at = buf.data_ptr()
+    ref, N = _pool(refs, dev if refs.is_cuda else None)
     table, n_table, st = None, 0, None
     if block_table is not None:
-        _need(block_table, "block_table", _I32, None, dev)
+        p = _i32(block_table, "block_table", block_table.shape, dev)
         if _meet(block_table, refs):
             raise ValueError("block_table overlaps refs")
         n_table = block_table.numel()
-        table = block_table.data_ptr() if n_table else None
+        table = p if n_table else None
     if status is not None:
         st = _i32(status, "status", (1,), dev)
-    need = _lib().sd_kv_compact_workspace_size(N)
-    ws = _workspace(need, dev)
-    rc = _lib().sd_kv_compact(N, ref, n_table, table, at, at + 4 * h, at + 8 * h,
-                              at + 8 * h + 4, at + 8 * h + 8, st, ws.data_ptr(), need,
-                              _stream_of(dev))
+    n, h = _scratch("sd_kv_compact_workspace_size", dev.index, N), N // 2
+    sizes = (n, h, h, 1, 1, N)
+    buf = torch.empty(sum(sizes), dtype=_I32, device=dev)
+    ws = buf.data_ptr()
+    src = ws + 4 * n
+    count = src + 8 * h
+    rc = _lib().sd_kv_compact(N, ref, n_table, table, src, src + 4 * h, count, count + 4,
+                              count + 8, st, ws, 4 * n, _stream_of(dev))
     if rc:
         _check(rc, "sd_kv_compact")
     _written(refs)
     if n_table:
         _written(block_table)
-    src, dst, count, live, new = buf.split((h, h, 1, 1, N))
+    _, src, dst, count, live, new = buf.split_with_sizes(sizes)
     return KVCompact(src, dst, count, new, live)
 
 
@@ -317,8 +320,7 @@ def _page_shape(shape, strides, size, first, name):
 
 
 @_on_device
-def kv_copy(caches, src, dst, *, count=None, fill=None, heads_first: bool = False, status=None,
-            stream=None) -> None:
+def kv_copy(caches, src, dst, *, count=None, fill=None, heads_first: bool = False, status=None) -> None:
     """Copies page src[i] to page dst[i] (int32 [pairs], the first count [1] of them; -1, -1 is
     passed over) in every cache, in place.  caches: one tensor [layers][N][...] or a sequence of
     [N][...] of one shape (keys and values of every layer), any type.  fill [pairs]: only the
@@ -373,6 +375,8 @@ def kv_copy(caches, src, dst, *, count=None, fill=None, heads_first: bool = Fals
         a.count = _i32(count, "count", (1,), dev)
     if status is not None:
         a.status = _i32(status, "status", (1,), dev)
-    _check(_lib().sd_kv_copy(a, _stream_of(dev)), "sd_kv_copy")
+    rc = _lib().sd_kv_copy(a, _stream_of(dev))
+    if rc:
+        _check(rc, "sd_kv_copy")
     for t in tensors:
         _written(t)
