@@ -13,7 +13,7 @@
 
 namespace sdv {
 
-constexpr int kCpNT = 256, kCpCtas = 4;   // threads of a CTA, CTAs per SM
+constexpr int kCpNT = 256, kCpCtas = 2;   // threads of a CTA, CTAs per SM
 constexpr int kCpU = 8;                   // vectors of a piece per lane
 constexpr int kCpWarps = kCpNT / 32;
 
