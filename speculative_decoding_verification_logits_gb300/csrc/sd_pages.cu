@@ -17,7 +17,10 @@ constexpr int kPgNT = 1024;              // threads of a chunk's CTA, and of the
 constexpr int kPgChunk = 8192;           // pages of a chunk
 constexpr int kPgWords = kPgChunk / 32;
 constexpr int kRowNT = 128;              // threads for the slots of a row
+constexpr int kRowTeam = kRowNT + 32;    // and a warp for its new pages
 constexpr int kRowU = 4;                 // slots of one of them in flight
+constexpr int64_t kForkCluster = 1 << 15;     // slots of the rows that one cluster takes
+constexpr int64_t kCompactCluster = 1 << 14;  // pages, or entries of tables, that one takes
 constexpr int kRowSlots = 512;           // slots that get pages at a time
 
 static int page_chunks(int N) { return (N + kPgChunk - 1) / kPgChunk; }
@@ -77,6 +80,7 @@ __device__ __forceinline__ void chunk_bits(int chunk, int N, const int32_t *refs
   if ((threadIdx.x & 31) == 0) atomicAdd(&total, mine);
   __syncthreads();
   if (threadIdx.x == 0) counts[chunk] = total;
+  __syncthreads();
 }
 
 // ------------------------------------------------------------------- fork --
@@ -270,12 +274,10 @@ __device__ __forceinline__ int free_pages(const uint32_t *bits, const int32_t *c
   return q;
 }
 
-// A CTA per row, new and old: four warps share the new row's slots out and give the old one's
-// pages back, the fifth finds the new row's own pages.
-__global__ void __launch_bounds__(kRowNT + 32) sd_kv_rows_kernel(const ForkParams P) {
-  __shared__ int slots[kRowSlots];
-  pdl();
-  const int i = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+// Row i, new and old, by five warps (tid in them): four share the new row's slots out and give
+// the old one's pages back, the fifth finds the new row's own pages.
+__device__ __forceinline__ void fork_row(const ForkParams &P, int i, int tid, int *slots) {
+  const int lane = tid & 31;
   unsigned bad = 0u;
   const int kids = i < P.rows_in ? ld_int(P.kids + i) : 1;
   if (i < P.R) {
@@ -378,6 +380,34 @@ __global__ void __launch_bounds__(kRowNT + 32) sd_kv_rows_kernel(const ForkParam
   if (bad) set_status(P.status, bad);
 }
 
+__global__ void __launch_bounds__(kRowTeam) sd_kv_rows_kernel(const ForkParams P) {
+  __shared__ int slots[kRowSlots];
+  pdl();
+  fork_row(P, blockIdx.x, threadIdx.x, slots);
+}
+
+// Both steps in one launch, for few rows: by one cluster, with its barrier between them.
+__global__ void __launch_bounds__(kPgNT) sd_kv_fork_kernel(const ForkParams P) {
+  constexpr int kTeams = kPgNT / kRowTeam;
+  extern __shared__ int plan_smem[];
+  __shared__ int slots[kTeams][kRowSlots];
+  pdl();
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank(), cs = (int)cluster.num_blocks();
+  if (rank == 0) plan_rows(P, plan_smem);
+  else
+    for (int c = rank - 1; c < P.nchunk; c += cs - 1)
+      chunk_bits(c, P.N, P.refs, true, P.bits, P.counts);
+  cluster.sync();
+  const int team = threadIdx.x / kRowTeam;
+  if (team >= kTeams) return;
+  const int rows = max(P.R, P.rows_in);
+  for (int i = rank * kTeams + team; i < rows; i += cs * kTeams) {
+    fork_row(P, i, threadIdx.x % kRowTeam, slots[team]);
+    __syncwarp();
+  }
+}
+
 // ------------------------------------------------------------------- free --
 constexpr int kFreeNT = 256, kFreeU = 4;
 
@@ -445,11 +475,10 @@ __device__ __forceinline__ int used_before(const CompactParams &P, int p, uint32
 
 // A page in use at or above L is the source of move `used before it` - `used
 // before L`, a free one below L the destination of move `free before it`.
-__global__ void __launch_bounds__(kPgNT) sd_kv_moves_kernel(const CompactParams P) {
+__device__ __forceinline__ void chunk_moves(const CompactParams &P, int chunk) {
   __shared__ int warps[kPgNT / 32];
   __shared__ int before_s[kPgWords];
-  pdl();
-  const int chunk = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int all = 0, ahead = 0;
   for (int c = tid; c < P.nchunk; c += kPgNT) {
     const int n = ld_int(P.counts + c);
@@ -503,10 +532,8 @@ __global__ void __launch_bounds__(kPgNT) sd_kv_moves_kernel(const CompactParams 
   }
 }
 
-__global__ void __launch_bounds__(256) sd_kv_moved_kernel(const CompactParams P) {
-  pdl();
-  const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
-  const int L = ld_int(P.meta), low = ld_int(P.meta + 1);
+// What becomes of page i, and of entry i of the tables.
+__device__ __forceinline__ void page_moved(const CompactParams &P, int64_t i, int L, int low) {
   if (i < P.N) {
     const int p = (int)i;
     const uint32_t word = ld4(P.bits + (p >> 5));
@@ -534,22 +561,70 @@ __global__ void __launch_bounds__(256) sd_kv_moved_kernel(const CompactParams P)
   }
 }
 
+__global__ void __launch_bounds__(kPgNT) sd_kv_moves_kernel(const CompactParams P) {
+  pdl();
+  chunk_moves(P, blockIdx.x);
+}
+__global__ void __launch_bounds__(256) sd_kv_moved_kernel(const CompactParams P) {
+  pdl();
+  page_moved(P, blockIdx.x * (int64_t)blockDim.x + threadIdx.x, ld_int(P.meta), ld_int(P.meta + 1));
+}
+
+// The three steps in one launch, for small pools: by one cluster, with its barrier between them.
+__global__ void __launch_bounds__(kPgNT) sd_kv_compact_kernel(const CompactParams P) {
+  pdl();
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank(), cs = (int)cluster.num_blocks();
+  for (int c = rank; c < P.nchunk; c += cs) chunk_bits(c, P.N, P.refs, false, P.bits, P.counts);
+  cluster.sync();
+  for (int c = rank; c < P.nchunk; c += cs) chunk_moves(P, c);
+  cluster.sync();
+  const int L = ld_int(P.meta), low = ld_int(P.meta + 1);
+  const int64_t n = max((int64_t)P.N, P.n_table);
+  for (int64_t i = rank * kPgNT + threadIdx.x; i < n; i += cs * kPgNT) page_moved(P, i, L, low);
+}
+
 // Programmatic dependents of the stream's previous kernel.
 struct PageLaunch {
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  PageLaunch(int64_t grid, int block, int smem, cudaStream_t s) {
+  cudaLaunchAttribute attr[2];
+  PageLaunch(int64_t grid, int block, int smem, cudaStream_t s, int cluster = 1) {
     cfg.gridDim = dim3((unsigned)grid, 1, 1);
     cfg.blockDim = dim3(block, 1, 1);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = s;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
   }
   PageLaunch(const PageLaunch &) = delete;
 };
+
+// CTAs of the one cluster that does a small call, 0: several launches are faster.  A launch costs
+// the host 3 to 5 us, which is what small calls wait for; on the GPU alone, where the launches
+// overlap, the cluster is a little behind.  Measured, us, one launch / several, call (GPU
+// alone): fork of one prompt into 8 rows of 513 slots 65 (7.2) / 73 (6.7) with its copies,
+// compaction of 2000 pages 67 (8.1) / 77 (7.3) with its copies; compaction of 65536 pages (15.5 / 9.5)
+// and a fork of 512 rows (43 / 11) are the GPU's.
+constexpr int kMaxCluster = 8;
+static int fork_cluster(int rows, int M, int nchunk) {
+  constexpr int kTeams = kPgNT / kRowTeam;
+  if ((int64_t)rows * std::max(M, 1) > kForkCluster || rows > kMaxCluster * kTeams) return 0;
+  int cs = 2;
+  while (cs < kMaxCluster && (cs * kTeams < rows || cs - 1 < nchunk)) cs *= 2;
+  return cs;
+}
+static int compact_cluster(int nchunk, int64_t places) {
+  if (places > kCompactCluster) return 0;
+  int cs = 1;
+  while (cs < kMaxCluster && (cs < nchunk || (int64_t)cs * kPgNT < places)) cs *= 2;
+  return cs;
+}
 
 static size_t round16(size_t n) { return (n + 15) & ~(size_t)15; }
 
@@ -615,14 +690,19 @@ extern "C" sd_status_t sd_kv_fork(const sd_kv_fork_args *a, void *stream) {
   ws += sizeof(ForkRow) * (size_t)P.R;
   P.counts = reinterpret_cast<int32_t *>(ws);
   P.kids = reinterpret_cast<int32_t *>(ws + round16(4 * (size_t)P.nchunk));
+  const int rows = std::max(P.R, P.rows_in);
+  const int cs = fork_cluster(rows, P.M, P.nchunk);
+  if (cs > 0) {
+    PageLaunch one(cs, kPgNT, 8 * P.rows_in, (cudaStream_t)stream, cs);
+    return cudaLaunchKernelEx(&one.cfg, sd_kv_fork_kernel, P) == cudaSuccess ? SD_OK : SD_ERR_CUDA;
+  }
   static FuncAttrs attrs;
   attrs.apply((const void *)sd_kv_plan_kernel, 8 * SD_MAX_ROWS, false, "the fork's plan kernel");
   cudaStream_t s = (cudaStream_t)stream;
   PageLaunch plan(1 + P.nchunk, kPgNT, 8 * P.rows_in, s);
   cudaError_t e = cudaLaunchKernelEx(&plan.cfg, sd_kv_plan_kernel, P);
-  const int rows = std::max(P.R, P.rows_in);
   if (e == cudaSuccess && rows > 0) {
-    PageLaunch each(rows, kRowNT + 32, 0, s);
+    PageLaunch each(rows, kRowTeam, 0, s);
     e = cudaLaunchKernelEx(&each.cfg, sd_kv_rows_kernel, P);
   }
   return e == cudaSuccess ? SD_OK : SD_ERR_CUDA;
@@ -685,6 +765,11 @@ extern "C" sd_status_t sd_kv_compact(int32_t N, int32_t *refs, int64_t n_table, 
   P.counts = reinterpret_cast<int32_t *>(ws);
   P.meta = reinterpret_cast<int32_t *>(ws + round16(4 * (size_t)P.nchunk));
   cudaStream_t s = (cudaStream_t)stream;
+  if (const int cs = compact_cluster(P.nchunk, std::max<int64_t>(N, n_table))) {
+    PageLaunch one(cs, kPgNT, 0, s, cs);
+    return cudaLaunchKernelEx(&one.cfg, sd_kv_compact_kernel, P) == cudaSuccess ? SD_OK
+                                                                                 : SD_ERR_CUDA;
+  }
   PageLaunch chunks(P.nchunk, kPgNT, 0, s);
   cudaError_t e = cudaLaunchKernelEx(&chunks.cfg, sd_kv_live_kernel, P);
   if (e == cudaSuccess) e = cudaLaunchKernelEx(&chunks.cfg, sd_kv_moves_kernel, P);
