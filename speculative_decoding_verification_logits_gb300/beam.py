@@ -10,6 +10,7 @@ Like the rest of the package this module only checks and marshals arguments.
 from __future__ import annotations
 
 import ctypes
+import math
 from typing import NamedTuple
 
 import torch
@@ -115,17 +116,21 @@ def beam_select(logits, scores, k: int, *, temperature: float = 1.0, finished=No
 
 
 def _state(x, name, B, W, dev):
-    """Checks a state [B][W][...] whose rows are contiguous; the bytes of a row."""
+    """Checks a state [B][W][...] whose rows are contiguous; its strides of a sequence and of a
+    row, and the bytes of a row."""
+    shape, strides, size = x.shape, x.stride(), x.element_size()
     if not x.is_cuda or x.device != dev:
         raise ValueError(f"{name} must be a CUDA tensor on {dev}")
-    if x.dim() < 2 or x.shape[0] != B or x.shape[1] != W:
-        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected ({B}, {W}, ...)")
+    if len(shape) < 2 or shape[0] != B or shape[1] != W:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected ({B}, {W}, ...)")
+    if x.is_contiguous():
+        return strides[0] * size, strides[1] * size, math.prod(shape[2:]) * size
     want = 1
-    for n, s in zip(reversed(x.shape[2:]), reversed(x.stride()[2:])):
+    for n, s in zip(reversed(shape[2:]), reversed(strides[2:])):
         if n > 1 and s != want:
             raise ValueError(f"{name} must have contiguous rows")
         want *= n
-    return want * x.element_size()
+    return strides[0] * size, strides[1] * size, want * size
 
 
 @_on_device
@@ -146,26 +151,32 @@ def beam_reorder(states, parents, *, out=None, status=None):
     if parents.dim() != 2 or xs[0].dim() < 2:
         raise ValueError("parents must be [B][k], states [B][W][...]")
     (B, k), W = parents.shape, xs[0].shape[1]
-    rows = [_state(x, "states", B, W, dev) for x in xs]
-    if ys is None:
-        if k > W:
-            raise ValueError("parents has more slots than there are rows: give out")
-        ys = tuple(torch.empty((B, k, *x.shape[2:]), dtype=x.dtype, device=dev) for x in xs)
-    else:
-        for x, y in zip(xs, ys):
-            _state(y, "out", B, k, dev)
+    if ys is None and k > W:
+        raise ValueError("parents has more slots than there are rows: give out")
+    a = (StateArgs * len(xs))()
+    made = []
+    for i, x in enumerate(xs):
+        sb, sw, row = _state(x, "states", B, W, dev)
+        if ys is None:
+            y = torch.empty((B, k, *x.shape[2:]), dtype=x.dtype, device=dev)
+            made.append(y)
+            a[i] = (x.data_ptr(), sb, sw, y.data_ptr(), k * row, row, row)
+            continue
+        y = ys[i]
+        if y is not x or k != W:
             if y.dtype != x.dtype or y.shape[2:] != x.shape[2:]:
                 raise ValueError("out must have the rows and types of the states")
-            if y.shape[0] > 1 and y.stride(0) == 0 or y.shape[1] > 1 and y.stride(1) == 0:
-                raise ValueError("out must not be expanded")
-        if len(ys) > 1 or _meet(xs[0], ys[0]):
+            to = _state(y, "out", B, k, dev)
+        else:
+            to = sb, sw, row
+        if B > 1 and to[0] == 0 and row or k > 1 and to[1] == 0 and row:
+            raise ValueError("out must not be expanded")
+        a[i] = (x.data_ptr(), sb, sw, y.data_ptr(), to[0], to[1], row)
+    if ys is not None:
+        if len(ys) > 1 or ys[0] is not xs[0]:
             _apart_or_same(xs, ys)
         if any(_meet(y, parents) for y in ys):
             raise ValueError("out overlaps parents")
-    a = (StateArgs * len(xs))(*((x.data_ptr(), x.stride(0) * x.element_size(),
-                                 x.stride(1) * x.element_size(), y.data_ptr(),
-                                 y.stride(0) * y.element_size(), y.stride(1) * y.element_size(), r)
-                                for x, y, r in zip(xs, ys, rows)))
     st = None if status is None else _i32(status, "status", (1,), dev)
     rc = _lib().sd_beam_reorder(B, W, k, parents.data_ptr(), len(xs), ctypes.addressof(a), st,
                                 _stream_of(dev))
@@ -175,7 +186,7 @@ def beam_reorder(states, parents, *, out=None, status=None):
         for y in ys:
             _written(y)
         return out
-    return ys[0] if single else list(ys)
+    return made[0] if single else made
 
 
 def _apart_or_same(xs, ys):

@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 from typing import NamedTuple
 
 import torch
@@ -185,7 +186,7 @@ def _fork(a, refs, status, dev, sizes):
     if rc:
         _check(rc, "sd_kv_fork")
     _written(refs)
-    return buf.split_with_sizes(sizes)
+    return buf.unsafe_split_with_sizes(sizes)   # arrays of their own, not views of one another
 
 
 @_on_device
@@ -305,7 +306,7 @@ def kv_compact(refs, block_table=None, *, status=None) -> KVCompact:
     _written(refs)
     if n_table:
         _written(block_table)
-    _, src, dst, count, live, new = buf.split_with_sizes(sizes)
+    _, src, dst, count, live, new = buf.unsafe_split_with_sizes(sizes)
     return KVCompact(src, dst, count, new, live)
 
 
@@ -329,29 +330,31 @@ def kv_copy(caches, src, dst, *, count=None, fill=None, heads_first: bool = Fals
     destination."""
     one = isinstance(caches, torch.Tensor)
     if one:
-        if caches.dim() < 3:
-            raise ValueError("caches must be [layers][N][...]")
-        base, lead = caches, 1
-        layers, tensors = caches.shape[0], (caches,)
+        base, lead, tensors = caches, 1, (caches,)
     else:
         tensors = tuple(caches)
         if not tensors:
             return
         if len(tensors) > SD_MAX_CACHES:
             raise ValueError(f"at most {SD_MAX_CACHES} caches")
-        base, lead, layers = tensors[0], 0, 1
-        if base.dim() < 2:
-            raise ValueError("each cache must be [N][...]")
+        base, lead = tensors[0], 0
     dev, shape, strides, size = base.device, base.shape, base.stride(), base.element_size()
+    if len(shape) < lead + 2:
+        raise ValueError("caches must be [layers][N][...], or each of a sequence [N][...]")
+    layers = shape[0] if one else 1
     for t in tensors:
         if not t.is_cuda:
             raise ValueError("caches must be CUDA tensors")
-        if t.device != dev or t.shape != shape or t.stride() != strides or t.dtype != base.dtype:
+        if t is not base and (t.device != dev or t.shape != shape or t.stride() != strides
+                              or t.dtype != base.dtype):
             raise ValueError("caches must be alike in shape, type, strides and device")
-    page = _page_shape(shape, strides, size, lead + 1, "caches")
-    for d in range(lead + 1):
-        if shape[d] > 1 and strides[d] == 0:
-            raise ValueError("caches must not be expanded")
+    if base.is_contiguous():
+        page = size * math.prod(shape[lead + 1:])
+    else:
+        page = _page_shape(shape, strides, size, lead + 1, "caches")
+        for d in range(lead + 1):
+            if shape[d] > 1 and strides[d] == 0:
+                raise ValueError("caches must not be expanded")
     at = lead + 2 if heads_first else lead + 1
     if fill is not None and len(shape) <= at:
         raise ValueError("fill needs pages of [page_size][...], or [heads][page_size][...]")
@@ -363,14 +366,15 @@ def kv_copy(caches, src, dst, *, count=None, fill=None, heads_first: bool = Fals
         return
     a = CopyArgs(len(tensors), layers, shape[lead], parts, entries, page // (parts * entries),
                  strides[0] * size if one else 0, strides[lead] * size)
-    a.caches = ctypes.cast((ctypes.c_void_p * len(tensors))(*(t.data_ptr() for t in tensors)), _P)
-    _need(src, "src", _I32, None, dev)
-    if src.dim() != 1:
+    pointers = (_P * len(tensors))(*(t.data_ptr() for t in tensors))
+    a.caches = ctypes.addressof(pointers)
+    pairs = src.shape
+    if len(pairs) != 1:
         raise ValueError("src must be [pairs]")
-    a.pairs = src.shape[0]
-    a.src, a.dst = src.data_ptr(), _i32(dst, "dst", src.shape, dev)
+    a.pairs = pairs[0]
+    a.src, a.dst = _i32(src, "src", pairs, dev), _i32(dst, "dst", pairs, dev)
     if fill is not None:
-        a.fill = _i32(fill, "fill", src.shape, dev)
+        a.fill = _i32(fill, "fill", pairs, dev)
     if count is not None:
         a.count = _i32(count, "count", (1,), dev)
     if status is not None:
