@@ -213,6 +213,16 @@ __device__ __forceinline__ ff ff_log(ff z) {
                       sum.lo + fmaf((float)e, -2.9088971e-5f, 2.f * fmaf(r, p, rest)));
 }
 
+// How far d below the best of a sequence, in bins: of d + 1 the exponent and the four leading bits
+// (steps of 1/16 at first, of 1/2 from 7 on, 2^16 in all; the last bin holds the rest).
+__device__ __forceinline__ int below_bin(float d) {
+  return min(__float_as_int(d + 1.f) - 0x3f800000 >> 19, kEndBins - 1);
+}
+// What everything in the bins up to this one reaches.
+__device__ __forceinline__ float bin_edge(float top, int bin) {
+  return bin < kEndBins - 1 ? top - (__int_as_float((bin + 1 << 19) + 0x3f800000) - 1.f) : kLowest;
+}
+
 // What a sequence's end holds on chip.
 struct SelectEnd {
   // a beam: 0 offers nothing, 1 live, 2 finished; its score less the log of its sum
@@ -237,8 +247,38 @@ struct SelectEnd {
   int best;
   int warp_n[kEndNT / 32];
   float bound;
+  float margin;                       // the largest size of what entered an o
   int n_list, n_cand, n_best;
+  unsigned long long kth;             // of kth_largest: the bits so far
+  int rank, count;
+
+  // by the first warp: the bin that holds the k-th of those counted, kEndBins where they are fewer
+  __device__ __forceinline__ int bin_of_rank(int k) const {
+    constexpr int J = kEndBins / 32;
+    const int lane = threadIdx.x & 31;
+    int n[J], upto = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) upto += n[j] = hist[lane * J + j];
+    const int here = upto;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      upto += lane >= o ? y : 0;
+    }
+    const unsigned enough = __ballot_sync(0xffffffffu, upto >= k);
+    int bin = kEndBins, at = upto - here;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      at += n[j];
+      bin = bin == kEndBins && at >= k ? lane * J + j : bin;
+    }
+    return enough ? __shfl_sync(0xffffffffu, bin, __ffs(enough) - 1) : kEndBins;
+  }
 };
+__device__ __forceinline__ float loosened(float bound, float size) {
+  return bound > kLowest ? fmaxf(bound - (fabsf(bound) + size) * 3.814697265625e-6f, kLowest)
+                         : bound;
+}
 constexpr int kTokenBits = 18;
 static_assert(SD_MAX_V <= 1 << kTokenBits, "a token and a beam fit an int");
 
@@ -265,6 +305,58 @@ struct EndView {
   }
   static __device__ __forceinline__ float approx(const float4 &f, float x) {
     return x > neg_inf() ? fmaxf(fmaf(x - f.x, f.y, f.z), kLowest) : neg_inf();
+  }
+  // calls f(beam, first token, logits) for the vectors of the listed groups
+  template <typename F>
+  __device__ __forceinline__ void each_listed(F f) const {
+    constexpr int kAhead = 2;
+    const int items = S.n_list * kSize;
+#pragma unroll 1
+    for (int i0 = threadIdx.x; i0 < items; i0 += kAhead * kEndNT) {
+      uint4 v[kAhead];
+      int at[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = i0 + u * kEndNT;
+        at[u] = -1;
+        if (i >= items) continue;
+        const int g = S.list[i / kSize];
+        const ElemRow<E> r = row(g >> 16);
+        const int q = vector(r, g & 0xffff, i % kSize);
+        if (q < 0) continue;
+        v[u] = r.load(q);
+        at[u] = (g >> 16) << kTokenBits | r.first(q);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (at[u] < 0) continue;
+        float x[VE];
+        Elt<E>::unpack(v[u], x);
+        f(at[u] >> kTokenBits, at[u] & ((1 << kTokenBits) - 1), x);
+      }
+    }
+  }
+  // what reaches the bound in the listed groups, and the finished beams, as candidates;
+  // whether there was room for them.  Ends with a barrier.
+  __device__ __forceinline__ bool offer_listed(float bound) const {
+    each_listed([&](int w, int v, const float(&x)[VE]) {
+      const float4 f = S.image[w];
+      unsigned pass = 0u;
+#pragma unroll
+      for (int e = 0; e < VE; ++e) pass |= (approx(f, x[e]) >= bound ? 1u : 0u) << e;
+      // once there is no room left nothing more is offered
+      while (pass && *(volatile int *)&S.n_cand <= kSelList) {
+        const int j = __ffs(pass) - 1;
+        pass &= pass - 1;
+        float y = x[0];
+#pragma unroll
+        for (int e = 1; e < VE; ++e) y = j == e ? x[e] : y;
+        offer(w, v + j, y);
+      }
+    });
+    if (threadIdx.x < P.W && S.kind[threadIdx.x] == 2) offer(threadIdx.x, P.eos, 0.f);
+    __syncthreads();
+    return S.n_cand <= kSelList;
   }
   // a candidate; logits of a finished beam are not looked at
   __device__ __noinline__ void offer(int w, int v, float x) const {
@@ -319,11 +411,122 @@ __device__ __forceinline__ int block_count(SelectEnd &S, int n) {
   return n;
 }
 
+// One more in a bin: lanes that all name the same one add together.
+__device__ __forceinline__ void count_in(int *hist, int bin) {
+  const unsigned here = __activemask();
+  const int first = __ffs(here) - 1;
+  if (__all_sync(here, bin == __shfl_sync(here, bin, first))) {
+    if ((threadIdx.x & 31) == first) atomicAdd(&hist[bin], __popc(here));
+  } else {
+    atomicAdd(&hist[bin], 1);
+  }
+}
+
+// The key of the k-th largest of those that each(f) calls f(key) for, 0 where they are
+// fewer: eight bits at a time.
+template <typename F>
+__device__ __forceinline__ unsigned long long kth_largest(SelectEnd &S, int k, int bits, F each) {
+  const int tid = threadIdx.x;
+  if (tid == 0) {
+    S.kth = 0ull;
+    S.rank = k;
+  }
+#pragma unroll 1
+  for (int shift = bits - 8; shift >= 0; shift -= 8) {
+    if (tid < kEndBins) S.hist[tid] = 0;
+    __syncthreads();
+    const unsigned long long known = S.kth;
+    const int rank = S.rank;
+    each([&](unsigned long long key) {
+      // the largest digit in the first bin
+      if (((key ^ known) >> shift) >> 8 == 0ull) count_in(S.hist, 255 - (int)(key >> shift & 255u));
+    });
+    __syncthreads();
+    if (tid < 32) {
+      const int bin = S.bin_of_rank(rank);
+      int above = 0;
+      for (int i = tid; i < min(bin, kEndBins); i += 32) above += S.hist[i];
+      __syncwarp();
+      above = __reduce_add_sync(0xffffffffu, above);
+      if (tid == 0) {
+        S.rank = bin < kEndBins ? rank - above : 0;
+        S.kth = known | (unsigned long long)(255 - min(bin, 255)) << shift;
+      }
+    }
+    __syncthreads();
+    if (S.rank == 0) return 0ull;
+  }
+  return S.kth;
+}
+static_assert(kEndBins == 256, "a digit of eight bits per bin");
+
+// Where more groups or logits reach the bound than there is room for: the groups from the best
+// down that there is room for, then a bound from their logits instead of their largest.
+// Whether that was enough: not where the k-th lies below those groups (or more than 2^16 below
+// the best), nor where more logits than there is room for lie in its bin.
+template <typename E, int U>
+__device__ __noinline__ bool narrow(const EndView<E, U> &X, float top, float margin) {
+  constexpr int NT = kEndNT, VE = Elt<E>::kPerVec;
+  SelectEnd &S = X.S;
+  const int tid = threadIdx.x, ng = X.P.nc * kSelSets, W = X.P.W;
+  const auto each_group = [&](auto f) {
+#pragma unroll 1
+    for (int i = tid; i < W * ng; i += NT) {
+      const int w = i / ng;
+      const float4 g = S.image[w];
+      if (g.w >= 0.f) f(w, i - w * ng, X.approx(g, ld_float(X.groups(0) + i)));
+    }
+  };
+  const auto count = [&](float a) {
+    const int bin = below_bin(top - a);
+    if (bin < kEndBins - 1) atomicAdd(&S.hist[bin], 1);
+  };
+  const auto clear = [&] {
+    __syncthreads();
+    if (tid < kEndBins) S.hist[tid] = 0;
+    if (tid == 0) S.n_cand = 0;
+    __syncthreads();
+  };
+  // in every thread
+  const auto bin_of_rank = [&](int k) {
+    __syncthreads();
+    const int bin = tid < 32 ? S.bin_of_rank(k) : 0;
+    if (tid == 0) S.count = bin;
+    __syncthreads();
+    return S.count;
+  };
+  clear();
+  if (tid == 0) S.n_list = 0;
+  each_group([&](int, int, float a) { count(a); });
+  const int past = min(bin_of_rank(kSelList + 1), kEndBins - 1);   // the first bin without room
+  if (past == 0) return false;
+  const float room = loosened(bin_edge(top, past - 1), margin);
+  each_group([&](int w, int g, float a) {
+    if (!(a >= room)) return;
+    const int at = atomicAdd(&S.n_list, 1);
+    if (at < kSelList) S.list[at] = w << 16 | g;
+  });
+  clear();
+  if (S.n_list > kSelList) return false;
+  X.each_listed([&](int w, int, const float(&x)[VE]) {
+    const float4 f = S.image[w];
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      const float a = X.approx(f, x[e]);
+      if (a >= room) count(a);
+    }
+  });
+  const int bin = bin_of_rank(X.P.k);
+  if (bin >= kEndBins - 1) return false;
+  const float bound = loosened(bin_edge(top, bin), margin);
+  return bound >= room && X.offer_listed(bound);
+}
+
 // The beams one by one, whatever their logits: the k best of one by value, then
 // by index, join the k best so far.
-//  - v*, the k-th largest of its groups' largest, bit by bit;
+//  - v*, the k-th largest of its groups' largest;
 //  - the logits above v* lie in fewer than k groups.  If they are more than k,
-//    the key (value, index) of the k-th is found bit by bit;
+//    the key (value, index) of the k-th bounds them;
 //  - if they are fewer, logits equal to v* fill up, lowest index first, from the
 //    row's beginning until there are enough.
 template <typename E, int U>
@@ -358,13 +561,9 @@ __device__ __noinline__ void each_beam(const EndView<E, U> &X) {
     const float *gm = X.groups(w);
     const int ng = P.nc * kSelSets;
     const unsigned low = (unsigned)ford(kLowest) ^ 0x80000000u;
-    unsigned r = 0u;
-    for (int bit = 31; bit >= 0; --bit) {
-      const unsigned t = r | (1u << bit);
-      int n = 0;
-      for (int i = tid; i < ng; i += NT) n += ((unsigned)ford(ld_float(gm + i)) ^ 0x80000000u) >= t;
-      if (block_count(S, n) >= k) r = t;
-    }
+    const unsigned r = (unsigned)kth_largest(S, k, 32, [&](auto f) {
+      for (int i = tid; i < ng; i += NT) f((unsigned)ford(ld_float(gm + i)) ^ 0x80000000u);
+    });
     const float least = fdeord((int)(max(r, low) ^ 0x80000000u));
     for (int i = tid; i < ng; i += NT)
       if (ld_float(gm + i) > least) {   // fewer than k
@@ -388,13 +587,10 @@ __device__ __noinline__ void each_beam(const EndView<E, U> &X) {
     above(0ull, [&](float, int) { ++more; });
     more = block_count(S, more);
     unsigned long long from = 0ull;
-    if (more > k) {
-      for (int bit = 63; bit >= 0; --bit) {
-        int n = 0;
-        above(from | (1ull << bit), [&](float, int) { ++n; });
-        if (block_count(S, n) >= k) from |= 1ull << bit;
-      }
-    }
+    if (more > k)
+      from = kth_largest(S, k, 64, [&](auto f) {
+        above(0ull, [&](float x, int v) { f(top_key(x, v)); });
+      });
     above(from, [&](float x, int v) { X.offer(w, v, x); });
     if (more < k) {
       int need = k - more;
@@ -560,47 +756,21 @@ __global__ void __launch_bounds__(kEndNT, 1) sd_beam_end_kernel(const SelectPara
   const int most = __reduce_max_sync(0xffffffffu, ford(best));
   if (lane == 0) atomicMax(&S.best, most);
   __syncthreads();
-  // what k of them reach: of d + 1, d how far one lies below the best of all, the exponent and the
-  // four leading bits are counted (steps of 1/16 at first, of 1/2 from 7 on); no bound is known
-  // where the k-th lies more than 2^16 below
+  // what k of them reach; no bound is known where the k-th lies more than 2^16 below the best
   const float top = fdeord(S.best);
-  if (best > neg_inf())
-    atomicAdd(&S.hist[min(__float_as_int(top - best + 1.f) - 0x3f800000 >> 19, kEndBins - 1)], 1);
+  if (best > neg_inf()) atomicAdd(&S.hist[below_bin(top - best)], 1);
   __syncthreads();
   if (warp == 0) {
-    constexpr int J = kEndBins / 32;
-    int n[J], upto = 0;
-#pragma unroll
-    for (int j = 0; j < J; ++j) upto += n[j] = S.hist[lane * J + j];
-    const int here = upto;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, upto, o);
-      upto += lane >= o ? y : 0;
-    }
-    const unsigned enough = __ballot_sync(0xffffffffu, upto >= k);
+    const int bin = S.bin_of_rank(k);
     size = rmax_f(size);
-    float bound = kLowest;
-    if (enough) {
-      if (lane == __ffs(enough) - 1) {
-        int j = 0, at = upto - here;
-#pragma unroll
-        for (; j < J - 1; ++j) {
-          at += n[j];
-          if (at >= k) break;
-        }
-        const int bin = lane * J + j;
-        if (bin < kEndBins - 1)
-          bound = top - (__int_as_float((bin + 1 << 19) + 0x3f800000) - 1.f);
-      }
-      bound = __shfl_sync(0xffffffffu, bound, __ffs(enough) - 1);
-    }
+    float bound = bin < kEndBins ? bin_edge(top, bin) : kLowest;
     // the image is off by less than 2^-19 of its own size and of what entered o (quotients of two
     // steps, a logarithm of 2^-22 near one): the groups that reach the bound and the logits
     // held against it by at most twice that
-    if (bound > kLowest)
-      bound = fmaxf(bound - (fabsf(bound) + size) * 3.814697265625e-6f, kLowest);
-    if (lane == 0) S.bound = bound;
+    if (lane == 0) {
+      S.margin = size;
+      S.bound = loosened(bound, size);
+    }
   } else if (mine) {   // meanwhile the beams' numbers in 64 bits
     const ff log_z = ff_log(z);
     S.base[lane] = ((double)s - (double)log_z.hi) - (double)log_z.lo;
@@ -616,7 +786,7 @@ __global__ void __launch_bounds__(kEndNT, 1) sd_beam_end_kernel(const SelectPara
                           __uint_as_float(v.w)};
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (X.approx(f, x[e]) >= bound) {
+        if (X.approx(f, x[e]) >= bound && *(volatile int *)&S.n_list <= kSelList) {
           const int at = atomicAdd(&S.n_list, 1);
           if (at < kSelList) S.list[at] = w << 16 | ((i - w * per) * 4 + e);
         }
@@ -629,49 +799,8 @@ __global__ void __launch_bounds__(kEndNT, 1) sd_beam_end_kernel(const SelectPara
   }
   __syncthreads();
   bool fits = S.n_list <= kSelList;
-  if (fits) {
-    const int items = S.n_list * X.kSize;
-    constexpr int kAhead = 2;
-#pragma unroll 1
-    for (int i0 = tid; i0 < items; i0 += kAhead * NT) {
-      uint4 v[kAhead];
-      int at[kAhead];
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int i = i0 + u * NT;
-        at[u] = -1;
-        if (i >= items) continue;
-        const int g = S.list[i / X.kSize];
-        const ElemRow<E> row = X.row(g >> 16);
-        const int q = X.vector(row, g & 0xffff, i % X.kSize);
-        if (q < 0) continue;
-        v[u] = row.load(q);
-        at[u] = (g >> 16) << kTokenBits | row.first(q);
-      }
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        if (at[u] < 0) continue;
-        const int w = at[u] >> kTokenBits;
-        const float4 f = S.image[w];
-        float x[VE];
-        Elt<E>::unpack(v[u], x);
-        unsigned pass = 0u;
-#pragma unroll
-        for (int e = 0; e < VE; ++e) pass |= (X.approx(f, x[e]) >= bound ? 1u : 0u) << e;
-        while (pass) {
-          const int j = __ffs(pass) - 1;
-          pass &= pass - 1;
-          float y = x[0];
-#pragma unroll
-          for (int e = 1; e < VE; ++e) y = j == e ? x[e] : y;
-          X.offer(w, (at[u] & ((1 << kTokenBits) - 1)) + j, y);
-        }
-      }
-    }
-    if (tid < W && S.kind[tid] == 2) X.offer(tid, P.eos, 0.f);
-    __syncthreads();
-    fits = S.n_cand <= kSelList;
-  }
+  if (fits) fits = X.offer_listed(bound);
+  if (!fits) fits = narrow<E, U>(X, top, S.margin);
   if (fits) rank_candidates(S, k);
   else each_beam<E, U>(X);
   for (int i = tid; i < k; i += NT) {
