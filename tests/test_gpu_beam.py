@@ -308,6 +308,25 @@ def test_reorder_several_states_strides_and_slots(dev):
     assert torch.equal(out.cpu(), want)
 
 
+@pytest.mark.parametrize("W", [2, 8, 9, 13, 32])
+@pytest.mark.parametrize("row", [1, 15, 16, 17, 4096, 4097, 9001, 20000])
+def test_reorder_rows_at_every_place_of_the_grid(dev, W, row):
+    # rows and their neighbours: bytes around the rows stay as they are
+    g = _g(row + W)
+    B, gap = 2, 16 + row % 7
+    for place in (0, 5):
+        buf = torch.randint(0, 256, (place + B * W * (row + gap),), generator=g, dtype=torch.uint8)
+        views = lambda t: t[place:].view(B, W, row + gap)[:, :, :row]
+        p = torch.randint(-1, W, (B, W), generator=g, dtype=torch.int32)
+        want, _ = ref.reorder(views(buf), p)
+        there = buf.to(dev)
+        assert torch.equal(sd.beam_reorder(views(there), p.to(dev)).cpu(), want)
+        sd.beam_reorder(views(there), p.to(dev), out=views(there))
+        left = buf.clone()
+        views(left).copy_(want)
+        assert torch.equal(there.cpu(), left)
+
+
 def test_reorder_bad_parents(dev):
     x = _state((2, 3, 5), torch.int32, 5)
     p = torch.tensor([[3, 0, -2], [1, 1, 2]], dtype=torch.int32)
