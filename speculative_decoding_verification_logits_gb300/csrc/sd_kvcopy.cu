@@ -71,6 +71,12 @@ __device__ __forceinline__ void copy_piece(const uint8_t *from, uint8_t *to, int
 #pragma unroll
   for (int u = 0; u < kCpU; ++u)
     if (lane + u * 32 < n) *reinterpret_cast<T *>(to + u * 32 * sizeof(T)) = v[u];
+  // entries need not end with a vector
+  const int rest = bytes - n * (int)sizeof(T);
+  if (lane < rest) {
+    const int at = n * (int)sizeof(T) + lane - lane * (int)sizeof(T);
+    to[at] = (uint8_t)ld1(from + at);
+  }
 }
 
 __global__ void __launch_bounds__(kCpNT, kCpCtas)
@@ -148,9 +154,7 @@ extern "C" sd_status_t sd_kv_copy(const sd_kv_copy_args *a, void *stream) {
   P.fill = a->fill;
   P.count = a->count;
   P.status = a->status;
-  // whole entries are copied, so that an entry's bytes bound the vectors' width; without
-  // fill whole parts
-  uint64_t bits = 16 | (uint64_t)(P.fill ? P.entry_bytes : P.part_bytes) | (uint64_t)P.part_bytes;
+  uint64_t bits = 16 | (uint64_t)P.part_bytes;   // what bounds the vectors' width
   if (P.layers > 1) bits |= (uint64_t)P.layer_stride;
   if (P.N > 1) bits |= (uint64_t)P.page_stride;
   for (int i = 0; i < P.n_caches; ++i) {

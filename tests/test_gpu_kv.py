@@ -335,6 +335,31 @@ def test_copy(dev, dtype, dim, heads_first):
             assert torch.equal(torch.stack(parts).cpu(), want)
 
 
+@pytest.mark.parametrize("page,entry", [(16, 1), (16, 33), (7, 16), (3, 5), (16, 66), (64, 1040)])
+def test_copy_of_entries_that_end_inside_a_vector(dev, page, entry):
+    g = _g(page * entry)
+    c = torch.randint(0, 256, (2, 30, page, entry), generator=g, dtype=torch.uint8)
+    ids = torch.randperm(30, generator=g).to(I32)
+    src, dst = ids[:15], ids[15:]
+    fill = torch.arange(15, dtype=I32) % (page + 1)
+    cd = c.to(dev)
+    sd.kv_copy(cd, src.to(dev), dst.to(dev), fill=fill.to(dev))
+    assert torch.equal(cd.cpu(), ref.copy(c, src, dst, fill=fill)[0])
+
+
+def test_extend_many_rows(dev):
+    g = _g(77)
+    t, n, refs = _tables(75, 4, 11, 4, g, free=3000, reserve=1)
+    refs[:] = torch.bincount(t[t >= 0].long(), minlength=len(refs)).to(I32)
+    td, rd = t.to(dev), refs.to(dev)
+    st = torch.zeros(1, dtype=I32, device=dev)
+    m = sd.kv_extend(td, n.to(dev), rd, 4, 6, status=st)
+    want = ref.fork(t, n, None, refs, 4, append=6)
+    for a, b in zip((td, *m, rd), (want[0], *want[2:7])):
+        assert torch.equal(a.cpu(), b)
+    assert int(st) == want[-1]
+
+
 def test_copy_strides_bad_ids_and_large_pages(dev):
     g = _g(14)
     buf = torch.randint(0, 99, (30, 5, 16, 24), generator=g, dtype=torch.int16).to(dev)
