@@ -16,7 +16,7 @@ from typing import NamedTuple
 import torch
 
 from . import _P, _check, _need
-from .kv import _i32, _meet, _on_device, _scratch
+from .kv import _all_apart, _i32, _on_device, _rows_meet, _scratch
 from .logits import _lib, _rows, _same, _stream_of, _written
 
 SD_MAX_BEAMS, SD_MAX_STATES = 32, 16
@@ -102,9 +102,9 @@ def beam_select(logits, scores, k: int, *, temperature: float = 1.0, finished=No
         a.parents = _i32(out.parents, "out.parents", (B, k), dev)
         a.tokens = _i32(out.tokens, "out.tokens", (B, k), dev)
         given = out
-        for t in out:
-            if any(_meet(t, x) for x in (logits, scores, finished, norm) if x is not None):
-                raise ValueError("out overlaps the input")
+        _all_apart(out, scores, finished, norm, status)
+        if any(_rows_meet(logits, t.view(1, 1, B * k), 2) for t in out):
+            raise ValueError("out overlaps the input")
     a.out_scores, a.ended = out.scores.data_ptr(), out.finished.data_ptr()
     a.workspace, a.workspace_bytes = ws.data_ptr(), 4 * n
     rc = _lib().sd_beam_select(a, _stream_of(dev))
@@ -175,7 +175,7 @@ def beam_reorder(states, parents, *, out=None, status=None):
     if ys is not None:
         if len(ys) > 1 or ys[0] is not xs[0]:
             _apart_or_same(xs, ys)
-        if any(_meet(y, parents) for y in ys):
+        if any(_rows_meet(y, parents[None], 2) for y in ys):
             raise ValueError("out overlaps parents")
     st = None if status is None else _i32(status, "status", (1,), dev)
     rc = _lib().sd_beam_reorder(B, W, k, parents.data_ptr(), len(xs), ctypes.addressof(a), st,
@@ -195,7 +195,7 @@ def _apart_or_same(xs, ys):
         for j, x in enumerate(xs):
             if i == j and x.shape == y.shape and _same(x, y):
                 continue
-            if _meet(x, y):
+            if _rows_meet(x, y, 2):
                 raise ValueError("out overlaps a state without being the same tensor")
-        if any(_meet(y, z) for z in ys[:i]):
+        if any(_rows_meet(y, z, 2) for z in ys[:i]):
             raise ValueError("outputs overlap")

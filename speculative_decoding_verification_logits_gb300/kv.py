@@ -139,6 +139,31 @@ def _meet(a, b):
     return a0 < b1 and b0 < a1
 
 
+def _rows_meet(a, b, lead):
+    """Whether two tensors whose rows (all dimensions from `lead` on) are contiguous share a byte:
+    rows of one may lie between those of the other."""
+    if not _meet(a, b):
+        return False
+
+    def starts(t):   # the rows' addresses, and their bytes
+        at = torch.tensor(t.data_ptr(), device="cpu")
+        for n, s in zip(t.shape[:lead], t.stride()[:lead]):
+            at = at[..., None] + torch.arange(n, device="cpu") * (s * t.element_size())
+        return at.flatten().sort().values, math.prod(t.shape[lead:]) * t.element_size()
+
+    (x, nx), (y, ny) = starts(a), starts(b)
+    return bool((torch.searchsorted(y, x + nx) > torch.searchsorted(y, x - ny, right=True)).any())
+
+
+def _all_apart(outs, *inputs):
+    """Refuses outputs that share memory with an input or with one another (contiguous ones)."""
+    for i, t in enumerate(outs):
+        if any(_meet(t, x) for x in inputs if x is not None):
+            raise ValueError("out overlaps the input")
+        if any(_meet(t, x) for x in outs[:i]):
+            raise ValueError("outputs overlap")
+
+
 def _pool(refs, device):
     shape = refs.shape
     if len(shape) != 1 or shape[0] < 1:
@@ -216,15 +241,12 @@ def kv_fork(block_table, kv_len, parents, refs, page_size: int, *, append: int =
     if out is None:
         _, t, n, src, dst, fill, count = _fork(a, refs, status, dev, (R * M, R, R, R, R, 1))
         return KVFork(t.view(R, M), n, src, dst, fill, count)
-    for x in (out.block_table, out.kv_len):
-        _need(x, "out", _I32, None, dev)
-        if any(_meet(x, y) for y in (block_table, kv_len, parents, refs)):
-            raise ValueError("out overlaps the input")
     a.table_out = _i32(out.block_table, "out.block_table", (R, M), dev)
     a.len_out = _i32(out.kv_len, "out.kv_len", (R,), dev)
     a.src, a.dst, a.fill = (_i32(getattr(out, n), "out." + n, (R,), dev)
                             for n in ("src", "dst", "fill"))
     a.count = _i32(out.count, "out.count", (1,), dev)
+    _all_apart(out, block_table, kv_len, parents, refs, status)
     _fork(a, refs, status, dev, ())
     for t in out:
         _written(t)

@@ -134,6 +134,20 @@ def test_binding_refuses_host_tensors():
             call()
 
 
+def test_which_memory_rows_share():
+    from speculative_decoding_verification_logits_gb300.kv import _rows_meet as meet
+    buf = torch.zeros((3, 4, 20), dtype=torch.uint8)
+    assert not meet(buf[..., :10], buf[..., 10:], 2) and meet(buf[..., :11], buf[..., 10:], 2)
+    assert not meet(buf[:, ::2], buf[:, 1::2], 2) and meet(buf[:, ::2], buf[:, 2:], 2)
+    assert meet(buf, buf, 2) and not meet(buf[:0], buf, 2)
+    assert not meet(buf[:, :3, :5], buf[:, 3:, :9], 2)
+    wide = buf.view(torch.int32)          # rows of different types and lengths
+    assert meet(wide[:, :2, 4:], buf[:, 1:, 16:18], 2) and not meet(wide[:, :, 4:], buf[..., :16], 2)
+    flat = torch.zeros(100, dtype=torch.int32)
+    assert not meet(flat[:6].view(1, 2, 3), flat[6:9].view(1, 1, 3), 2)
+    assert meet(flat[:6].view(1, 2, 3), flat[5:9].view(1, 2, 2), 2)
+
+
 # ------------------------------------------------------- the definitions --
 def test_reference_select_by_hand():
     x = torch.log(torch.tensor([[[0.5, 0.25, 0.25, 0.0], [0.1, 0.2, 0.3, 0.4]]], dtype=torch.float64))

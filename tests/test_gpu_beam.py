@@ -204,6 +204,9 @@ def test_select_into_given_outputs(dev):
     got = sd.beam_select(x, s, k, eos=3, out=out)
     assert got is out and all(torch.equal(a, b) for a, b in zip(got, want))
     assert [t._version for t in out] == [v + 1 for v in before]
+    for twice in (dict(tokens=out.parents), dict(parents=out.tokens)):
+        with pytest.raises(ValueError, match="overlap"):
+            sd.beam_select(x, s, k, out=out._replace(**twice))
     with pytest.raises(ValueError, match="overlaps"):
         sd.beam_select(x, s, W, out=sd.Beams(s, *(t[:, :W].contiguous() for t in want[1:])))
     assert sd.beam_select(x[:0], s[:0], k).scores.shape == (0, k)
@@ -333,6 +336,27 @@ def test_reorder_bad_parents(dev):
     st = torch.zeros(1, dtype=torch.int32, device=dev)
     y = sd.beam_reorder(x.to(dev), p.to(dev), status=st)
     assert torch.equal(y.cpu(), ref.reorder(x, p)[0]) and int(st) == sd.SD_STATUS_BAD_PARENT
+
+
+def test_reorder_into_rows_between_the_states(dev):
+    B, W, V = 3, 5, 37
+    x = _state((B, W, V), torch.int32, 7).to(dev)
+    p = torch.randint(0, W, (B, W), generator=_g(8), dtype=torch.int32).to(dev)
+    buf = torch.zeros((B, W, 2 * V), dtype=torch.int32, device=dev)
+    buf[..., :V] = x
+    got = sd.beam_reorder(buf[..., :V], p, out=buf[..., V:])
+    assert torch.equal(got, sd.beam_reorder(x, p)) and torch.equal(buf[..., :V], x)
+    with pytest.raises(ValueError, match="overlaps"):
+        sd.beam_reorder(buf[..., :V], p, out=buf[..., V - 1:2 * V - 1])
+
+
+def test_under_inference_mode(dev):
+    with torch.inference_mode():
+        x, s = _logits((2, 3, 500), F32, 30).to(dev), _scores(2, 3, 31).to(dev)
+        b = sd.beam_select(x, s, 3)
+        state = _state((2, 3, 9), torch.int32, 9).to(dev)
+        want, _ = ref.reorder(state.cpu(), b.parents.cpu())
+        assert torch.equal(sd.beam_reorder(state, b.parents, out=state).cpu(), want)
 
 
 def test_reorder_offsets_past_32_bits(dev):

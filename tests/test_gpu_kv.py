@@ -197,6 +197,8 @@ def test_fork_given_outputs_and_refusals(dev):
     assert got is out and all(torch.equal(a, b) for a, b in zip(got, want))
     assert [x._version for x in (*out, r2)] == [x + 1 for x in v]
     for bad in (lambda: sd.kv_fork(td, nd, p, rd, 4, out=out._replace(block_table=td[:4])),
+                lambda: sd.kv_fork(td, nd, p, rd, 4, out=out._replace(src=out.dst)),
+                lambda: sd.kv_fork(td, nd, p, rd, 4, out=out._replace(fill=p)),
                 lambda: sd.kv_fork(td, nd, p.view(2, 2)[:, :0], rd, 4),
                 lambda: sd.kv_fork(td[:5], nd[:5], p.view(2, 2), rd, 4),
                 lambda: sd.kv_fork(td, nd[:3], p, rd, 4), lambda: sd.kv_fork(td[0], nd, p, rd, 4),
