@@ -2,17 +2,25 @@
 // over W rows of V logits, by two launches.
 //
 //  1. sd_beam_stream_kernel: a warp per piece of a row, of up to 4 KB.  It writes
-//     the piece's (largest m, sum of 2^((x - m) c)) and the
-//     largest logit of every four lanes' vectors (a group).  No beam's row is
-//     read twice, and no warp waits for another.
-//  2. sd_beam_end_kernel: one CTA per sequence joins the sums of each beam in 64
-//     bits, and finds from the groups' largest logits alone a value that k of
-//     them reach: no candidate below it is among the k best.  The groups that
-//     reach it (little more than k of them) are read again, their logits that
-//     do are ranked in 64 bits.
+//     the piece's (largest m, sum of 2^((x - m) c)) and the largest logit of every
+//     four lanes' vectors (a group).  No beam's row is read twice, and no warp
+//     waits for another.
+//  2. sd_beam_end_kernel: one CTA per sequence joins the sums of each beam in whole
+//     units (the same in any order), and finds from the groups' largest logits
+//     alone a value that k of them reach: no candidate below it is among the k
+//     best.  The groups that reach it (little more than k of them) are read
+//     again, their logits that do are ranked in 64 bits.
 // A sequence of which more groups or logits reach the bound than there is room
-// for (thousands of equal logits at the k-th place) takes its beams one by one:
-// see each_beam.
+// for finds a better one from the logits of its best groups (narrow); where even
+// that is not enough (thousands of equal logits at the k-th place) its beams are
+// taken one by one (each_beam).
+//
+// Measured on the GPU: 64 x 8 rows of 151936 bf16 (a tenth of them finished), k 16,
+// 33.9 us: the stream 26 (140 MB, 5.4 TB/s; without the exponentials 25.5), the end
+// 8, chains of L2 and DRAM latencies, barriers and one search.  16 x 4 x 128256
+// bf16 10.7 us, 1 x 4 x 32000 fp32 7.4: launches and the end.  Tried: persistent
+// warps with a copy ring (40 us for the stream), one CTA of 256 threads per piece
+// with block sums (28), pieces of 2, 6 and 8 KB (40, 34.1, 36.6 in all).
 
 #include "sd_rows.cuh"
 #include "sd_beam.h"
@@ -24,7 +32,7 @@ constexpr int kSelSet = 4;       // lanes of a group
 constexpr int kSelSets = 32 / kSelSet;
 constexpr int kEndNT = 512;      // threads of a sequence's end
 constexpr int kEndU = 8;         // vectors of groups that one of them holds
-constexpr int kEndPieces = 2;    // pieces that a lane holds
+constexpr int kEndPieces = 4;    // pieces that a lane holds
 constexpr int kEndBins = 256;    // steps of the bound below the best
 constexpr int kSelList = 1024;   // listed groups, and candidates, of a sequence
 
@@ -55,7 +63,10 @@ __device__ __forceinline__ int ld_near(const uint8_t *p) {
   return v;
 }
 
-// How rows are cut: nc pieces of `share` vectors, at most U of them per lane.
+// How rows are cut: nc pieces of `share` vectors, at most U of them per lane: eight, or two
+// where that leaves SMs idle (two / eight, us: 8 x 4 x 1000 bf16 7.4 / 11.4, 1 x 4 x 32000 bf16
+// 7.5 / 8.1, fp32 7.6 / 7.7, 1 x 4 x 128256 bf16 8.4 / 8.1, 64 x 8 x 151936 57 / 34: the end reads
+// four times as much).
 struct SelectCut {
   int U, nc, share;
 };
@@ -63,7 +74,7 @@ static SelectCut select_cut(int64_t rows, int V, int es) {
   const int ve = 16 / es;
   const int nvec = (int)(((int64_t)V + ve - 1) / ve);
   SelectCut c;
-  c.U = rows * nvec >= (int64_t)8 * kSelNT * sm_count() ? 8 : 2;
+  c.U = rows * nvec >= (int64_t)2 * kSelNT * sm_count() ? 8 : 2;
   c.nc = (nvec + c.U * 32 - 1) / (c.U * 32);
   c.share = (nvec + c.nc - 1) / c.nc;
   return c;
@@ -121,9 +132,10 @@ struct ElemRow {
 
 // A warp per piece, in registers: warps share nothing, and CTAs are small, so that an SM asks
 // for new pieces whenever one of its warps is done.  The rows' scores come
-// through L1, where the CTAs before left them.
+// through L1, where the CTAs before left them.  Registers for ten CTAs per SM
+// (64 x 8 x 151936 bf16 33.9 us; the compiler's eight 35.3, eleven 34.9).
 template <typename E, int U>
-__global__ void __launch_bounds__(kSelNT) sd_beam_stream_kernel(const SelectParams P) {
+__global__ void __launch_bounds__(kSelNT, 10) sd_beam_stream_kernel(const SelectParams P) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
