@@ -1,7 +1,11 @@
 // Pages copied inside a cache's tensors: after a fork (the filled entries of
 // last pages) and after compaction (whole pages).
 //
-// A copy: what bounds it is memory.  The work is cut into pieces of at most
+// A copy: what bounds it is memory.  Measured on the GPU: 16384 pages of 4 KB in each of
+// 4 layers 88.8 us (537 MB, 6.0 TB/s, 90 % of a plain copy's rate); with eight
+// CTAs per SM and half the piece 112, with four 89.7, three 89.0, one CTA of
+// twice the piece 88.9.  By CTAs of 256 threads, a page each: 194.
+// The work is cut into pieces of at most
 // 32 kCpU vectors of one part of one page of one layer, one warp each; the number
 // of pairs is read on the device, and warps take pieces until there are none
 // left, with the next piece's page ids already asked for.  A piece's five
