@@ -33,13 +33,14 @@ extern "C" {
  * [B][k]: scores = c (fp32; not divided), parents = w, tokens = v, ended = 1
  * where the beam was finished or v == eos (eos = -1: no token ends a beam).
  * Slots left over hold -inf, -1, -1, 0.  Scores, their differences and the
- * ranking are in 64 bits, the sums of exponentials in fp32 per 16-byte vector
- * group and in 64 bits above that.
+ * ranking are in 64 bits, the sums of exponentials in fp32 per piece of a row
+ * (up to 4 KB) and in whole units of 2^-31 above that.
  *   A beam offers nothing where its score is -inf (a dead beam), where its
  * row holds only -inf, where its row holds a NaN or +inf or its score is NaN
  * or +inf (SD_STATUS_NONFINITE), or where its norm is not positive and finite
  * (SD_STATUS_BAD_PENALTY).
- * 1 <= W <= SD_MAX_BEAMS, 1 <= k <= SD_MAX_TOP; T (host) positive and finite.
+ * 1 <= W <= SD_MAX_BEAMS, 1 <= k <= SD_MAX_TOP; T (host) positive, normal and
+ * finite.
  * workspace: at least sd_beam_select_workspace_size bytes, 16-byte aligned;
  * nothing in it needs clearing, and calls that share it must not overlap on
  * the GPU.

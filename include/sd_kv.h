@@ -68,7 +68,8 @@ extern "C" {
  *   parents null (R = rows_in, table_out = table, len_out null, keep = 0):
  * the rows go on in place, each as its own heir: sd_kv_extend.
  * Otherwise table_out and len_out must not overlap table and kv_len.
- * R, rows_in <= SD_MAX_ROWS; N <= SD_MAX_PAGES.  workspace: at least
+ * R, rows_in <= SD_MAX_ROWS; N <= SD_MAX_PAGES; max_pages page_size and
+ * max_pages R below 2^31.  workspace: at least
  * sd_kv_fork_workspace_size bytes, 16-byte aligned; nothing in it needs
  * clearing, and calls that share it must not overlap on the GPU.
  */

@@ -261,6 +261,7 @@ struct SelectEnd {
   float bound;
   float margin;                       // the largest size of what entered an o
   int n_list, n_cand, n_best;
+  int wild;                           // an image passes fp32: it prunes nothing
   unsigned long long kth;             // of kth_largest: the bits so far
   int rank, count;
 
@@ -370,10 +371,13 @@ struct EndView {
     __syncthreads();
     return S.n_cand <= kSelList;
   }
+  // the score of a live beam's token
+  __device__ __forceinline__ double score(int w, float x) const {
+    return S.base[w] + ((double)x - (double)S.image[w].x) * P.inv_T;
+  }
   // a candidate; logits of a finished beam are not looked at
   __device__ __noinline__ void offer(int w, int v, float x) const {
-    double c = S.base[w];
-    if (S.kind[w] == 1) c += ((double)x - (double)S.image[w].x) * P.inv_T;
+    const double c = S.kind[w] == 1 ? score(w, x) : S.base[w];
     const int i = atomicAdd(&S.n_cand, 1);
     if (i < kSelList) {
       S.key[i] = dord(c * S.over[w]);
@@ -537,10 +541,11 @@ __device__ __noinline__ bool narrow(const EndView<E, U> &X, float top, float mar
 // The beams one by one, whatever their logits: the k best of one by value, then
 // by index, join the k best so far.
 //  - v*, the k-th largest of its groups' largest;
-//  - the logits above v* lie in fewer than k groups.  If they are more than k,
+//  - the logits above v* lie in fewer than k groups.  If they are k or more,
 //    the key (value, index) of the k-th bounds them;
 //  - if they are fewer, logits equal to v* fill up, lowest index first, from the
-//    row's beginning until there are enough.
+//    row's beginning until there are enough; so do other logits of the k-th's
+//    score, where there are any.
 template <typename E, int U>
 __device__ __noinline__ void each_beam(const EndView<E, U> &X) {
   constexpr int VE = EndView<E, U>::VE, NT = kEndNT, size = EndView<E, U>::kSize;
@@ -599,23 +604,42 @@ __device__ __noinline__ void each_beam(const EndView<E, U> &X) {
     above(0ull, [&](float, int) { ++more; });
     more = block_count(S, more);
     unsigned long long from = 0ull;
-    if (more > k)
+    if (more >= k)
       from = kth_largest(S, k, 64, [&](auto f) {
         above(0ull, [&](float x, int v) { f(top_key(x, v)); });
       });
-    above(from, [&](float x, int v) { X.offer(w, v, x); });
-    if (more < k) {
-      int need = k - more;
+    // the k-th logit, and those whose scores are the same in 64 bits: others than itself only
+    // where its neighbours' are (logits near zero, temperatures that leave no difference)
+    const float kth = more >= k ? key_value(from) : least;
+    const double rank = X.score(w, kth);
+    const bool alone = X.score(w, nextafterf(kth, -INFINITY)) < rank &&
+                       X.score(w, nextafterf(kth, INFINITY)) > rank;
+    const double near = alone ? 0.0
+                              : (fabs(S.base[w]) + fabs(rank) + 1.0) * 3.6e-15 / P.inv_T;
+    const auto ties = [&](float x) {
+      return x == kth ||
+             (!alone && fabs((double)x - (double)kth) <= near && X.score(w, x) == rank);
+    };
+    if (more >= k && alone) {
+      above(from, [&](float x, int v) { X.offer(w, v, x); });
+    } else {
+      int better = 0;
+      above(0ull, [&](float x, int v) {
+        if (!(x > kth) || ties(x)) return;
+        X.offer(w, v, x);
+        ++better;
+      });
+      int need = k - block_count(S, better);
       for (int q0 = 0; q0 < row.nvec && need > 0; q0 += NT) {
         float x[VE];
-        int n = 0;
-        if (q0 + tid < row.nvec) Elt<E>::unpack(row.load(q0 + tid), x);
+        unsigned same = 0u;
+        if (q0 + tid < row.nvec) {
+          Elt<E>::unpack(row.load(q0 + tid), x);
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          if (q0 + tid >= row.nvec) x[e] = neg_inf();
-          n += x[e] == least;
+          for (int e = 0; e < VE; ++e) same |= (x[e] > neg_inf() && ties(x[e]) ? 1u : 0u) << e;
         }
         // places in the order of the threads
+        const int n = __popc(same);
         int upto = n;
         __syncwarp();
 #pragma unroll
@@ -633,7 +657,7 @@ __device__ __noinline__ void each_beam(const EndView<E, U> &X) {
         }
 #pragma unroll
         for (int e = 0; e < VE; ++e)
-          if (x[e] == least) {
+          if (same >> e & 1u) {
             if (before < need) X.offer(w, row.first(q0 + tid) + e, x[e]);
             ++before;
           }
@@ -686,7 +710,7 @@ __global__ void __launch_bounds__(kEndNT, 1) sd_beam_end_kernel(const SelectPara
 #pragma unroll 1
     for (int i = warp + kEndPieces * NW; i < W * blocks; i += NW) f(i / blocks, load_piece(i));
   };
-  if (tid == 0) S.n_list = S.n_cand = 0;
+  if (tid == 0) S.n_list = S.n_cand = S.wild = 0;
   if (tid < kEndBins) S.hist[tid] = 0;
   if (tid < SD_MAX_BEAMS) {
     S.best = ford(neg_inf());
@@ -742,8 +766,10 @@ __global__ void __launch_bounds__(kEndNT, 1) sd_beam_end_kernel(const SelectPara
     // an fp32 image of what follows in 64 bits
     const float over = __fdividef(1.f, nm);
     const float log_z = 0.693147180559945309f * __log2f(z.hi);
-    S.image[lane] = make_float4(m, __fdividef(over, P.T), (s - log_z) * over,
-                                kind == 1 ? (fabsf(s) + log_z + 1.f) * over : -1.f);
+    const float4 f = make_float4(m, __fdividef(over, P.T), (s - log_z) * over,
+                                 kind == 1 ? (fabsf(s) + log_z + 1.f) * over : -1.f);
+    S.image[lane] = f;
+    if (kind == 1 && !(f.y < INFINITY && f.w < INFINITY)) S.wild = 1;
     if (bad && P.status) atomicOr(P.status, bad);
   }
   __syncthreads();
@@ -813,6 +839,7 @@ __global__ void __launch_bounds__(kEndNT, 1) sd_beam_end_kernel(const SelectPara
   bool fits = S.n_list <= kSelList;
   if (fits) fits = X.offer_listed(bound);
   if (!fits) fits = narrow<E, U>(X, top, S.margin);
+  if (S.wild) fits = false;
   if (fits) rank_candidates(S, k);
   else each_beam<E, U>(X);
   for (int i = tid; i < k; i += NT) {
@@ -871,7 +898,7 @@ extern "C" sd_status_t sd_beam_select(const sd_beam_select_args *a, void *stream
       a->k < 1 || a->k > SD_MAX_TOP)
     return SD_ERR_INVALID_ARG;
   if (a->dtype != SD_F32 && a->dtype != SD_BF16) return SD_ERR_INVALID_ARG;
-  if (!(a->T > 0.f) || !std::isfinite(a->T)) return SD_ERR_INVALID_ARG;
+  if (!(a->T >= 1.17549435e-38f) || !std::isfinite(a->T)) return SD_ERR_INVALID_ARG;
   if (a->eos < -1 || a->eos >= a->V || (a->finished && a->eos < 0)) return SD_ERR_INVALID_ARG;
   if (a->B == 0) return SD_OK;
   const int es = a->dtype == SD_BF16 ? 2 : 4;

@@ -656,7 +656,9 @@ extern "C" sd_status_t sd_kv_fork(const sd_kv_fork_args *a, void *stream) {
   if (need == 0 || a->max_pages < 0 || a->page_size < 1 || a->append < 0 || a->groups < 0 ||
       (a->keep != 0 && a->keep != 1))
     return SD_ERR_INVALID_ARG;
-  if ((int64_t)a->max_pages * a->page_size > INT32_MAX) return SD_ERR_INVALID_ARG;
+  if ((int64_t)a->max_pages * a->page_size > INT32_MAX ||
+      (int64_t)a->max_pages * a->R > INT32_MAX)
+    return SD_ERR_INVALID_ARG;
   const bool in_place = !a->parents;
   if (in_place && a->R > 0 && (a->R != a->rows_in || a->table_out != a->table || a->keep || a->len_out))
     return SD_ERR_INVALID_ARG;

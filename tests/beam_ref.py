@@ -16,6 +16,7 @@ def select(x, scores, k, T=1.0, finished=None, eos=-1, norm=None):
     """Per sequence the ranked candidates (rank, beam, token, score, ended), at least k + 1 of them
     where there are, with how far the device's score may be off; and the status."""
     B, W, V = x.shape
+    T = torch.tensor(T, dtype=torch.float32).item()   # an fp32 argument of the call
     out, tol, status = [], [], 0
     for b in range(B):
         found, off = [], 0.0

@@ -33,7 +33,7 @@ def test_select_refuses_bad_requests():
     assert L.sd_beam_select(None, None) == BAD
     for bad in (dict(B=-1), dict(W=0), dict(W=sd.SD_MAX_BEAMS + 1), dict(V=0),
                 dict(V=sd.SD_MAX_V + 1), dict(k=0), dict(k=sd.SD_MAX_TOP + 1), dict(dtype=2),
-                dict(T=0.0), dict(T=-1.0), dict(T=math.inf), dict(T=math.nan), dict(eos=-2),
+                dict(T=0.0), dict(T=-1.0), dict(T=math.inf), dict(T=math.nan), dict(T=1e-39), dict(eos=-2),
                 dict(eos=100), dict(finished=FAKE), dict(logits=None), dict(scores=None),
                 dict(out_scores=None), dict(parents=None), dict(tokens=None),
                 dict(workspace=None), dict(workspace=FAKE + 8), dict(workspace_bytes=size - 1),
@@ -79,7 +79,8 @@ def test_fork_refuses_bad_requests():
                 dict(table_out=None), dict(len_out=None), dict(src=None), dict(dst=None),
                 dict(fill=None), dict(count=None), dict(workspace=None),
                 dict(workspace=FAKE + 4), dict(workspace_bytes=size - 1),
-                dict(max_pages=2 ** 20, page_size=2 ** 12), dict(parents=None),
+                dict(max_pages=2 ** 20, page_size=2 ** 12),
+                dict(max_pages=2 ** 29, page_size=1), dict(parents=None),
                 dict(parents=None, R=4, table_out=FAKE, len_out=FAKE),
                 dict(parents=None, R=4, table_out=2 * FAKE, len_out=None),
                 dict(parents=None, R=4, table_out=FAKE, len_out=None, keep=1)):

@@ -156,6 +156,28 @@ def test_select_extreme_logits(dev):
         _run(dev, x, _scores(4, 3, 16), k, temperature=T)
 
 
+def test_select_scores_that_tie_where_logits_do_not(dev):
+    # differences of logits that no 64-bit score sees (below 2^-58 of it; between that and 2^-51 two
+    # ways of rounding tie different ones): ties go to the lowest token
+    for V, k in ((900, 12), (40000, 40)):
+        x = torch.randn((2, 3, V), generator=_g(34)) * 1e-30
+        x[1, 0, 5:50] = 1.0
+        x[1, 1, V - 30:] = 2e-15
+        _run(dev, x, _scores(2, 3, 35), k)
+        _run(dev, _logits((2, 3, V), F32, 36), _scores(2, 3, 37), k, temperature=1e18)
+
+
+def test_select_scales_that_pass_fp32(dev):
+    # temperatures and norms at the ends of the type's range: scores over norm beyond fp32
+    x, s = _logits((2, 4, 700), F32, 32), _scores(2, 4, 33)
+    s[1] = -s[1]
+    norm = torch.ones((2, 4))
+    norm[0, 1], norm[0, 3], norm[1, 0], norm[1, 2] = 1e-38, 1e38, 2e-37, 3e38
+    for T in (1.2e-38, 1e-20, 1.0, 1e20, 3e38):
+        for n in (None, norm):
+            _run(dev, x, s, 7, temperature=T, **({} if n is None else {"norm": n}))
+
+
 def test_select_nonfinite_rows_and_scores(dev):
     V, k = 4001, 8
     for bad in (math.nan, math.inf):
