@@ -2,7 +2,8 @@
 over beams and vocabulary, and the reordering of what a loop keeps per beam.  Paged caches
 follow the same parents by kv_fork.
 
-Like the rest of the package this module only checks and marshals arguments.
+Like the rest of the package this module only checks and marshals arguments; every call takes
+stream= as well, and runs on the current stream without it.
 
   beam_select(...)     sd_beam_select
   beam_reorder(...)    sd_beam_reorder

@@ -312,8 +312,9 @@ __device__ __forceinline__ void fork_row(const ForkParams &P, int i, int tid, in
           const bool page = (unsigned)e[u] < (unsigned)P.N;
           if (j < s.used && !page) bad |= SD_STATUS_BAD_PAGE;
           if (j < s.full && page && add) atomicAdd(P.refs + e[u], add);
-          if (j >= s.full && j < s.used && copy) {   // gets a page of its own
-            if (heir && !give_back(P.refs, e[u])) bad |= SD_STATUS_BAD_PAGE;
+          if (j >= s.full && j < s.used && copy) {   // gets a page of its own: in place it may be
+            // there already, so that the old one's id is the plan's
+            if (heir && !give_back(P.refs, row.last)) bad |= SD_STATUS_BAD_PAGE;
             continue;
           }
           if (j >= s.used && j < s.need && !(heir && page)) continue;   // gets a page

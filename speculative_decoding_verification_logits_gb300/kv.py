@@ -3,7 +3,8 @@ extending block tables, giving pages back, copying pages and moving the pages in
 front of the pool.  kv_rollback truncates the same tables.
 
 A pool of N pages is refs [N] (int32): how many table entries hold each page; 0 is a free page.
-Like the rest of the package this module only checks and marshals arguments.
+Like the rest of the package this module only checks and marshals arguments; every call takes
+stream= as well, and runs on the current stream without it.
 
   kv_fork(...), kv_extend(...)   sd_kv_fork
   kv_free(...)                   sd_kv_free

@@ -184,6 +184,28 @@ def test_extend_prompts_and_a_shared_last_page(dev):
         assert torch.equal(a.cpu(), b)
 
 
+@pytest.mark.parametrize("rows", [12, 600])
+def test_extend_rows_that_share_their_last_pages(dev, rows):
+    # every row copies its last page in place while its old one is given back
+    g = _g(rows)
+    M, page = 40, 8
+    t = torch.full((rows, M), -1, dtype=I32)
+    ids = torch.randperm(4000 + rows * 8, generator=g).to(I32)
+    n = torch.zeros(rows, dtype=I32)
+    for r in range(0, rows, 3):
+        held = int(_ints(1, 30, (1,), g))
+        t[r:r + 3, :held] = ids[r * 10 % 3000:][:held]
+        n[r:r + 3] = held * page - int(_ints(0, page, (1,), g))
+    refs = torch.bincount(t[t >= 0].long(), minlength=len(ids)).to(I32)
+    want = ref.fork(t, n, None, refs, page, append=9)
+    assert int(want[5]) > rows // 3
+    for _ in range(20):
+        td, rd = t.to(dev), refs.to(dev)
+        m = sd.kv_extend(td, n.to(dev), rd, page, 9)
+        for a, b in zip((td, *m, rd), (want[0], *want[2:7])):
+            assert torch.equal(a.cpu(), b)
+
+
 def test_fork_given_outputs_and_refusals(dev):
     g = _g(11)
     t, n, refs = _tables(2, 3, 5, 4, g)
