@@ -147,21 +147,20 @@ def beam_reorder(states, parents, *, out=None, status=None):
         return [] if out is None else out
     if len(xs) > SD_MAX_STATES or (ys is not None and len(ys) != len(xs)):
         raise ValueError(f"at most {SD_MAX_STATES} states, and as many outputs")
-    dev = xs[0].device
-    _need(parents, "parents", torch.int32, None, dev)
-    if parents.dim() != 2 or xs[0].dim() < 2:
+    dev, shape = xs[0].device, parents.shape
+    if len(shape) != 2 or xs[0].dim() < 2:
         raise ValueError("parents must be [B][k], states [B][W][...]")
-    (B, k), W = parents.shape, xs[0].shape[1]
+    p = _i32(parents, "parents", shape, dev)
+    (B, k), W = shape, xs[0].shape[1]
     if ys is None and k > W:
         raise ValueError("parents has more slots than there are rows: give out")
-    a = (StateArgs * len(xs))()
-    made = []
+    a, made = [], []   # the fields of the sd_beam_states, all of 64 bits
     for i, x in enumerate(xs):
         sb, sw, row = _state(x, "states", B, W, dev)
         if ys is None:
             y = torch.empty((B, k, *x.shape[2:]), dtype=x.dtype, device=dev)
             made.append(y)
-            a[i] = (x.data_ptr(), sb, sw, y.data_ptr(), k * row, row, row)
+            a += x.data_ptr(), sb, sw, y.data_ptr(), k * row, row, row
             continue
         y = ys[i]
         if y is not x or k != W:
@@ -172,14 +171,15 @@ def beam_reorder(states, parents, *, out=None, status=None):
             to = sb, sw, row
         if B > 1 and to[0] == 0 and row or k > 1 and to[1] == 0 and row:
             raise ValueError("out must not be expanded")
-        a[i] = (x.data_ptr(), sb, sw, y.data_ptr(), to[0], to[1], row)
+        a += x.data_ptr(), sb, sw, y.data_ptr(), to[0], to[1], row
     if ys is not None:
         if len(ys) > 1 or ys[0] is not xs[0]:
             _apart_or_same(xs, ys)
         if any(_rows_meet(y, parents[None], 2) for y in ys):
             raise ValueError("out overlaps parents")
     st = None if status is None else _i32(status, "status", (1,), dev)
-    rc = _lib().sd_beam_reorder(B, W, k, parents.data_ptr(), len(xs), ctypes.addressof(a), st,
+    fields = (ctypes.c_int64 * len(a))(*a)
+    rc = _lib().sd_beam_reorder(B, W, k, p, len(xs), ctypes.addressof(fields), st,
                                 _stream_of(dev))
     if rc:
         _check(rc, "sd_beam_reorder")
