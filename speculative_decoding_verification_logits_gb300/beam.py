@@ -17,7 +17,7 @@ from typing import NamedTuple
 import torch
 
 from . import _P, _check, _need
-from .kv import _all_apart, _i32, _on_device, _rows_meet, _scratch
+from .kv import _all_apart, _i32, _on_device, _rows_meet, _scratch, _small
 from .logits import _lib, _rows, _same, _stream_of, _written
 
 SD_MAX_BEAMS, SD_MAX_STATES = 32, 16
@@ -74,6 +74,7 @@ def beam_select(logits, scores, k: int, *, temperature: float = 1.0, finished=No
     dt = _rows(logits, "logits", (3,))
     dev = logits.device
     B, W, V = logits.shape
+    _small(k, eos)
     a = SelectArgs(B, W, V, k, dt, logits.data_ptr(), logits.stride(0), logits.stride(1))
     if scores.dtype is not torch.float32 or scores.device != dev or scores.shape != (B, W) \
             or not scores.is_contiguous():

@@ -427,17 +427,6 @@ __device__ __forceinline__ int block_count(SelectEnd &S, int n) {
   return n;
 }
 
-// One more in a bin: lanes that all name the same one add together.
-__device__ __forceinline__ void count_in(int *hist, int bin) {
-  const unsigned here = __activemask();
-  const int first = __ffs(here) - 1;
-  if (__all_sync(here, bin == __shfl_sync(here, bin, first))) {
-    if ((threadIdx.x & 31) == first) atomicAdd(&hist[bin], __popc(here));
-  } else {
-    atomicAdd(&hist[bin], 1);
-  }
-}
-
 // The key of the k-th largest of those that each(f) calls f(key) for, 0 where they are
 // fewer: eight bits at a time.
 template <typename F>
@@ -455,7 +444,7 @@ __device__ __forceinline__ unsigned long long kth_largest(SelectEnd &S, int k, i
     const int rank = S.rank;
     each([&](unsigned long long key) {
       // the largest digit in the first bin
-      if (((key ^ known) >> shift) >> 8 == 0ull) count_in(S.hist, 255 - (int)(key >> shift & 255u));
+      if (((key ^ known) >> shift) >> 8 == 0ull) atomicAdd(&S.hist[255 - (int)(key >> shift & 255u)], 1);
     });
     __syncthreads();
     if (tid < 32) {

@@ -190,6 +190,13 @@ def _scratch(which, device, *sizes):
     return (n + 15) // 16 * 4
 
 
+def _small(*numbers):
+    """Refuses numbers that would wrap around on their way into the library's int32."""
+    for n in numbers:
+        if not -(1 << 31) <= n < 1 << 31:
+            raise ValueError(f"{n} is out of range")
+
+
 def _fork(a, refs, status, dev, sizes):
     """Runs sd_kv_fork with new outputs of these sizes (in the struct's order) where there are
     any; returns them."""
@@ -234,6 +241,7 @@ def kv_fork(block_table, kv_len, parents, refs, page_size: int, *, append: int =
     R = parents.numel()
     if R == 0:
         raise ValueError("parents must name at least one row")
+    _small(page_size, append)
     groups = shape[0] if len(shape) == 2 else 0
     if groups and rows % groups:
         raise ValueError(f"{rows} rows are not {groups} groups")
@@ -260,6 +268,7 @@ def kv_extend(block_table, kv_len, refs, page_size: int, append: int, *, status=
     pages, and a partly filled last page that others hold too becomes the row's own (kv_copy of
     the returned pairs must follow where rows may share one)."""
     rows, M, table, lens, dev = _table(block_table, kv_len)
+    _small(page_size, append)
     a = ForkArgs(rows, rows, 0, M, page_size, append, 0)
     a.table = a.table_out = table
     a.kv_len = lens

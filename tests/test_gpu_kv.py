@@ -227,6 +227,10 @@ def test_fork_given_outputs_and_refusals(dev):
                 lambda: sd.kv_fork(td, nd, p, rd[:0], 4)):
         with pytest.raises(ValueError):
             bad()
+    for bad in (lambda: sd.kv_fork(td, nd, p, rd, 4, append=2 ** 32 + 1),
+                lambda: sd.kv_extend(td, nd, rd, 2 ** 32 + 4, 1)):
+        with pytest.raises(ValueError, match="out of range"):
+            bad()
     for bad in (lambda: sd.kv_fork(td.long(), nd, p, rd, 4), lambda: sd.kv_fork(td, nd, p.long(), rd, 4),
                 lambda: sd.kv_fork(td, nd, p, rd.float(), 4)):
         with pytest.raises(TypeError):
@@ -234,6 +238,31 @@ def test_fork_given_outputs_and_refusals(dev):
     for bad in (lambda: sd.kv_fork(td, nd, p, rd, 0), lambda: sd.kv_fork(td, nd, p, rd, 4, append=-1)):
         with pytest.raises(sd.SDError):
             bad()
+
+
+def test_fork_of_no_rows_no_slots_and_no_entries(dev):
+    i = lambda *s: torch.zeros(s, dtype=I32, device=dev)
+    refs = torch.ones(3, dtype=I32, device=dev)
+    refs[1] = 0
+    # from an empty table: empty rows, or bad parents
+    st = i(1)
+    f = sd.kv_fork(i(0, 4), i(0), torch.tensor([-1, 0], dtype=I32, device=dev), refs, 4, append=3,
+                   status=st)
+    assert f.block_table.tolist() == [[-1] * 4] * 2 and f.kv_len.tolist() == [0, 0]
+    assert int(st) == sd.SD_STATUS_BAD_PARENT and refs.tolist() == [1, 0, 1]
+    # tables without slots
+    f = sd.kv_fork(i(2, 0), i(2) + 7, i(3), refs, 4)
+    assert f.block_table.shape == (3, 0) and f.kv_len.tolist() == [0, 0, 0]
+    # extending nothing, and empty rows
+    m = sd.kv_extend(i(0, 4), i(0), refs, 4, 5)
+    assert m.count.tolist() == [0] and m.src.numel() == 0
+    t = i(1, 4) - 1
+    sd.kv_extend(t, i(1), refs, 4, 1)
+    assert t.tolist() == [[1, -1, -1, -1]] and refs.tolist() == [1, 1, 1]
+    assert sd.kv_free(i(0, 4), refs, which=torch.zeros(0, dtype=torch.uint8, device=dev)) is refs
+    one = torch.ones(1, dtype=I32, device=dev)
+    c = sd.kv_compact(one)
+    assert c.src.numel() == 0 and c.live.tolist() == [1] and c.new_ids.tolist() == [0]
 
 
 # --------------------------------------------------------------------- free --
