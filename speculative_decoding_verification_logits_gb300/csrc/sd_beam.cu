@@ -3,7 +3,7 @@
 //
 //  1. sd_beam_stream_kernel: a warp per piece of a row, of up to 4 KB.  It writes
 //     the piece's (largest m, sum of 2^((x - m) c)) and the largest logit of every
-//     four lanes' vectors (a group).  No beam's row is read twice, and no warp
+//     two lanes' vectors (a group).  No beam's row is read twice, and no warp
 //     waits for another.
 //  2. sd_beam_end_kernel: one CTA per sequence joins the sums of each beam in whole
 //     units (the same in any order), and finds from the groups' largest logits
@@ -16,11 +16,12 @@
 // taken one by one (each_beam).
 //
 // Measured on the GPU: 64 x 8 rows of 151936 bf16 (a tenth of them finished), k 16,
-// 33.9 us: the stream 26 (140 MB, 5.4 TB/s; without the exponentials 25.5), the end
-// 8, chains of L2 and DRAM latencies, barriers and one search.  16 x 4 x 128256
-// bf16 10.7 us, 1 x 4 x 32000 fp32 7.4: launches and the end.  Tried: persistent
+// 33.1 us: the stream 26 (140 MB, 5.4 TB/s; without the exponentials 25.5), the end
+// 7, chains of L2 and DRAM latencies, barriers and one search.  16 x 4 x 128256
+// bf16 10.2 us, 1 x 4 x 32000 fp32 7.7: launches and the end.  Tried: persistent
 // warps with a copy ring (40 us for the stream), one CTA of 256 threads per piece
-// with block sums (28), pieces of 2, 6 and 8 KB (40, 34.1, 36.6 in all).
+// with block sums (28), pieces of 2, 6 and 8 KB (40, 34.1, 36.6 in all);
+// groups of one, four and eight lanes (35.7, 33.5, 35).
 
 #include "sd_rows.cuh"
 #include "sd_beam.h"
@@ -28,7 +29,7 @@
 namespace sdv {
 
 constexpr int kSelNT = 128;      // threads of a streaming CTA
-constexpr int kSelSet = 4;       // lanes of a group
+constexpr int kSelSet = 2;       // lanes of a group
 constexpr int kSelSets = 32 / kSelSet;
 constexpr int kEndNT = 512;      // threads of a sequence's end
 constexpr int kEndU = 8;         // vectors of groups that one of them holds
@@ -133,7 +134,7 @@ struct ElemRow {
 // A warp per piece, in registers: warps share nothing, and CTAs are small, so that an SM asks
 // for new pieces whenever one of its warps is done.  The rows' scores come
 // through L1, where the CTAs before left them.  Registers for ten CTAs per SM
-// (64 x 8 x 151936 bf16 33.9 us; the compiler's eight 35.3, eleven 34.9).
+// (64 x 8 x 151936 bf16 33.1 us; the compiler's eight 1.4 more, eleven 1).
 template <typename E, int U>
 __global__ void __launch_bounds__(kSelNT, 10) sd_beam_stream_kernel(const SelectParams P) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -322,31 +323,16 @@ struct EndView {
   // calls f(beam, first token, logits) for the vectors of the listed groups
   template <typename F>
   __device__ __forceinline__ void each_listed(F f) const {
-    constexpr int kAhead = 2;
     const int items = S.n_list * kSize;
 #pragma unroll 1
-    for (int i0 = threadIdx.x; i0 < items; i0 += kAhead * kEndNT) {
-      uint4 v[kAhead];
-      int at[kAhead];
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int i = i0 + u * kEndNT;
-        at[u] = -1;
-        if (i >= items) continue;
-        const int g = S.list[i / kSize];
-        const ElemRow<E> r = row(g >> 16);
-        const int q = vector(r, g & 0xffff, i % kSize);
-        if (q < 0) continue;
-        v[u] = r.load(q);
-        at[u] = (g >> 16) << kTokenBits | r.first(q);
-      }
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        if (at[u] < 0) continue;
-        float x[VE];
-        Elt<E>::unpack(v[u], x);
-        f(at[u] >> kTokenBits, at[u] & ((1 << kTokenBits) - 1), x);
-      }
+    for (int i = threadIdx.x; i < items; i += kEndNT) {
+      const int g = S.list[i / kSize], w = g >> 16;
+      const ElemRow<E> r = row(w);
+      const int q = vector(r, g & 0xffff, i % kSize);
+      if (q < 0) continue;
+      float x[VE];
+      Elt<E>::unpack(r.load(q), x);
+      f(w, r.first(q), x);
     }
   }
   // what reaches the bound in the listed groups, and the finished beams, as candidates;
@@ -376,7 +362,7 @@ struct EndView {
     return S.base[w] + ((double)x - (double)S.image[w].x) * P.inv_T;
   }
   // a candidate; logits of a finished beam are not looked at
-  __device__ __noinline__ void offer(int w, int v, float x) const {
+  __device__ __forceinline__ void offer(int w, int v, float x) const {
     const double c = S.kind[w] == 1 ? score(w, x) : S.base[w];
     const int i = atomicAdd(&S.n_cand, 1);
     if (i < kSelList) {
