@@ -31,9 +31,7 @@ namespace sdv {
 constexpr int kSelNT = 128;      // threads of a streaming CTA
 constexpr int kSelSet = 2;       // lanes of a group
 constexpr int kSelSets = 32 / kSelSet;
-constexpr int kEndNT = 512;      // threads of a sequence's end
-constexpr int kEndU = 8;         // vectors of groups that one of them holds
-constexpr int kEndPieces = 4;    // pieces that a lane holds
+constexpr int kEndNT = 512;      // threads of a sequence's end, at most
 constexpr int kEndBins = 256;    // steps of the bound below the best
 constexpr int kSelList = 1024;   // listed groups, and candidates, of a sequence
 
@@ -325,7 +323,7 @@ struct EndView {
   __device__ __forceinline__ void each_listed(F f) const {
     const int items = S.n_list * kSize;
 #pragma unroll 1
-    for (int i = threadIdx.x; i < items; i += kEndNT) {
+    for (int i = threadIdx.x; i < items; i += blockDim.x) {
       const int g = S.list[i / kSize], w = g >> 16;
       const ElemRow<E> r = row(w);
       const int q = vector(r, g & 0xffff, i % kSize);
@@ -379,7 +377,7 @@ __device__ __forceinline__ void rank_candidates(SelectEnd &S, int k) {
   __syncthreads();
   const int n = min(S.n_cand, kSelList), lane = threadIdx.x & 31;
 #pragma unroll 1
-  for (int i = threadIdx.x >> 5; i < n; i += kEndNT / 32) {
+  for (int i = threadIdx.x >> 5; i < n; i += blockDim.x / 32) {
     const unsigned long long key = S.key[i];
     const int at = S.at[i];
     int above = 0;
@@ -408,8 +406,7 @@ __device__ __forceinline__ int block_count(SelectEnd &S, int n) {
   if ((threadIdx.x & 31) == 0) S.warp_n[threadIdx.x >> 5] = n;
   __syncthreads();
   n = 0;
-#pragma unroll
-  for (int i = 0; i < kEndNT / 32; ++i) n += S.warp_n[i];
+  for (int i = 0; i < blockDim.x / 32; ++i) n += S.warp_n[i];
   return n;
 }
 
@@ -457,7 +454,8 @@ static_assert(kEndBins == 256, "a digit of eight bits per bin");
 // the best), nor where more logits than there is room for lie in its bin.
 template <typename E, int U>
 __device__ __noinline__ bool narrow(const EndView<E, U> &X, float top, float margin) {
-  constexpr int NT = kEndNT, VE = Elt<E>::kPerVec;
+  constexpr int VE = Elt<E>::kPerVec;
+  const int NT = blockDim.x;
   SelectEnd &S = X.S;
   const int tid = threadIdx.x, ng = X.P.nc * kSelSets, W = X.P.W;
   const auto each_group = [&](auto f) {
@@ -523,7 +521,8 @@ __device__ __noinline__ bool narrow(const EndView<E, U> &X, float top, float mar
 //    score, where there are any.
 template <typename E, int U>
 __device__ __noinline__ void each_beam(const EndView<E, U> &X) {
-  constexpr int VE = EndView<E, U>::VE, NT = kEndNT, size = EndView<E, U>::kSize;
+  constexpr int VE = EndView<E, U>::VE, size = EndView<E, U>::kSize;
+  const int NT = blockDim.x;
   SelectEnd &S = X.S;
   const SelectParams &P = X.P;
   const int tid = threadIdx.x, k = P.k;
@@ -643,16 +642,20 @@ __device__ __noinline__ void each_beam(const EndView<E, U> &X) {
   }
 }
 
-template <typename E, int U>
-__global__ void __launch_bounds__(kEndNT, 1) sd_beam_end_kernel(const SelectParams P) {
-  constexpr int VE = Elt<E>::kPerVec, NT = kEndNT, NW = NT / 32;
+// NT threads, CTAs of them per SM: 512 and one where every sequence has an SM of its own, 256 and
+// four where there are more (us: 64 x 8 x 151936 bf16 33 / 44, 256 x 4 x 128256 57 / 53, 2000 x 8 x
+// 32000 251 / 201; 512 and two 37, 55, 232).
+template <typename E, int U, int NT, int CTAS>
+__global__ void __launch_bounds__(NT, CTAS) sd_beam_end_kernel(const SelectParams P) {
+  constexpr int NW = NT / 32, kEndU = NT / 64, kEndPieces = NT / 128;
+  static_assert(NT >= kEndBins && NT <= kEndNT, "a thread per bin, a count per warp");
   __shared__ SelectEnd S;
   const EndView<E, U> X(P, S);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, W = P.W, k = P.k;
   const int64_t b = blockIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // the groups' largest, kEndU vectors of four per thread
+  // the groups' largest, vectors of four held by the threads
   const int per = P.nc * kSelSets / 4, all = W * per;
   const float *gm = X.groups(0);
   uint4 held[kEndU];
@@ -843,8 +846,12 @@ static cudaError_t launch_select_u(const SelectParams &P, cudaStream_t s) {
   const cudaError_t e = cudaLaunchKernelEx(&cfg, sd_beam_stream_kernel<E, U>, P);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)P.B, 1, 1);
-  cfg.blockDim = dim3(kEndNT, 1, 1);
-  return cudaLaunchKernelEx(&cfg, sd_beam_end_kernel<E, U>, P);
+  if (P.B <= sm_count()) {
+    cfg.blockDim = dim3(512, 1, 1);
+    return cudaLaunchKernelEx(&cfg, sd_beam_end_kernel<E, U, 512, 1>, P);
+  }
+  cfg.blockDim = dim3(256, 1, 1);
+  return cudaLaunchKernelEx(&cfg, sd_beam_end_kernel<E, U, 256, 4>, P);
 }
 
 template <typename E>

@@ -278,7 +278,8 @@ def kv_extend(block_table, kv_len, refs, page_size: int, append: int, *, status=
 
 
 @_on_device
-def kv_free(pages, refs, *, which=None, count=None, clear: bool = False, status=None) -> torch.Tensor:
+def kv_free(pages, refs, *, which=None, count=None, clear: bool = False,
+            status=None) -> torch.Tensor:
     """Gives pages back to refs [N], in place: the ids in pages (int32, any shape; -1 is passed
     over), as kv_rollback lists them (pages=freed, count=free_offsets[-1:]), or the rows of a
     block table (which [rows] uint8: those whose flag is set).  clear=True makes the entries that
@@ -353,7 +354,8 @@ def _page_shape(shape, strides, size, first, name):
 
 
 @_on_device
-def kv_copy(caches, src, dst, *, count=None, fill=None, heads_first: bool = False, status=None) -> None:
+def kv_copy(caches, src, dst, *, count=None, fill=None, heads_first: bool = False,
+            status=None) -> None:
     """Copies page src[i] to page dst[i] (int32 [pairs], the first count [1] of them; -1, -1 is
     passed over) in every cache, in place.  caches: one tensor [layers][N][...] or a sequence of
     [N][...] of one shape (keys and values of every layer), any type.  fill [pairs]: only the

@@ -52,7 +52,7 @@ def _run(dev, x, scores, k, status=0, **more):
 @pytest.mark.parametrize("B,W,V,k", [
     (1, 1, 1, 1), (1, 1, 1, 5), (2, 3, 1, 4), (3, 1, 7, 7), (2, 2, 33, 128), (1, 4, 1000, 4),
     (5, 7, 4099, 14), (3, 32, 517, 128), (1, 32, 32000, 32), (2, 4, 50021, 8), (4, 8, 128256, 16),
-    (1, 1, 262144, 128), (40, 3, 32000, 6)])
+    (1, 1, 262144, 128), (40, 3, 32000, 6), (200, 3, 700, 9), (170, 17, 2000, 40)])
 def test_select(dev, dtype, B, W, V, k):
     x = _logits((B, W, V), dtype, B + W + V + k)
     _run(dev, x, _scores(B, W, V), k, eos=V // 2)
@@ -130,6 +130,19 @@ def test_select_many_equal_logits(dev, dtype, V):
     s = torch.zeros((B, W)) - torch.arange(W) * 0.25
     s[1, 1] = -math.inf
     _run(dev, x, s, k, finished=fin, eos=1)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_select_many_sequences_of_every_kind(dev, dtype):
+    # more sequences than SMs: ordinary, equal, masked and crowded ones in turn
+    B, W, V, k = 180, 4, 9000, 24
+    x = _logits((B, W, V), dtype, 40)
+    x[1::6] = 0.5
+    x[2::6] = torch.finfo(dtype).min
+    x[2::6, :, 5:8] = 1.0
+    x[3::6, :, :3000] += 20
+    x[4::6, 1] = -math.inf
+    _run(dev, x, _scores(B, W, 41), k, eos=6)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
