@@ -184,18 +184,14 @@ __global__ void __launch_bounds__(kSelNT, 10) sd_beam_stream_kernel(const Select
   const int64_t at = (int64_t)n * P.nc + piece;
   if (lane % kSelSet == 0) P.gmax[at * kSelSets + lane / kSelSet] = m;
   m = rmax_f(m);
-  const ExpBase B(m, log2e_over(P.T));
+  // differences first: a beam that is sure of a token has a sum of exactly one
+  const ExpBase B = ExpBase::difference(m, log2e_over(P.T));
   uint64_t acc = 0ull;
-  if (!B.far) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) acc = VecExp<E>::template sum<false>(v[u], B, acc);
-  } else {
-#pragma unroll
-    for (int u = 0; u < U; ++u) acc = VecExp<E>::template sum<true>(v[u], B, acc);
-  }
+  for (int u = 0; u < U; ++u) acc = VecExp<E>::template sum<true>(v[u], B, acc);
   float x, y;
   upk2(acc, x, y);
-  const float z = warp_sum((x + y) * B.fix);
+  const float z = warp_sum(x + y);
   if (lane == 0) P.part[at] = make_float2(m, z);
 }
 

@@ -398,6 +398,17 @@ struct ExpBase {
     o = pk2(b, b);
     c = pk2(cc, cc);
   }
+  // the difference first at any offset: the term of m itself is then 1 to the bit
+  static __device__ __forceinline__ ExpBase difference(float m, float cc) {
+    ExpBase B;
+    const float s = m == neg_inf() ? 0.f : m;
+    B.far = true;
+    B.fix = 1.f;
+    B.o = pk2(-s, -s);
+    B.c = pk2(cc, cc);
+    return B;
+  }
+  __device__ __forceinline__ ExpBase() {}
   template <bool FAR>
   __device__ __forceinline__ void pair(uint64_t x, float &a, float &b) const {
     upk2(FAR ? mul2(add2(x, o), c) : fma2(x, c, o), a, b);

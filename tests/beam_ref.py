@@ -13,8 +13,8 @@ NONFINITE, BAD_PENALTY, BAD_PARENT, BAD_PAGE, NO_PAGE = 0x4, 0x8, 0x10, 0x20, 0x
 
 # ------------------------------------------------------------------- select --
 def select(x, scores, k, T=1.0, finished=None, eos=-1, norm=None):
-    """Per sequence the ranked candidates (rank, beam, token, score, ended), at least k + 1 of them
-    where there are, with how far the device's score may be off; and the status."""
+    """Per sequence the ranked candidates (rank, beam, token, score, ended), every beam's k + 1 best,
+    with how far the device's score may be off; and the status."""
     B, W, V = x.shape
     T = torch.tensor(T, dtype=torch.float32).item()   # an fp32 argument of the call
     out, tol, status = [], [], 0
@@ -59,35 +59,36 @@ def select(x, scores, k, T=1.0, finished=None, eos=-1, norm=None):
 
 
 def check_select(beams, want, k, norm=None):
-    """Holds the device's beams to the ranked candidates: the same ones, in the same order, but
-    for candidates that lie closer together than their scores may be off."""
+    """Holds the device's beams to the ranked candidates: nothing that was left out lies further
+    above what was taken than the two may be off, the order is theirs but for candidates as close
+    as that, and a beam's own candidates come in the order of their logits, then tokens."""
     found, tol, _ = want
     for b, cand in enumerate(found):
         n = min(k, len(cand))
-        got = [t[b].tolist() for t in beams]
-        at = {(w, v): (r, c, e) for r, w, v, c, e in cand}
-        seen = set()
-        for j in range(k):
-            score, w, v, ended = (g[j] for g in got)
-            if j >= n:
-                assert (score, w, v, ended) == (-math.inf, -1, -1, 0)
-                continue
-            r, rw, rv, c, e = cand[j]
-            scale = 1.0 if norm is None else float(norm[b, rw])
-            assert (w, v) not in seen
-            seen.add((w, v))
-            if (w, v) != (rw, rv):     # only where the definition nearly ties
-                assert (w, v) in at, (b, j, (w, v), cand[j])
-                mine = 1.0 if norm is None else float(norm[b, w])
-                near = tol[b] / scale + tol[b] / mine + abs(r) * 2.0 ** -50
-                assert 0 < abs(at[w, v][0] - r) <= near, (b, j, (w, v), cand[j], at[w, v])
-                r, c, e = at[w, v]
-            assert ended == e
+        scores, parents, tokens, ended = (t[b].tolist() for t in beams)
+        assert all(g == (-math.inf, -1, -1, 0)
+                   for g in zip(scores[n:], parents[n:], tokens[n:], ended[n:]))
+        at = {(w, v): i for i, (_, w, v, _, _) in enumerate(cand)}
+        over = lambda w: tol[b] / (1.0 if norm is None else float(norm[b, w]))
+        near = lambda p, q: over(p[1]) + over(q[1]) + abs(p[0]) * 2.0 ** -50
+        places = [at.get((w, v)) for w, v in zip(parents[:n], tokens[:n])]
+        assert None not in places and len(set(places)) == n, (b, places)
+        for p, q in zip(places, places[1:]):
+            assert cand[p][0] >= cand[q][0] - near(cand[p], cand[q]), (b, cand[p], cand[q])
+        for w in set(parents[:n]):
+            own = [p for p in places if cand[p][1] == w]
+            assert own == sorted(own), (b, w, own)
+        for i in sorted(set(range(n)) - set(places)):   # left out: as good as what came instead
+            worst = cand[max(places)]
+            assert cand[i][0] <= worst[0] + near(cand[i], worst), (b, cand[i], worst)
+        for score, p, e in zip(scores, places, ended):
+            c = cand[p][3]
+            assert e == cand[p][4]
             f = torch.tensor(c, dtype=D).to(torch.float32).item()
             if math.isinf(f):
                 assert score == f
             else:
-                assert abs(score - c) <= tol[b] + U * abs(c) + U * tol[b], (b, j, score, c)
+                assert abs(score - c) <= tol[b] + U * abs(c) + U * tol[b], (b, score, cand[p])
 
 
 # ------------------------------------------------------------------ reorder --

@@ -86,6 +86,21 @@ def test_select_first_step_and_equal_beams(dev):
     assert b.parents[0, :8].tolist() == [0, 1, 2, 3] * 2
 
 
+@pytest.mark.parametrize("V", [1, 2, 701, 40000])
+def test_select_beams_that_are_sure_tie_in_their_order(dev, V):
+    # one token has all of the probability: its score is the beam's own, to the bit
+    g = _g(V)
+    for dtype, T in ((BF, 1.0), (F32, 0.3), (F32, 7.0)):
+        B, W = 3, 9
+        x = torch.randn((B, W, V), generator=g) - 900.0
+        at = torch.randint(0, V, (B, W, 1), generator=g)
+        x = x.scatter(2, at, 20 + 20 * torch.rand((B, W, 1), generator=g)).to(dtype)
+        s = torch.tensor([0.0, -1.25, 3.0])[:, None].expand(B, W).contiguous()
+        b = sd.beam_select(x.to(dev), s.to(dev), W, temperature=T)
+        assert torch.equal(b.scores.cpu(), s) and torch.equal(b.tokens.cpu().long(), at[..., 0])
+        assert b.parents.tolist() == [list(range(W))] * B
+
+
 def test_select_masked_rows(dev):
     # rows of which a mask leaves nothing, one token, and fewer tokens than slots
     for dtype in (BF, F32):
