@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import math
 from typing import NamedTuple
 
@@ -96,21 +97,29 @@ _device = torch._C._cuda_getDevice   # the current one's index
 
 
 def _on_device(fn):
-    """Runs a wrapper with its first tensor's device as the current one, and with `stream` (when
-    given) as the current stream: what it allocates belongs to the stream that it launches on."""
+    """Runs a wrapper with the device of its first parameter, however that is passed, as the current
+    one, and with `stream` (when given) as the current stream: what it allocates belongs to the
+    stream that it launches on."""
+    first = next(iter(inspect.signature(fn).parameters))
+
     @functools.wraps(fn)
     def call(*args, stream=None, **kwargs):
-        t = args[0] if args else next(iter(kwargs.values()), None)
+        t = args[0] if args else kwargs.get(first)
+        if t is not None and not isinstance(t, (torch.Tensor, list, tuple)):
+            t = tuple(t)   # looked at here and by the wrapper
+            if args:
+                args = (t, *args[1:])
+            else:
+                kwargs[first] = t
         while isinstance(t, (list, tuple)) and t:
             t = t[0]
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            return fn(*args, **kwargs)   # which says what is wrong
+        there = isinstance(t, torch.Tensor) and t.is_cuda   # if not, the wrapper says what is wrong
         if stream is not None:
-            if stream.device != t.device:
+            if there and stream.device != t.device:
                 raise ValueError(f"stream is on {stream.device}, expected {t.device}")
             with torch.cuda.stream(stream):
                 return fn(*args, **kwargs)
-        if t.get_device() != _device():
+        if there and t.get_device() != _device():
             with torch.cuda.device(t.device):
                 return fn(*args, **kwargs)
         return fn(*args, **kwargs)
