@@ -309,14 +309,15 @@ __device__ __forceinline__ void fork_row(const ForkParams &P, int i, int tid, in
         for (int u = 0; u < kRowU; ++u) {
           const int j = j0 + u * kRowNT;
           if (j >= P.M) break;
-          const bool page = (unsigned)e[u] < (unsigned)P.N;
-          if (j < s.used && !page) bad |= SD_STATUS_BAD_PAGE;
-          if (j < s.full && page && add) atomicAdd(P.refs + e[u], add);
-          if (j >= s.full && j < s.used && copy) {   // gets a page of its own: in place it may be
-            // there already, so that the old one's id is the plan's
+          if (j >= s.full && j < s.used && copy) {   // gets a page of its own: in place that (or -1
+            // where there is none) may be there already, so that the old one's id is the plan's,
+            // which found it to be one
             if (heir && !give_back(P.refs, row.last)) bad |= SD_STATUS_BAD_PAGE;
             continue;
           }
+          const bool page = (unsigned)e[u] < (unsigned)P.N;
+          if (j < s.used && !page) bad |= SD_STATUS_BAD_PAGE;
+          if (j < s.full && page && add) atomicAdd(P.refs + e[u], add);
           if (j >= s.used && j < s.need && !(heir && page)) continue;   // gets a page
           if (!in_place) out[j] = j < s.need || heir ? e[u] : -1;
         }
