@@ -52,11 +52,15 @@ extern "C" {
  *   Pages are taken in the order of rows, then slots: the i-th that is needed
  * is the i-th free page by id, as refs were before the call.  Where none is
  * left the slot becomes -1 and SD_STATUS_NO_PAGE is set (the pair of such a
- * copy is -1, -1); the same bit is set where n + append passes the table,
- * which then bounds it.
+ * copy is -1, -1), but an heir keeps the page that it could not copy, shared as
+ * it was: no row that goes on loses entries.  A later call in place
+ * (sd_kv_extend) takes the pages that were missing, that copy's among them;
+ * until then such a row must not be written.  Other rows whose last page
+ * could not be copied are to be forked again.  NO_PAGE is set too where
+ * n + append passes the table, which then bounds it.
  *   refs: + 1 for each slot that holds a page anew; old rows that end without
- * an heir give their pages back, and an heir gives back a page that it had to
- * copy.
+ * an heir give their pages back, and an heir gives back a page that it
+ * copied.
  *   A parent of -1 (or, with SD_STATUS_BAD_PARENT, one outside the rows) makes
  * an empty row.  Slots within a row's length that hold no page id are passed
  * on and set SD_STATUS_BAD_PAGE.

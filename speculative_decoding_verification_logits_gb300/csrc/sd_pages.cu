@@ -283,7 +283,8 @@ __device__ __forceinline__ int free_pages(const uint32_t *bits, const int32_t *c
 }
 
 // Row i, new and old, by five warps (tid in them): four share the new row's slots out and give
-// the old one's pages back, the fifth finds the new row's own pages.
+// the old one's pages back, the fifth finds the new row's own pages and gives the one back that an
+// heir copied.
 __device__ __forceinline__ void fork_row(const ForkParams &P, int i, int tid, int *slots) {
   const int lane = tid & 31;
   unsigned bad = 0u;
@@ -309,12 +310,9 @@ __device__ __forceinline__ void fork_row(const ForkParams &P, int i, int tid, in
         for (int u = 0; u < kRowU; ++u) {
           const int j = j0 + u * kRowNT;
           if (j >= P.M) break;
-          if (j >= s.full && j < s.used && copy) {   // gets a page of its own: in place that (or -1
-            // where there is none) may be there already, so that the old one's id is the plan's,
-            // which found it to be one
-            if (heir && !give_back(P.refs, row.last)) bad |= SD_STATUS_BAD_PAGE;
-            continue;
-          }
+          // a page of its own comes here: in place it may be there already, so that the plan is
+          // asked for the old one, which it found to be one
+          if (j >= s.full && j < s.used && copy) continue;
           const bool page = (unsigned)e[u] < (unsigned)P.N;
           if (j < s.used && !page) bad |= SD_STATUS_BAD_PAGE;
           if (j < s.full && page && add) atomicAdd(P.refs + e[u], add);
@@ -361,8 +359,12 @@ __device__ __forceinline__ void fork_row(const ForkParams &P, int i, int tid, in
             P.dst[row.pair] = page;
           }
         });
+        // the old page of a copy: its row holds it on where no page was found for the copy
+        const bool stays = first && heir && got == q;
+        if (first && heir && !stays && lane == 0 && !give_back(P.refs, row.last))
+          bad |= SD_STATUS_BAD_PAGE;
         for (int x = got - q + lane; x < n; x += 32) {   // none left
-          out[slots[x]] = -1;
+          out[slots[x]] = stays && x == 0 ? row.last : -1;
           bad |= SD_STATUS_NO_PAGE;
           if (first && x == 0) {
             P.src[row.pair] = -1;

@@ -275,7 +275,9 @@ def kv_fork(block_table, kv_len, parents, refs, page_size: int, *, append: int =
 def kv_extend(block_table, kv_len, refs, page_size: int, append: int, *, status=None) -> KVMoves:
     """Room for `append` more entries in every row of block_table, in place: its rows get free
     pages, and a partly filled last page that others hold too becomes the row's own (kv_copy of
-    the returned pairs must follow where rows may share one)."""
+    the returned pairs must follow where rows may share one).  Where the pool runs out (status:
+    SD_STATUS_NO_PAGE) rows keep what they hold: give pages back and call again before they
+    are written."""
     rows, M, table, lens, dev = _table(block_table, kv_len)
     _small(page_size, append)
     a = ForkArgs(rows, rows, 0, M, page_size, append, 0)

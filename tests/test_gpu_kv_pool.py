@@ -5,6 +5,8 @@ import torch
 
 pytestmark = pytest.mark.gpu
 
+from tests import pool_ref  # noqa: E402
+
 sd = pytest.importorskip("speculative_decoding_verification_logits_gb300")
 
 I32 = torch.int32
@@ -43,3 +45,68 @@ def test_extend_without_pages_says_so_alone(dev, rows, full, free):
         assert int(m.count) == rows and int((m.src >= 0).sum()) == min(free, rows)
         got = td[:min(free, rows), full].cpu()
         assert got.tolist() == list(range(len(refs) - free, len(refs)))[:rows]
+
+
+def _check(dev, t, n, parents, refs, page, times=1, **more):
+    """kv_fork (or kv_extend, without parents) held to the definition, the status too."""
+    want = pool_ref.fork(t, n, parents, refs, page, **more)
+    for _ in range(times):
+        td, nd, rd = t.to(dev), n.to(dev), refs.to(dev)
+        st = torch.zeros(1, dtype=I32, device=dev)
+        if parents is None:
+            m = sd.kv_extend(td, nd, rd, page, more["append"], status=st)
+            got = (td, nd, *m, rd)
+        else:
+            got = (*sd.kv_fork(td, nd, parents.to(dev), rd, page, status=st, **more), rd)
+            assert torch.equal(td.cpu(), t) and torch.equal(nd.cpu(), n)
+        names = ("table", "len", "src", "dst", "fill", "count", "refs")
+        for name, a, b in zip(names, got, want if parents is not None else (want[0], n, *want[2:])):
+            assert torch.equal(a.cpu(), b), name
+        assert int(st) == want[-1]
+    return want
+
+
+@pytest.mark.parametrize("rows,full", [(2, 0), (6, 3), (6, 600), (300, 5), (60, 700)])
+@pytest.mark.parametrize("free", [0, 1, 2, 3, 7])
+def test_rows_keep_last_pages_that_they_cannot_copy(dev, rows, full, free):
+    page = 4
+    t, n, refs = _sharing(rows, full, full + 4, page, free)
+    for append in (0, 1, 9):
+        want = _check(dev, t, n, None, refs, page, times=3, append=append)
+        if free < rows:
+            assert want[-1] == sd.SD_STATUS_NO_PAGE
+            assert bool((want[0][:, full] >= 0).all())
+            held = want[0][want[0] >= 0].long()
+            assert torch.equal(torch.bincount(held, minlength=len(refs)).to(I32), want[6])
+    g = torch.Generator().manual_seed(rows + free)
+    for R in (1, rows, rows + 5):
+        p = torch.randint(-1, rows, (R,), generator=g, dtype=I32)
+        for keep in (False, True):
+            _check(dev, t, n, p, refs, page, append=2, keep=keep)
+
+
+def test_extend_again_after_pages_come_free(dev):
+    # the entries of shared last pages outlast a pool that is full, and a later call copies them
+    rows, full, page = 8, 2, 4
+    t, n, refs = _sharing(rows, full, full + 2, page, 1)
+    n += 1
+    spare = torch.arange(len(refs), len(refs) + 12, dtype=I32)[None]
+    refs = torch.cat([refs, torch.ones(12, dtype=I32)])
+    td, nd, rd, sp = t.to(dev), n.to(dev), refs.to(dev), spare.to(dev)
+    cache = torch.randint(0, 99, (1, len(refs), page, 3), dtype=I32, device=dev)
+    read = lambda: cache[0, td.long().clamp(min=0)].flatten(1, 2)[:, :full * page + 2]
+    before = read()
+    st = torch.zeros(1, dtype=I32, device=dev)
+    for status in (sd.SD_STATUS_NO_PAGE, 0):
+        st.zero_()
+        m = sd.kv_extend(td, nd, rd, page, 3, status=st)
+        sd.kv_copy(cache, m.src, m.dst, count=m.count, fill=m.fill)
+        assert int(st) == status and torch.equal(read(), before)
+        if status:
+            sd.kv_free(sp, rd)           # another request ends
+            sd.kv_free(td[7:], rd)       # and one of the rows
+            td, nd, before = td[:7].contiguous(), nd[:7].contiguous(), before[:7]
+    # every row now writes into pages of its own
+    for j in (full, full + 1):
+        own = td[:, j]
+        assert len(set(own.tolist())) == 7 and bool((rd[own.long()] == 1).all())
