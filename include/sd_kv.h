@@ -60,7 +60,10 @@ extern "C" {
  * n + append passes the table, which then bounds it.
  *   refs: + 1 for each slot that holds a page anew; old rows that end without
  * an heir give their pages back, and an heir gives back a page that it
- * copied.
+ * copied.  Ids outside [0, N), pages that were free before the call (rows
+ * that were given back and not cleared name such), and pages given back more
+ * often than they are then held set SD_STATUS_BAD_PAGE; counts end at 0, and a
+ * page that the call handed out stays held.
  *   A parent of -1 (or, with SD_STATUS_BAD_PARENT, one outside the rows) makes
  * an empty row.  Slots within a row's length that hold no page id are passed
  * on and set SD_STATUS_BAD_PAGE.

@@ -1,5 +1,6 @@
 """Forks and extensions of block tables from their definition, in plain Python: also of pools that run
-out, where a row that goes on keeps a shared last page that it cannot copy."""
+out, where a row that goes on keeps a shared last page that it cannot copy, and of tables that name
+pages which they do not hold: what is added to the counts comes first, then what is given back."""
 import torch
 
 BAD_PAGE, NO_PAGE = 0x20, 0x40
@@ -33,7 +34,8 @@ def fork(table, kv_len, parents, refs, page, append=0, keep=False):
                 if copy:
                     pairs.append((old, row[j], held) if got else (-1, -1, held))
                     if heir and got:
-                        less[old] += 1
+                        less[old] += before[old] != 0
+                        status |= 0 if before[old] else BAD_PAGE
                     elif heir:
                         row[j] = old
                 if got:
@@ -46,9 +48,9 @@ def fork(table, kv_len, parents, refs, page, append=0, keep=False):
     for p in range(len(T)):
         if not keep and p not in heirs:
             for e in T[p]:
-                if 0 <= e < N:
+                if 0 <= e < N and before[e]:
                     less[e] += 1
-                elif e != -1:
+                elif e != -1:   # none, or one that was free before the call
                     status |= BAD_PAGE
     after = [before[p] + more[p] - less[p] for p in range(N)]
     status |= BAD_PAGE if min(after) < 0 else 0

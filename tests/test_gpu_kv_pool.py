@@ -110,3 +110,49 @@ def test_extend_again_after_pages_come_free(dev):
     for j in (full, full + 1):
         own = td[:, j]
         assert len(set(own.tolist())) == 7 and bool((rd[own.long()] == 1).all())
+
+
+@pytest.mark.parametrize("groups,M", [(3, 5), (16, 20), (60, 9), (130, 300)])
+@pytest.mark.parametrize("free", [0, 4, 60])
+def test_fork_leaves_out_rows_that_were_given_back(dev, groups, M, free):
+    # rows given back without clear name pages that are free by then, or that only others hold
+    page, W = 4, 4
+    g = torch.Generator().manual_seed(groups + free)
+    shared = M // 2
+    own = torch.randperm(groups * (shared + W * (M - 1 - shared)), generator=g).to(I32)
+    t = torch.full((groups, W, M), -1, dtype=I32)
+    t[:, :, :shared] = own[:groups * shared].view(groups, 1, shared)
+    t[:, :, shared:M - 1] = own[groups * shared:].view(groups, W, -1)
+    t = t.view(groups * W, M)
+    n = torch.full((groups * W,), (M - 1) * page - 1, dtype=I32)
+    refs = torch.bincount(t[t >= 0].long(), minlength=len(own)).to(I32)
+    gone = torch.zeros(groups * W, dtype=torch.uint8)
+    gone[torch.randperm(groups * W, generator=g)[:groups * W // 3]] = 1
+    gone[0], gone[1] = 1, 0
+    rd = torch.cat([refs, torch.zeros(free, dtype=I32)]).to(dev)
+    sd.kv_free(t.to(dev), rd, which=gone.to(dev))
+    refs = rd.cpu()
+    left = (gone == 0).nonzero().flatten()
+    for R in (len(left), groups * W):   # pages that were given back come into use again, or run out
+        p = left[torch.randint(0, len(left), (R,), generator=g)].to(I32)
+        want = _check(dev, t, n, p, refs, page, times=10, append=2)
+        assert want[-1] & sd.SD_STATUS_BAD_PAGE
+        new = want[0]
+        taken = new[(new >= 0) & (refs[new.clamp(min=0).long()] == 0)].long()
+        assert bool((want[6][taken] >= 1).all())
+    _check(dev, t, n, p, refs, page, append=2, keep=True)
+
+
+@pytest.mark.parametrize("rows", [6, 40, 900])
+def test_fork_gives_back_more_than_is_held(dev, rows):
+    # one page in every row, counted once: it gains holders and loses more of them, in any order
+    t = torch.zeros((rows, 3), dtype=I32)
+    t[:, 1:] = 1 + torch.arange(2 * rows, dtype=I32).view(rows, 2) // 4
+    n = torch.full((rows,), 12, dtype=I32)
+    refs = torch.ones(10 + rows, dtype=I32)
+    g = torch.Generator().manual_seed(rows)
+    for R in (1, rows // 2, rows, rows + 5):
+        for held in (1, 2, rows // 2):
+            refs[0] = held
+            p = torch.randint(0, max(1, rows // 3), (R,), generator=g, dtype=I32)
+            _check(dev, t, n, p, refs, 4, times=10)

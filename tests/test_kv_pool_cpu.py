@@ -44,3 +44,15 @@ def test_definitions_agree_while_pages_last():
                 a = beam_ref.fork(t, n, parents, refs, page, append=app, keep=keep)
                 b = pool_ref.fork(t, n, parents, refs, page, append=app, keep=keep)
                 assert a[7] == b[7] and all(torch.equal(x, y) for x, y in zip(a[:7], b)), seed
+
+
+def test_tables_that_name_pages_of_others_by_hand():
+    # row 0 was given back and not cleared: page 4 is free, page 3 is row 1's alone
+    t, n = i32([[3, 4], [3, 5]]), i32([8, 6])
+    got = pool_ref.fork(t, n, i32([1, 1]), i32([1, 1, 1, 1, 0, 1]), 4)
+    # page 4 is handed out by this call and stays held, page 3 is shared and given back once
+    assert got[0].tolist() == [[3, 5], [3, 4]] and got[6].tolist() == [1, 1, 1, 1, 1, 1]
+    assert got[7] == pool_ref.BAD_PAGE
+    # counts end at zero
+    got = pool_ref.fork(i32([[3], [3], [3]]), i32([4, 4, 4]), i32([-1]), i32([0, 0, 0, 1]), 4)
+    assert got[6].tolist() == [0, 0, 0, 0] and got[7] == pool_ref.BAD_PAGE
