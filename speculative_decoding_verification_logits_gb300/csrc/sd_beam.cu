@@ -129,11 +129,33 @@ struct ElemRow {
   }
 };
 
+// From this temperature on x / T is taken as (x / 2) / (T / 2), the same but for logits that are zero
+// to it: the difference of two logits may pass fp32's range, and at lower ones its exponential is zero.
+constexpr float kFarT = 1.329227995784915872903807060280344576e36f;   // 2^120
+
+// Terms 2^((x - m) c), the differences first: the term of m itself is 1 to the bit.
+template <bool HALVES>
+struct BeamExp {
+  uint64_t o, c;
+  __device__ __forceinline__ BeamExp(float m, float T) {
+    constexpr float unit = HALVES ? 0.5f : 1.f;
+    const float s = m == neg_inf() ? 0.f : -m * unit, k = log2e_over(T * unit);
+    o = pk2(s, s);
+    c = pk2(k, k);
+  }
+  template <bool FAR>
+  __device__ __forceinline__ void pair(uint64_t x, float &a, float &b) const {
+    upk2(mul2(HALVES ? fma2(x, pk2(0.5f, 0.5f), o) : add2(x, o), c), a, b);
+    a = ex2(a);
+    b = ex2(b);
+  }
+};
+
 // A warp per piece, in registers: warps share nothing, and CTAs are small, so that an SM asks
 // for new pieces whenever one of its warps is done.  The rows' scores come
 // through L1, where the CTAs before left them.  Registers for ten CTAs per SM
 // (64 x 8 x 151936 bf16 33.1 us; the compiler's eight 1.4 more, eleven 1).
-template <typename E, int U>
+template <typename E, int U, bool HALVES>
 __global__ void __launch_bounds__(kSelNT, 10) sd_beam_stream_kernel(const SelectParams P) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -184,8 +206,8 @@ __global__ void __launch_bounds__(kSelNT, 10) sd_beam_stream_kernel(const Select
   const int64_t at = (int64_t)n * P.nc + piece;
   if (lane % kSelSet == 0) P.gmax[at * kSelSets + lane / kSelSet] = m;
   m = rmax_f(m);
-  // differences first: a beam that is sure of a token has a sum of exactly one
-  const ExpBase B = ExpBase::difference(m, log2e_over(P.T));
+  // a beam that is sure of a token has a sum of exactly one
+  const BeamExp<HALVES> B(m, P.T);
   uint64_t acc = 0ull;
 #pragma unroll
   for (int u = 0; u < U; ++u) acc = VecExp<E>::template sum<true>(v[u], B, acc);
@@ -256,7 +278,7 @@ struct SelectEnd {
   float bound;
   float margin;                       // the largest size of what entered an o
   int n_list, n_cand, n_best;
-  int wild;                           // an image passes fp32: it prunes nothing
+  int wild;                           // an image leaves fp32: it prunes nothing
   unsigned long long kth;             // of kth_largest: the bits so far
   int rank, count;
 
@@ -699,10 +721,10 @@ __global__ void __launch_bounds__(NT, CTAS) sd_beam_end_kernel(const SelectParam
     if (lane == 0) atomicMax(&S.top[w], m);
   });
   __syncthreads();
-  const float c2 = log2e_over(P.T);
+  const float unit = P.T >= kFarT ? 0.5f : 1.f, c2 = log2e_over(P.T * unit);
   each_block([&](int w, const float2 &p) {
     // at most 2^11; a piece with a NaN or +inf has a sum of NaN
-    const float t = p.y == 0.f ? 0.f : p.y * ex2((p.x - fdeord(S.top[w])) * c2);
+    const float t = p.y == 0.f ? 0.f : p.y * ex2((p.x * unit - fdeord(S.top[w]) * unit) * c2);
     const float units = t * 1024.f, whole = truncf(units);
     const bool bad = __any_sync(0xffffffffu, !(t <= 4096.f));
     const unsigned hi = __reduce_add_sync(0xffffffffu, __float2uint_rn(whole));
@@ -743,7 +765,11 @@ __global__ void __launch_bounds__(NT, CTAS) sd_beam_end_kernel(const SelectParam
     const float4 f = make_float4(m, __fdividef(over, P.T), (s - log_z) * over,
                                  kind == 1 ? (fabsf(s) + log_z + 1.f) * over : -1.f);
     S.image[lane] = f;
-    if (kind == 1 && !(f.y < INFINITY && f.w < INFINITY)) S.wild = 1;
+    // where a factor or a difference of logits passes fp32, or a quotient is too small for it (and
+    // zero for divisors from 2^126 on), the image says nothing
+    if (kind == 1 && !(f.y >= 1.1754943508222875e-38f && f.y < INFINITY && f.w < INFINITY &&
+                       m - kLowest < INFINITY))
+      S.wild = 1;
     if (bad && P.status) atomicOr(P.status, bad);
   }
   __syncthreads();
@@ -839,7 +865,8 @@ static cudaError_t launch_select_u(const SelectParams &P, cudaStream_t s) {
   cfg.stream = s;
   cfg.gridDim = dim3((unsigned)(P.B * P.W * P.per_row), 1, 1);
   cfg.blockDim = dim3(kSelNT, 1, 1);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, sd_beam_stream_kernel<E, U>, P);
+  const cudaError_t e = P.T >= kFarT ? cudaLaunchKernelEx(&cfg, sd_beam_stream_kernel<E, U, true>, P)
+                                     : cudaLaunchKernelEx(&cfg, sd_beam_stream_kernel<E, U, false>, P);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)P.B, 1, 1);
   if (P.B <= sm_count()) {

@@ -398,17 +398,6 @@ struct ExpBase {
     o = pk2(b, b);
     c = pk2(cc, cc);
   }
-  // the difference first at any offset: the term of m itself is then 1 to the bit
-  static __device__ __forceinline__ ExpBase difference(float m, float cc) {
-    ExpBase B;
-    const float s = m == neg_inf() ? 0.f : m;
-    B.far = true;
-    B.fix = 1.f;
-    B.o = pk2(-s, -s);
-    B.c = pk2(cc, cc);
-    return B;
-  }
-  __device__ __forceinline__ ExpBase() {}
   template <bool FAR>
   __device__ __forceinline__ void pair(uint64_t x, float &a, float &b) const {
     upk2(FAR ? mul2(add2(x, o), c) : fma2(x, c, o), a, b);
@@ -434,13 +423,13 @@ struct VecExp<__nv_bfloat16> {
   static __device__ __forceinline__ uint64_t widen(uint32_t w) {
     return pk2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   }
-  template <bool FAR>
-  static __device__ __forceinline__ uint64_t sum(const uint4 &v, const ExpBase &B, uint64_t acc) {
+  template <bool FAR, typename Base>
+  static __device__ __forceinline__ uint64_t sum(const uint4 &v, const Base &B, uint64_t acc) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float a, b;
-      B.pair<FAR>(widen(w[i]), a, b);
+      B.template pair<FAR>(widen(w[i]), a, b);
       acc = add2(acc, pk2(a, b));
     }
     return acc;
@@ -471,12 +460,12 @@ struct VecExp<float> {
   static __device__ __forceinline__ uint64_t two(uint32_t x, uint32_t y) {
     return pk2(__uint_as_float(x), __uint_as_float(y));
   }
-  template <bool FAR>
-  static __device__ __forceinline__ uint64_t sum(const uint4 &v, const ExpBase &B, uint64_t acc) {
+  template <bool FAR, typename Base>
+  static __device__ __forceinline__ uint64_t sum(const uint4 &v, const Base &B, uint64_t acc) {
     float a, b;
-    B.pair<FAR>(two(v.x, v.y), a, b);
+    B.template pair<FAR>(two(v.x, v.y), a, b);
     acc = add2(acc, pk2(a, b));
-    B.pair<FAR>(two(v.z, v.w), a, b);
+    B.template pair<FAR>(two(v.z, v.w), a, b);
     return add2(acc, pk2(a, b));
   }
   template <bool FAR>
