@@ -257,7 +257,7 @@ struct SelectEnd {
   // a beam: 0 offers nothing, 1 live, 2 finished; its score less the log of its sum
   int kind[SD_MAX_BEAMS];
   double base[SD_MAX_BEAMS];
-  double over[SD_MAX_BEAMS];          // 1 / norm
+  double norm[SD_MAX_BEAMS];          // where there are any
   int top[SD_MAX_BEAMS];              // its largest logit, ordered
   unsigned hi[SD_MAX_BEAMS];          // its sum in units of 2^-10 and of 2^-31
   unsigned lo[SD_MAX_BEAMS];
@@ -312,7 +312,7 @@ __device__ __forceinline__ float loosened(float bound, float size) {
 constexpr int kTokenBits = 18;
 static_assert(SD_MAX_V <= 1 << kTokenBits, "a token and a beam fit an int");
 
-template <typename E, int U>
+template <typename E, int U, bool NORMS>
 struct EndView {
   static constexpr int VE = Elt<E>::kPerVec;
   static constexpr int kSize = kSelSet * U;   // vectors of a group
@@ -377,12 +377,17 @@ struct EndView {
   __device__ __forceinline__ double score(int w, float x) const {
     return S.base[w] + ((double)x - (double)S.image[w].x) * P.inv_T;
   }
+  // What ranks it: the quotient itself, so that equal ones tie (5 / 5 and 49 / 49, say).  The product
+  // with 1 / norm, which may round to a neighbour, is 0.5 us faster (16 x 4 x 128256 bf16).
+  __device__ __forceinline__ double ranked(int w, double c) const {
+    return NORMS ? c / S.norm[w] : c;
+  }
   // a candidate; logits of a finished beam are not looked at
   __device__ __forceinline__ void offer(int w, int v, float x) const {
     const double c = S.kind[w] == 1 ? score(w, x) : S.base[w];
     const int i = atomicAdd(&S.n_cand, 1);
     if (i < kSelList) {
-      S.key[i] = dord(c * S.over[w]);
+      S.key[i] = dord(ranked(w, c));
       S.at[i] = w << kTokenBits | v;
       S.score[i] = (float)c;
     }
@@ -470,8 +475,8 @@ static_assert(kEndBins == 256, "a digit of eight bits per bin");
 // down that there is room for, then a bound from their logits instead of their largest.
 // Whether that was enough: not where the k-th lies below those groups (or more than 2^16 below
 // the best), nor where more logits than there is room for lie in its bin.
-template <typename E, int U>
-__device__ __noinline__ bool narrow(const EndView<E, U> &X, float top, float margin) {
+template <typename E, int U, bool NORMS>
+__device__ __noinline__ bool narrow(const EndView<E, U, NORMS> &X, float top, float margin) {
   constexpr int VE = Elt<E>::kPerVec;
   const int NT = blockDim.x;
   SelectEnd &S = X.S;
@@ -537,9 +542,9 @@ __device__ __noinline__ bool narrow(const EndView<E, U> &X, float top, float mar
 //  - if they are fewer, logits equal to v* fill up, lowest index first, from the
 //    row's beginning until there are enough; so do other logits of the k-th's
 //    score, where there are any.
-template <typename E, int U>
-__device__ __noinline__ void each_beam(const EndView<E, U> &X) {
-  constexpr int VE = EndView<E, U>::VE, size = EndView<E, U>::kSize;
+template <typename E, int U, bool NORMS>
+__device__ __noinline__ void each_beam(const EndView<E, U, NORMS> &X) {
+  constexpr int VE = EndView<E, U, NORMS>::VE, size = EndView<E, U, NORMS>::kSize;
   const int NT = blockDim.x;
   SelectEnd &S = X.S;
   const SelectParams &P = X.P;
@@ -600,17 +605,16 @@ __device__ __noinline__ void each_beam(const EndView<E, U> &X) {
       from = kth_largest(S, k, 64, [&](auto f) {
         above(0ull, [&](float x, int v) { f(top_key(x, v)); });
       });
-    // the k-th logit, and those whose scores are the same in 64 bits: others than itself only
-    // where its neighbours' are (logits near zero, temperatures that leave no difference)
+    // the k-th logit, and those that rank the same in 64 bits: others than itself only where its
+    // neighbours do (logits near zero, temperatures that leave no difference)
     const float kth = more >= k ? key_value(from) : least;
-    const double rank = X.score(w, kth);
-    const bool alone = X.score(w, nextafterf(kth, -INFINITY)) < rank &&
-                       X.score(w, nextafterf(kth, INFINITY)) > rank;
-    const double near = alone ? 0.0
-                              : (fabs(S.base[w]) + fabs(rank) + 1.0) * 3.6e-15 / P.inv_T;
+    const auto ranked = [&](float x) { return X.ranked(w, X.score(w, x)); };
+    const double c = X.score(w, kth), rank = X.ranked(w, c);
+    const bool alone = ranked(nextafterf(kth, -INFINITY)) < rank &&
+                       ranked(nextafterf(kth, INFINITY)) > rank;
+    const double near = alone ? 0.0 : (fabs(S.base[w]) + fabs(c) + 1.0) * 3.6e-15 / P.inv_T;
     const auto ties = [&](float x) {
-      return x == kth ||
-             (!alone && fabs((double)x - (double)kth) <= near && X.score(w, x) == rank);
+      return x == kth || (!alone && fabs((double)x - (double)kth) <= near && ranked(x) == rank);
     };
     if (more >= k && alone) {
       above(from, [&](float x, int v) { X.offer(w, v, x); });
@@ -663,12 +667,12 @@ __device__ __noinline__ void each_beam(const EndView<E, U> &X) {
 // NT threads, CTAs of them per SM: 512 and one where every sequence has an SM of its own, 256 and
 // four where there are more (us: 64 x 8 x 151936 bf16 33 / 44, 256 x 4 x 128256 57 / 53, 2000 x 8 x
 // 32000 251 / 201; 512 and two 37, 55, 232).
-template <typename E, int U, int NT, int CTAS>
+template <typename E, int U, int NT, int CTAS, bool NORMS>
 __global__ void __launch_bounds__(NT, CTAS) sd_beam_end_kernel(const SelectParams P) {
   constexpr int NW = NT / 32, kEndU = NT / 64, kEndPieces = NT / 128;
   static_assert(NT >= kEndBins && NT <= kEndNT, "a thread per bin, a count per warp");
   __shared__ SelectEnd S;
-  const EndView<E, U> X(P, S);
+  const EndView<E, U, NORMS> X(P, S);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, W = P.W, k = P.k;
   const int64_t b = blockIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -686,7 +690,7 @@ __global__ void __launch_bounds__(NT, CTAS) sd_beam_end_kernel(const SelectParam
   int ended = 0;
   if (mine) {
     s = ld_float(P.scores + b * W + lane);
-    if (P.norm) nm = ld_float(P.norm + b * W + lane);
+    if (NORMS) nm = ld_float(P.norm + b * W + lane);
     if (P.finished) ended = ld1(P.finished + b * W + lane);
   }
   // 32 pieces of a beam per warp.  Of a beam that is not read they may be anything.
@@ -812,7 +816,7 @@ __global__ void __launch_bounds__(NT, CTAS) sd_beam_end_kernel(const SelectParam
   } else if (mine) {   // meanwhile the beams' numbers in 64 bits
     const ff log_z = ff_log(z);
     S.base[lane] = ((double)s - (double)log_z.hi) - (double)log_z.lo;
-    S.over[lane] = P.norm ? 1.0 / (double)nm : 1.0;
+    if (NORMS) S.norm[lane] = (double)nm;
   }
   __syncthreads();
   const float bound = S.bound;
@@ -838,10 +842,10 @@ __global__ void __launch_bounds__(NT, CTAS) sd_beam_end_kernel(const SelectParam
   __syncthreads();
   bool fits = S.n_list <= kSelList;
   if (fits) fits = X.offer_listed(bound);
-  if (!fits) fits = narrow<E, U>(X, top, S.margin);
+  if (!fits) fits = narrow<E, U, NORMS>(X, top, S.margin);
   if (S.wild) fits = false;
   if (fits) rank_candidates(S, k);
-  else each_beam<E, U>(X);
+  else each_beam<E, U, NORMS>(X);
   for (int i = tid; i < k; i += NT) {
     const int64_t to = b * k + i;
     const bool have = i < S.n_best;
@@ -852,6 +856,17 @@ __global__ void __launch_bounds__(NT, CTAS) sd_beam_end_kernel(const SelectParam
     P.tokens[to] = v;
     if (P.ended) P.ended[to] = have && (S.kind[w] == 2 || v == P.eos);
   }
+}
+
+template <typename E, int U, bool NORMS>
+static cudaError_t launch_select_end(const SelectParams &P, cudaLaunchConfig_t &cfg) {
+  cfg.gridDim = dim3((unsigned)P.B, 1, 1);
+  if (P.B <= sm_count()) {
+    cfg.blockDim = dim3(512, 1, 1);
+    return cudaLaunchKernelEx(&cfg, sd_beam_end_kernel<E, U, 512, 1, NORMS>, P);
+  }
+  cfg.blockDim = dim3(256, 1, 1);
+  return cudaLaunchKernelEx(&cfg, sd_beam_end_kernel<E, U, 256, 4, NORMS>, P);
 }
 
 template <typename E, int U>
@@ -868,13 +883,7 @@ static cudaError_t launch_select_u(const SelectParams &P, cudaStream_t s) {
   const cudaError_t e = P.T >= kFarT ? cudaLaunchKernelEx(&cfg, sd_beam_stream_kernel<E, U, true>, P)
                                      : cudaLaunchKernelEx(&cfg, sd_beam_stream_kernel<E, U, false>, P);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)P.B, 1, 1);
-  if (P.B <= sm_count()) {
-    cfg.blockDim = dim3(512, 1, 1);
-    return cudaLaunchKernelEx(&cfg, sd_beam_end_kernel<E, U, 512, 1>, P);
-  }
-  cfg.blockDim = dim3(256, 1, 1);
-  return cudaLaunchKernelEx(&cfg, sd_beam_end_kernel<E, U, 256, 4>, P);
+  return P.norm ? launch_select_end<E, U, true>(P, cfg) : launch_select_end<E, U, false>(P, cfg);
 }
 
 template <typename E>

@@ -77,3 +77,21 @@ def test_differences_that_pass_fp32_between_worse_beams(dev, T):
     b = sd.beam_select(x.to(dev), s.to(dev), k, temperature=T)
     assert b.parents[0].tolist() == [0, 0] + [1] * (k - 2) and b.tokens[0, :2].tolist() == [7, 1900]
     _check(dev, x, s, k, T)
+
+
+@pytest.mark.parametrize("V", [1, 3, 5000])
+def test_scores_over_norms_that_are_equal_tie_in_their_order(dev, V):
+    # -n over n for n up to 256: finished beams, and beams that are sure of their token
+    g = torch.Generator().manual_seed(V)
+    B, W = 40, 32
+    n = torch.stack([torch.randperm(256, generator=g)[:W] + 1 for _ in range(B)]).float()
+    x = torch.full((B, W, V), -2e3)
+    x[:, :, V // 2] = 0.0
+    fin = (torch.rand((B, W), generator=g) < 0.5).to(torch.uint8)
+    for unit in (1.0, 0.375, 3.0):
+        s = -unit * n
+        b = sd.beam_select(x.to(dev), s.to(dev), W, norm=n.to(dev), finished=fin.to(dev), eos=V - 1)
+        assert b.parents.tolist() == [list(range(W))] * B
+        assert torch.equal(b.scores.cpu(), s) and torch.equal(b.finished.cpu() > 0, (fin > 0) |
+                                                              (b.tokens.cpu() == V - 1))
+        _check(dev, x, s, W, norm=n, eos=0)
