@@ -206,12 +206,31 @@ def _small(*numbers):
             raise ValueError(f"{n} is out of range")
 
 
+def _apart(what, at, n, *others):
+    """Refuses n int32s at an address, which a call writes, where they share memory with other
+    arguments: (address or None, bytes)."""
+    if at is None or not n:
+        return
+    end = at + 4 * n
+    for other, size in others:
+        if other is not None and size and other < end and at < other + size:
+            raise ValueError(f"{what} overlaps another argument")
+
+
 def _fork(a, refs, status, dev, sizes):
     """Runs sd_kv_fork with new outputs of these sizes (in the struct's order) where there are
     any; returns them."""
-    a.refs, a.N = _pool(refs, dev)
+    ref, N = _pool(refs, dev)
+    a.refs, a.N = ref, N
+    st = None
     if status is not None:
-        a.status = _i32(status, "status", (1,), dev)
+        a.status = st = _i32(status, "status", (1,), dev)
+    table, slots, parents = a.table, a.rows_in * a.max_pages, a.parents
+    read = (a.kv_len, 4 * a.rows_in), (parents, 4 * a.R)
+    _apart("refs", ref, N, (table, 4 * slots), (st, 4), *read)
+    _apart("status", st, 1, (table, 4 * slots), *read)
+    if parents is None:   # the table is written
+        _apart("block_table", table, slots, *read)
     n = _scratch("sd_kv_fork_workspace_size", dev.index, a.rows_in, a.R, a.N)
     sizes = (n, *sizes)
     buf = torch.empty(sum(sizes), dtype=_I32, device=dev)
@@ -298,9 +317,8 @@ def kv_free(pages, refs, *, which=None, count=None, clear: bool = False,
     dev, shape = pages.device, pages.shape
     p = _i32(pages, "pages", shape, dev if pages.is_cuda else None)
     ref, N = _pool(refs, dev)
-    if _meet(pages, refs):
-        raise ValueError("pages overlaps refs")
-    rows, cols, w, n, st = 1, pages.numel(), None, None, None
+    size = pages.numel()
+    rows, cols, w, n, st = 1, size, None, None, None
     if which is not None:
         if len(shape) != 2:
             raise ValueError("which needs pages [rows][max_pages]")
@@ -311,6 +329,11 @@ def kv_free(pages, refs, *, which=None, count=None, clear: bool = False,
         n = _i32(count, "count", (1,), dev)
     if status is not None:
         st = _i32(status, "status", (1,), dev)
+    read = (w, rows), (n, 4)
+    _apart("refs", ref, N, (p, 4 * size), (st, 4), *read)
+    _apart("status", st, 1, (p, 4 * size), *read)
+    if clear:
+        _apart("pages", p, size, *read)
     rc = _lib().sd_kv_free(rows, cols, p, w, n, bool(clear), N, ref, st, _stream_of(dev))
     if rc:
         _check(rc, "sd_kv_free")
@@ -331,12 +354,12 @@ def kv_compact(refs, block_table=None, *, status=None) -> KVCompact:
     table, n_table, st = None, 0, None
     if block_table is not None:
         p = _i32(block_table, "block_table", block_table.shape, dev)
-        if _meet(block_table, refs):
-            raise ValueError("block_table overlaps refs")
         n_table = block_table.numel()
         table = p if n_table else None
     if status is not None:
         st = _i32(status, "status", (1,), dev)
+    _apart("refs", ref, N, (table, 4 * n_table), (st, 4))
+    _apart("status", st, 1, (table, 4 * n_table))
     n, h = _scratch("sd_kv_compact_workspace_size", dev.index, N), N // 2
     sizes = (n, h, h, 1, 1, N)
     buf = torch.empty(sum(sizes), dtype=_I32, device=dev)
