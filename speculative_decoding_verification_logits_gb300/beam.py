@@ -17,7 +17,7 @@ from typing import NamedTuple
 import torch
 
 from . import _P, _check, _need
-from .kv import _all_apart, _i32, _on_device, _rows_meet, _scratch, _small
+from .kv import _all_apart, _i32, _lie_apart, _on_device, _rows_meet, _scratch, _small
 from .logits import _lib, _rows, _same, _stream_of, _written
 
 SD_MAX_BEAMS, SD_MAX_STATES = 32, 16
@@ -170,8 +170,8 @@ def beam_reorder(states, parents, *, out=None, status=None):
             to = _state(y, "out", B, k, dev)
         else:
             to = sb, sw, row
-        if B > 1 and to[0] == 0 and row or k > 1 and to[1] == 0 and row:
-            raise ValueError("out must not be expanded")
+        if not (y.is_contiguous() or _lie_apart(row, (B, to[0]), (k, to[1]))):
+            raise ValueError("rows of out overlap")
         a += x.data_ptr(), sb, sw, y.data_ptr(), to[0], to[1], row
     if ys is not None:
         if len(ys) > 1 or ys[0] is not xs[0]:

@@ -165,6 +165,22 @@ def _rows_meet(a, b, lead):
     return bool((torch.searchsorted(y, x + nx) > torch.searchsorted(y, x - ny, right=True)).any())
 
 
+def _lie_apart(size, *dims):
+    """Whether pieces of `size` bytes, (how many, bytes between them) along each dimension, share no
+    byte with one another."""
+    reach = size
+    for s, n in sorted((s, n) for n, s in dims if n > 1):
+        if s < reach:
+            break
+        reach += s * (n - 1)
+    else:
+        return True
+    at = torch.zeros((), dtype=torch.int64, device="cpu")
+    for n, s in dims:   # dimensions that lie between one another
+        at = at[..., None] + torch.arange(n, device="cpu") * s
+    return not bool((at.flatten().sort().values.diff() < size).any())
+
+
 def _all_apart(outs, *inputs):
     """Refuses outputs that share memory with an input or with one another (contiguous ones)."""
     for i, t in enumerate(outs):
@@ -420,9 +436,8 @@ def kv_copy(caches, src, dst, *, count=None, fill=None, heads_first: bool = Fals
         page = size * math.prod(shape[lead + 1:])
     else:
         page = _page_shape(shape, strides, size, lead + 1, "caches")
-        for d in range(lead + 1):
-            if shape[d] > 1 and strides[d] == 0:
-                raise ValueError("caches must not be expanded")
+        if not _lie_apart(page, *((shape[d], strides[d] * size) for d in range(lead + 1))):
+            raise ValueError("pages of a cache overlap")
     at = lead + 2 if heads_first else lead + 1
     if fill is not None and len(shape) <= at:
         raise ValueError("fill needs pages of [page_size][...], or [heads][page_size][...]")

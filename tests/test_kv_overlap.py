@@ -1,5 +1,5 @@
-"""Page calls refuse arguments that they write and that share memory with others (the counts above
-all: they change while tables and lengths are read)."""
+"""Calls refuse arguments that they write and that share memory with others (the counts of pages above
+all: they change while tables and lengths are read), and memory whose rows or pages overlap."""
 import pytest
 import torch
 
@@ -14,6 +14,50 @@ def test_which_addresses_overlap():
     for at, n, other, size in ((100, 4, 96, 4), (100, 4, 116, 1), (100, 4, 108, 0), (100, 0, 96, 8),
                                (None, 4, 0, 1000), (100, 4, None, 8)):
         kv._apart("refs", at, n, (other, size))
+
+
+def test_whether_pieces_lie_apart():
+    g = torch.Generator().manual_seed(1)
+    seen = set()
+    for _ in range(3000):
+        size, *dims = torch.randint(0, 9, (7,), generator=g).tolist()
+        dims = list(zip(dims[:3], dims[3:]))
+        used = [i * dims[0][1] + j * dims[1][1] + k * dims[2][1] + b for i in range(dims[0][0])
+                for j in range(dims[1][0]) for k in range(dims[2][0]) for b in range(size)]
+        want = len(set(used)) == len(used)
+        assert kv._lie_apart(size, *dims) == want, (size, dims)
+        seen.add(want)
+    assert len(seen) == 2 and kv._lie_apart(4, (2, 8), (2, 12)) and not kv._lie_apart(4, (2, 8), (3, 4))
+
+
+@pytest.mark.gpu
+def test_refusals_of_rows_and_pages_that_overlap():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    buf = torch.arange(600, dtype=torch.int32, device="cuda:0")
+    p = torch.tensor([[1, 0, 1], [2, 2, 0]], dtype=torch.int32, device="cuda:0")
+    x = buf[300:330].view(2, 3, 5)
+    before = buf.clone()
+    for strides in ((30, 4, 1), (4, 30, 1), (15, 0, 1), (0, 5, 1), (12, 5, 1), (8, 6, 1)):
+        y = torch.as_strided(buf, (2, 3, 5), strides)
+        for call in (lambda: sd.beam_reorder(x, p, out=y), lambda: sd.beam_reorder(y, p, out=y)):
+            with pytest.raises(ValueError, match="overlap"):
+                call()
+    i = lambda v: torch.tensor([v], dtype=torch.int32, device="cuda:0")
+    for shape, strides in (((2, 3, 4, 2), (30, 7, 2, 1)), ((2, 3, 4, 2), (8, 0, 2, 1)),
+                           ((2, 3, 4, 2), (8, 8, 2, 1))):
+        with pytest.raises(ValueError, match="overlap"):
+            sd.kv_copy(torch.as_strided(buf, shape, strides), i(0), i(1))
+    assert torch.equal(buf, before)
+    # rows of one sequence between those of another, pages of one layer between another's
+    y = torch.as_strided(buf, (2, 3, 5), (5, 11, 1))
+    sd.beam_reorder(x, p, out=y)
+    assert torch.equal(y, x.gather(1, p.long()[..., None].expand(2, 3, 5)))
+    c = torch.as_strided(buf, (2, 3, 4, 2), (8, 17, 2, 1))
+    want = c.clone()
+    want[:, 2] = want[:, 0]
+    sd.kv_copy(c, i(0), i(2))
+    assert torch.equal(c, want)
 
 
 @pytest.mark.gpu
