@@ -16,9 +16,9 @@
 // taken one by one (each_beam).
 //
 // Measured on the GPU: 64 x 8 rows of 151936 bf16 (a tenth of them finished), k 16,
-// 33.1 us: the stream 26 (140 MB, 5.4 TB/s; without the exponentials 25.5), the end
+// 33.3 us: the stream 26 (140 MB, 5.4 TB/s; without the exponentials 25.5), the end
 // 7, chains of L2 and DRAM latencies, barriers and one search.  16 x 4 x 128256
-// bf16 10.2 us, 1 x 4 x 32000 fp32 7.7: launches and the end.  Tried: persistent
+// bf16 with norms 10.8 us, 1 x 4 x 32000 fp32 7.7: launches and the end.  Tried: persistent
 // warps with a copy ring (40 us for the stream), one CTA of 256 threads per piece
 // with block sums (28), pieces of 2, 6 and 8 KB (40, 34.1, 36.6 in all);
 // groups of one, four and eight lanes (35.7, 33.5, 35).

@@ -10,11 +10,13 @@
 // in one launch of one cluster (fork_cluster, compact_cluster).
 //
 // Measured on the GPU: a fork of 512 rows of 513 slots (64 groups of 8 that share 400
-// pages) 11.3 us, of one row into 8 7.3; 171 rows of 513 slots given back, half of
-// them shared, 3.3; compaction of 65536 pages with 64 tables of 513 slots 9.8, of
-// 2000 pages 7.9.  None of them moves more than 3 MB: what they take are chains
-// of dependent loads through L2 (parent, length, last page, its count; counts,
-// bits, page) and launches.
+// pages) 12.6 us, of one row into 8 8.2; 171 rows of 513 slots given back, half of
+// them shared, 3.3; compaction of 65536 pages with 64 tables of 513 slots 9.5, of
+// 2000 pages 7.9; 9 entries more in each of 64 rows of 513 slots, in place, 10.3.  None
+// of them moves more than 3 MB: what they take are chains of dependent loads
+// through L2 (parent, length, last page, its count; counts, bits, page) and
+// launches.  A row that gets many pages is slow: one thread counts its empty slots and one warp
+// fills them, 513 pages of one row 71 us, 8192 1058.
 
 #include "sd_rows.cuh"
 #include "sd_kv.h"
@@ -674,9 +676,9 @@ struct PageLaunch {
 // CTAs of the one cluster that does a small call, 0: several launches are faster.  A launch costs
 // the host 3 to 5 us, which is what small calls wait for; on the GPU alone, where the launches
 // overlap, the cluster is a little behind.  Measured, us, one launch / several, call (GPU
-// alone): fork of one prompt into 8 rows of 513 slots 65 (7.2) / 73 (6.7) with its copies,
+// alone): fork of one prompt into 8 rows of 513 slots 56 (8.3) / 65 (7.6) with its copies,
 // compaction of 2000 pages 67 (8.1) / 77 (7.3) with its copies; compaction of 65536 pages (15.5 / 9.5)
-// and a fork of 512 rows (43 / 11) are the GPU's.
+// and a fork of 512 rows (48 / 12.6) are the GPU's.
 constexpr int kMaxCluster = 8;
 static int fork_cluster(int rows, int M, int nchunk) {
   constexpr int kTeams = kPgNT / kRowTeam;
